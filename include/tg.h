@@ -534,6 +534,146 @@ int tg_alloc_admit(void *state, int n_lists, const int32_t *pages_per_list, int3
 int tg_alloc_release(void *state, int64_t n, const int32_t *ids);
 int tg_alloc_query(const void *state, int64_t *n_free, int64_t *n_live);
 
+/* ------------------------------------------------------------------ p1 ---
+ * tg_qk_norm_rope -- one layer's packed projections into queries and context rows:
+ *   RMS norm of every query and key head (optional), position rotation, and the
+ *   placement of the K and V rows, in one pass.  With one token per request it is
+ *   the step ahead of tg_decode_attn, with whole prompts or chunks the one ahead of
+ *   tg_prefill_attn and tg_compact_topk / tg_compact_chunk.
+ *   Request b owns the packed tokens [cu_q[b], cu_q[b+1]); its token cu_q[b] + i is
+ *   row start[b] + i of its context.  For a query or key head x of a token:
+ *     y = x / sqrt(mean(x^2) + eps) * weight          (weight NULL: y = x)
+ *     (z_a, z_b) = (y_a c - y_b s, y_b c + y_a s)     for the rot/2 pairs (a, b)
+ *   with (c, s) = cos_sin[position][i] of pair i; pair i is (i, i + rot/2), or
+ *   (2i, 2i+1) with TG_ROPE_PAIRS; values from rot on are only normalised.  V heads
+ *   are copied.  The table carries the angles, so any frequency scaling is the
+ *   caller's, and far positions lose nothing (make it in 64 bits).
+ *   float32 arithmetic, one rounding to bf16 at the end.
+ * Arguments (device): cu_q int32 [batch+1], ascending, cu_q[0] = 0; start int32 [batch];
+ *   qkv bf16, T rows of (H_q + 2H) heads of d (queries, keys, values), qkv_stride
+ *   elements apart (a multiple of 8, >= (H_q + 2H) * d); q_weight, k_weight
+ *   float32 [d], each may be NULL; positions int32 [T] (NULL: the context row);
+ *   cos_sin float32 [max_pos][rot/2][2]; q bf16 [T][H_q][d] and K, V bf16
+ *   [batch][H][Nmax][d] (outputs; q may not overlap qkv).  Every pointer 16-byte aligned
+ *   (cu_q, start, positions: 4).
+ *   Host sizes: d in {128, 256}, rot % 16 == 0, 0 <= rot <= d, eps >= 0.
+ *   Rows from cu_q[batch] on are left as they are.  A token whose position is outside
+ *   [0, max_pos) (with rot > 0) or whose context row is outside [0, Nmax) sets
+ *   TG_STATUS_BAD_INPUT and writes nothing.  T = 0 launches nothing. */
+#define TG_ROPE_PAIRS 0x1u
+int tg_qk_norm_rope(tg_stream_t stream, int batch, int T, int H_q, int H, int d, int Nmax, int rot, int max_pos,
+                    uint32_t flags, const int32_t *cu_q, const int32_t *start, const uint16_t *qkv,
+                    int64_t qkv_stride, const float *q_weight, const float *k_weight, float eps,
+                    const int32_t *positions, const float *cos_sin, uint16_t *q, uint16_t *K, uint16_t *V,
+                    int32_t *dev_status);
+
+/* ------------------------------------------------------------- p2 + p3 ---
+ * Tile plan: the work of tg_prefill_attn or tg_prefix_attn, laid out ahead of the
+ * calls like the decode plan.  An item is up to 256 (d = 128) or 128 (d = 256) query
+ * rows of one KV head -- consecutive tokens (requests) x the head's g query heads --
+ * over a range of 128-key blocks.  Items are given to the N_CTA thread blocks longest
+ * first, each to the least loaded; runs of keys are cut only where that shortens the
+ * longest block's work, and the cut pieces leave float32 partials that a second,
+ * dependent kernel merges.  One byte buffer:
+ *   tg_tile_header | tg_tile_item lead[N_CTA] | tg_tile_item items[] | tg_tile_merge[]
+ * (sections 16-byte aligned; offsets in bytes).  lead[c] is block c's first item, with
+ * reserved[0] = its item count and reserved[1] = the index of that item in items[]. */
+#define TG_TILE_MAGIC 0x31544754u /* "TGT1" */
+#define TG_TILE_VERSION 1
+
+typedef struct tg_tile_header {
+  uint32_t magic;
+  int32_t version;
+  int32_t kind;   /* 0: tg_plan_prefill, 1: tg_plan_prefix */
+  int32_t batch;  /* requests */
+  int32_t groups; /* prefix: groups of requests; prefill: batch */
+  int32_t rows;   /* query rows: tokens (prefill) or requests (prefix) */
+  int32_t H, H_q, H_p, P, d; /* H_p, P: prefix only */
+  int32_t window;            /* prefill only */
+  int32_t max_kv;            /* longest context (prefill) or retained run (prefix) */
+  int32_t N_CTA, n_items, n_merge, n_slots;
+  int32_t reserved;
+  int64_t plan_bytes, workspace_bytes;
+  int64_t lead, items, merges;
+} tg_tile_header;
+
+typedef struct tg_tile_item {
+  int32_t row0, nrow; /* query rows: tokens or requests [row0, row0 + nrow) */
+  int32_t h;          /* KV head */
+  int32_t src;        /* prefill: request; prefix: page list group * (H / H_p) + page group */
+  int32_t hpos;       /* prefix: the head's place in its page group */
+  int32_t pos0;       /* prefill: context position of row0 (may be negative: it sees no key) */
+  int32_t kv_len;     /* keys [0, kv_len) exist */
+  int32_t blk0, blk1; /* key blocks [blk0, blk1) of 128 */
+  int32_t slot;       /* partial slot, -1: the item finishes its rows alone */
+  int32_t reserved[2];
+} tg_tile_item;
+
+typedef struct tg_tile_merge {
+  int32_t row0, nrow, h, slot0, nparts;
+  int32_t reserved[3];
+} tg_tile_merge;
+
+/* tg_plan_prefill -- plan of tg_prefill_attn for one packed pass (all layers share it).
+ * Inputs (host): q_len, kv_len int32 [batch], >= 0: request b brings q_len[b] query
+ *   tokens, the last q_len[b] of its kv_len[b] context tokens (kv_len counts them).
+ *   q_len > kv_len is allowed: the rows before the context see no key.
+ *   window 0: token at position p sees keys [0, p]; > 0: keys (p - window, p].
+ *   d in {128, 256}; g = H_q / H in [1, 8]; N_CTA >= 1 (one per SM).
+ * Outputs (host): plan (NULL to query the size); *plan_bytes; *workspace_bytes = the
+ *   device scratch a call needs (0 if no run is cut).  TG_ERR_CAPACITY if plan_cap is
+ *   smaller. */
+int tg_plan_prefill(int batch, int H, int H_q, int d, int N_CTA, const int32_t *q_len, const int32_t *kv_len,
+                    int window, void *plan, int64_t plan_cap, int64_t *plan_bytes, int64_t *workspace_bytes);
+
+/* tg_prefill_attn -- causal attention of a packed pass over its contexts, one layer.
+ *   For query head j = h*g + i of a token at position p of request b:
+ *     out = sum_t softmax_t(scale * q . k_t) v_t over the keys t of (b, h) that p sees,
+ *     lse = ln sum_t exp(scale * q . k_t)   (out = 0, lse = -inf where it sees none).
+ *   bf16 inputs; float32 products, sums and softmax; the weights are rounded to bf16 for
+ *   the second product (their sum is of the unrounded ones); bf16 output.
+ * Arguments (device): plan_host / plan_dev the same tg_plan_prefill bytes;
+ *   q bf16 [rows][H_q][d], rows = the sum of q_len, requests one after the other;
+ *   K, V bf16 [batch][H][Nmax][d], Nmax >= every kv_len, rows [0, kv_len) of each request
+ *   finite (rows behind them may hold anything); scale > 0; workspace 256-byte
+ *   aligned, no initial contents (may be NULL if the plan needs none), one per stream;
+ *   out bf16 [rows][H_q][d]; lse float32 [rows][H_q] (may be NULL).  q, K, V, out
+ *   16-byte aligned.  batch * H and Nmax fit TMA coordinates (int32). */
+int tg_prefill_attn(tg_stream_t stream, const void *plan_host, const void *plan_dev, const uint16_t *q,
+                    const uint16_t *K, const uint16_t *V, int Nmax, float scale, void *workspace,
+                    int64_t workspace_bytes, uint16_t *out, float *lse, int32_t *dev_status);
+
+/* tg_plan_prefix -- plan of tg_prefix_attn for one layer.
+ * Inputs (host): groups of requests that share a prefix: group r is the requests
+ *   [req_off[r], req_off[r+1]) (int32 [groups+1], req_off[0] = 0, ascending), batch =
+ *   req_off[groups]; head_order int32 [H] and ntok int32 [groups][H], >= 0, of the layer
+ *   as tg_build_pages gives them for `groups` requests (ntok 0: the group shares nothing).
+ *   Sizes as tg_plan_prefill; H % H_p == 0, P % 16 == 0. */
+int tg_plan_prefix(int groups, int H, int H_q, int H_p, int P, int d, int N_CTA, const int32_t *req_off,
+                   const int32_t *head_order, const int32_t *ntok, void *plan, int64_t plan_cap,
+                   int64_t *plan_bytes, int64_t *workspace_bytes);
+
+/* tg_prefix_attn -- decode attention of a batch over retained tokens its requests share,
+ *   read once for all of them, merged with what each request attended to on its own.
+ *   For request b of group r and query head j of KV head h, over the ntok[r][h] tokens t
+ *   of the group's page list:  w_t = exp(scale * q . k_t), s = sum_t w_t,
+ *     out = (sum_t w_t v_t + e^own_lse own_out) / (s + e^own_lse),
+ *     lse = ln(s + e^own_lse)
+ *   (without own_out / own_lse: those terms are 0; out = 0, lse = -inf where both are
+ *   empty).  Arithmetic as tg_prefill_attn.
+ * Arguments (device): q bf16 [batch][H_q][d]; pool, pt_off (int64 [groups*G + 1]) and
+ *   pt_ids as tg_decode_attn, list r*G + g being page group g of group r, with a
+ *   list's pages covering its ntok (a shorter list counts as pages outside the pool);
+ *   own_out bf16 [batch][H_q][d] and own_lse float32 [batch][H_q], both or neither NULL:
+ *   tg_decode_attn's out and lse over the requests' own tokens; out and lse (may be
+ *   NULL) the results, which may be the same buffers as own_out and own_lse; workspace
+ *   as tg_prefill_attn.  A page id outside [0, pool_pages) sets TG_STATUS_BAD_PAGE and
+ *   reads as zeros.  q, pool, own_out, out 16-byte aligned. */
+int tg_prefix_attn(tg_stream_t stream, const void *plan_host, const void *plan_dev, const uint16_t *q,
+                   const uint16_t *pool, int64_t pool_pages, const int64_t *pt_off, const int32_t *pt_ids,
+                   float scale, const uint16_t *own_out, const float *own_lse, void *workspace,
+                   int64_t workspace_bytes, uint16_t *out, float *lse, int32_t *dev_status);
+
 /* tg_check_status -- synchronously read a device status word (waits for the
  *   device).  Returns TG_OK when it is 0, TG_ERR_TIMEOUT when TG_STATUS_TIMEOUT
  *   is set, TG_ERR_DEVICE for any other bit; *host_status (may be NULL) gets

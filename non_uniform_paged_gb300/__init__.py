@@ -23,6 +23,8 @@ __all__ = ["TGError", "load", "tg_build_pages", "tg_split_map", "tg_query_ncta",
            "tg_page_score_workspace", "tg_page_score_topk_rows", "tg_rerank_rows", "tg_plan_set_flags",
            "PLAN_WAIT_TABLES", "SCORE_LET_NEXT_START", "PageAllocator",
            "tg_sparse_layer", "tg_compact_chunk", "tg_compact_chunk_workspace", "tg_tier_promote", "tg_tier_promote_background", "tg_alloc_state_bytes", "tg_alloc_init", "tg_alloc_admit", "tg_alloc_release", "tg_alloc_query",
+           "tg_qk_norm_rope", "tg_plan_prefill", "tg_prefill_attn", "tg_plan_prefix", "tg_prefix_attn", "tile_header",
+           "tile_items", "TilePlan", "TILE_ITEM_DTYPE", "ROPE_PAIRS",
            "tg_check_status", "tg_version", "plan_header", "plan_items", "plan_lead", "WORK_ITEM_DTYPE",
            "STATUS_NONFINITE", "STATUS_BAD_PAGE", "STATUS_TIMEOUT", "STATUS_BAD_INPUT", "ERR_INVALID_ARG",
            "ERR_SHAPE", "ERR_NONFINITE", "ERR_CAPACITY", "ERR_CUDA", "ERR_TIMEOUT", "ERR_DEVICE"]
@@ -32,7 +34,9 @@ STATUS_NONFINITE, STATUS_BAD_PAGE, STATUS_TIMEOUT, STATUS_BAD_INPUT = 0x1, 0x2, 
 ERR_INVALID_ARG, ERR_SHAPE, ERR_NONFINITE, ERR_CAPACITY, ERR_CUDA, ERR_TIMEOUT, ERR_DEVICE = -1, -2, -3, -4, -5, -6, -7
 PLAN_WAIT_TABLES = 0x1       # tg.h TG_PLAN_WAIT_TABLES
 SCORE_LET_NEXT_START = 0x1   # tg.h TG_SCORE_LET_NEXT_START
+ROPE_PAIRS = 0x1             # tg.h TG_ROPE_PAIRS
 PLAN_MAGIC = 0x31504754
+TILE_MAGIC = 0x31544754
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -72,6 +76,12 @@ _SIGS = {
     "tg_page_score_topk_rows": (_I, [_P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _L,
                                      ctypes.c_uint32, _P]),
     "tg_rerank_rows": (_I, [_I, _I, _I, _P, _I, _I, _I, _I, _P, _P]),
+    "tg_qk_norm_rope": (_I, [_P, _I, _I, _I, _I, _I, _I, _I, _I, ctypes.c_uint32, _P, _P, _P, _L, _P, _P, _F, _P, _P, _P,
+                             _P, _P, _P]),
+    "tg_plan_prefill": (_I, [_I, _I, _I, _I, _I, _P, _P, _I, _P, _L, _P, _P]),
+    "tg_prefill_attn": (_I, [_P, _P, _P, _P, _P, _P, _I, _F, _P, _L, _P, _P, _P]),
+    "tg_plan_prefix": (_I, [_I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _L, _P, _P]),
+    "tg_prefix_attn": (_I, [_P, _P, _P, _P, _P, _L, _P, _P, _F, _P, _P, _P, _L, _P, _P, _P]),
     "tg_check_status": (_I, [_P, _P]),
 }
 
@@ -492,6 +502,194 @@ class PageAllocator:
 
     def query(self):
         return tg_alloc_query(self._state)
+
+
+# ------------------------------------------------------------------ prompt side and shared prefixes
+# These calls sit on the latency path of a decode step, so their checks are lean: one pass per tensor.
+
+def _arg(t, dtype, shape, name, dev):
+    """Pointer of a contiguous tensor of that type and shape on device `dev`."""
+    try:
+        at = t.get_device()
+    except AttributeError:
+        raise TypeError(f"{name} must be a CUDA torch.Tensor") from None
+    if at != dev:
+        if at < 0:
+            raise TypeError(f"{name} must be a CUDA torch.Tensor")
+        raise ValueError(f"{name} is on cuda:{at}, the current device is cuda:{dev}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _opt(t, dtype, shape, name, dev):
+    return None if t is None else _arg(t, dtype, shape, name, dev)
+
+
+def _where(stream):
+    """(torch, current device, stream handle); the library launches on the current device."""
+    import torch
+    dev = torch.cuda.current_device()
+    if stream is None:
+        return torch, dev, torch._C._cuda_getCurrentRawStream(dev)
+    return torch, dev, stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def tg_qk_norm_rope(qkv, cu_q, start, cos_sin, q, K, V, q_weight=None, k_weight=None, eps=1e-6, pairs=False,
+                    positions=None, dev_status=None, stream=None):
+    """RMS norm and rotation of queries and keys, and placement of K and V rows (tg.h:
+    tg_qk_norm_rope).  qkv [T][H_q + 2H][d] (rows may be strided), q [T][H_q][d],
+    K, V [batch][H][Nmax][d], cos_sin [max_pos][rot/2][2] (None: no rotation)."""
+    torch, dev, stream = _where(stream)
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    try:
+        T, H_q, d = q.shape
+        batch, H, Nmax, _ = K.shape
+        max_pos, half, two = (0, 0, 2) if cos_sin is None else cos_sin.shape
+    except (AttributeError, ValueError):
+        raise ValueError("q must be [T][H_q][d], K [batch][H][Nmax][d] and cos_sin [max_pos][rot/2][2] tensors") from None
+    heads = H_q + 2 * H
+    if qkv.shape != (T, heads, d) or two != 2:
+        raise ValueError(f"qkv has shape {tuple(qkv.shape)}, not {(T, heads, d)}" if two == 2 else "cos_sin must end in 2")
+    if qkv.dtype is not bf16 or qkv.get_device() != dev:
+        raise TypeError(f"qkv must be a bfloat16 tensor on cuda:{dev}")
+    stride, inner, last = qkv.stride()
+    if T and (inner != d or last != 1):
+        raise ValueError("qkv must have contiguous token rows")
+    _check(load().tg_qk_norm_rope(
+        stream, batch, T, H_q, H, d, Nmax, 2 * half, max_pos, ROPE_PAIRS if pairs else 0,
+        _arg(cu_q, i32, (batch + 1,), "cu_q", dev), _arg(start, i32, (batch,), "start", dev), qkv.data_ptr(),
+        stride if T > 1 else heads * d, _opt(q_weight, f32, (d,), "q_weight", dev),
+        _opt(k_weight, f32, (d,), "k_weight", dev), eps, _opt(positions, i32, (T,), "positions", dev),
+        _opt(cos_sin, f32, None, "cos_sin", dev), _arg(q, bf16, None, "q", dev),
+        _arg(K, bf16, (batch, H, Nmax, d), "K", dev), _arg(V, bf16, K.shape, "V", dev),
+        _opt(dev_status, i32, None, "dev_status", dev)))
+
+
+def _tile_plan(call):
+    """The two calls of a plan builder: its size, then its bytes -> (plan, workspace bytes)."""
+    nbytes, wbytes = ctypes.c_int64(0), ctypes.c_int64(0)
+    _check(call(None, 0, ctypes.addressof(nbytes), ctypes.addressof(wbytes)))
+    plan = np.zeros(nbytes.value, np.uint8)
+    _check(call(plan.ctypes.data, plan.size, ctypes.addressof(nbytes), ctypes.addressof(wbytes)))
+    return plan, wbytes.value
+
+
+def tg_plan_prefill(q_len, kv_len, H: int, H_q: int, d: int, N_CTA: int, window: int = 0):
+    """Plan of tg_prefill_attn (tg.h: tg_plan_prefill) -> (plan uint8 array, workspace bytes)."""
+    lib = load()
+    q_len, pq = _np(np.asarray(q_len).reshape(-1), np.int32)
+    kv_len, pk = _np(np.asarray(kv_len).reshape(-1), np.int32)
+    if q_len.size != kv_len.size:
+        raise ValueError(f"q_len has {q_len.size} requests, kv_len {kv_len.size}")
+    return _tile_plan(lambda *out: lib.tg_plan_prefill(q_len.size, H, H_q, d, N_CTA, pq, pk, window, *out))
+
+
+def tg_plan_prefix(req_off, head_order, ntok, H_q: int, H_p: int, P: int, d: int, N_CTA: int):
+    """Plan of tg_prefix_attn (tg.h: tg_plan_prefix): ntok int32 [groups][H] -> (plan uint8 array,
+    workspace bytes)."""
+    lib = load()
+    ntok = np.asarray(ntok)
+    if ntok.ndim != 2:
+        raise ValueError("ntok must be [groups][H]")
+    groups, H = ntok.shape
+    ntok, pt = _np(ntok, np.int32)
+    req_off, pr = _np(np.asarray(req_off).reshape(-1), np.int32)
+    head_order, po = _np(np.asarray(head_order).reshape(-1), np.int32)
+    if req_off.size != groups + 1 or head_order.size != H:
+        raise ValueError(f"req_off has {req_off.size} entries for {groups} groups, head_order {head_order.size} for {H} heads")
+    return _tile_plan(lambda *out: lib.tg_plan_prefix(groups, H, H_q, H_p, P, d, N_CTA, pr, po, pt, *out))
+
+
+_TILE_HEADER_DTYPE = np.dtype([("magic", "<u4")] + [(n, "<i4") for n in (
+    "version", "kind", "batch", "groups", "rows", "H", "H_q", "H_p", "P", "d", "window", "max_kv", "N_CTA", "n_items",
+    "n_merge", "n_slots", "reserved")] + [(n, "<i8") for n in ("plan_bytes", "workspace_bytes", "lead", "items", "merges")])
+TILE_ITEM_DTYPE = np.dtype([(n, "<i4") for n in ("row0", "nrow", "h", "src", "hpos", "pos0", "kv_len", "blk0", "blk1",
+                                                 "slot")] + [("reserved", "<i4", (2,))])
+
+
+def tile_header(plan: np.ndarray) -> dict:
+    """Read a tile plan's documented header (tg.h: tg_tile_header)."""
+    if plan.size < _TILE_HEADER_DTYPE.itemsize:
+        raise ValueError("not a tile plan")
+    h = np.frombuffer(plan[:_TILE_HEADER_DTYPE.itemsize].tobytes(), _TILE_HEADER_DTYPE)[0]
+    if int(h["magic"]) != TILE_MAGIC:
+        raise ValueError("not a tile plan")
+    return {k: int(h[k]) for k in _TILE_HEADER_DTYPE.names}
+
+
+def tile_items(plan: np.ndarray):
+    """(lead TILE_ITEM_DTYPE [N_CTA], items TILE_ITEM_DTYPE [n_items]) of a tile plan."""
+    hd = tile_header(plan)
+    n = TILE_ITEM_DTYPE.itemsize
+    lead = np.frombuffer(plan[hd["lead"]:hd["lead"] + hd["N_CTA"] * n].tobytes(), TILE_ITEM_DTYPE)
+    return lead, np.frombuffer(plan[hd["items"]:hd["items"] + hd["n_items"] * n].tobytes(), TILE_ITEM_DTYPE)
+
+
+class TilePlan:
+    """A tile plan's host and device bytes with what the calls check of it, read once."""
+
+    def __init__(self, plan: np.ndarray, plan_dev):
+        if not (isinstance(plan, np.ndarray) and plan.dtype == np.uint8 and plan.flags.c_contiguous):
+            raise TypeError("plan must be the contiguous uint8 array a tile plan call returned")
+        hd = tile_header(plan)
+        if hd["plan_bytes"] != plan.size:
+            raise ValueError(f"plan has {plan.size} bytes, its header says {hd['plan_bytes']}")
+        import torch
+        self._host, self.plan_dev, self._at = plan, plan_dev, plan_dev.get_device()
+        self.host_ptr, self.dev_ptr = plan.ctypes.data, _arg(plan_dev, torch.uint8, (plan.size,), "plan_dev", self._at)
+        if self._at < 0:
+            raise TypeError("plan_dev must be a CUDA torch.Tensor")
+        self.header = hd
+        self.q_shape = (hd["rows"], hd["H_q"], hd["d"])
+        self.kv_lead = (hd["batch"], hd["H"])
+        self.lists = hd["groups"] * (hd["H"] // max(1, hd["H_p"])) + 1
+        self.page_values = hd["H_p"] * 2 * hd["P"] * hd["d"]
+
+    def pointers(self, dev):
+        if self._at != dev:
+            raise ValueError(f"the plan is on cuda:{self._at}, the current device is cuda:{dev}")
+        return self.host_ptr, self.dev_ptr
+
+
+def tg_prefill_attn(plan: TilePlan, q, K, V, scale: float, out, lse=None, workspace=None, dev_status=None, stream=None):
+    """Causal attention of a packed prefill pass (tg.h: tg_prefill_attn); asynchronous.
+    q, out [rows][H_q][d], K, V [batch][H][Nmax][d], lse [rows][H_q]."""
+    torch, dev, stream = _where(stream)
+    bf16 = torch.bfloat16
+    ph, pd = plan.pointers(dev)
+    shape = plan.q_shape
+    kv = K.shape
+    if len(kv) != 4 or kv[:2] != plan.kv_lead or kv[3] != shape[2]:
+        raise ValueError(f"K has shape {tuple(kv)}, not [batch][H][Nmax][d] = {plan.kv_lead} x [Nmax] x {shape[2]}")
+    _check(load().tg_prefill_attn(
+        stream, ph, pd, _arg(q, bf16, shape, "q", dev), _arg(K, bf16, None, "K", dev), _arg(V, bf16, kv, "V", dev), kv[2],
+        scale, _opt(workspace, torch.uint8, None, "workspace", dev), 0 if workspace is None else workspace.numel(),
+        _arg(out, bf16, shape, "out", dev), _opt(lse, torch.float32, shape[:2], "lse", dev),
+        _opt(dev_status, torch.int32, None, "dev_status", dev)))
+
+
+def tg_prefix_attn(plan: TilePlan, q, pool, pool_pages: int, pt_off, pt_ids, scale: float, out, lse=None, own_out=None,
+                   own_lse=None, workspace=None, dev_status=None, stream=None):
+    """Decode attention over a shared prefix, merged with the requests' own results (tg.h:
+    tg_prefix_attn); asynchronous.  q, out, own_out [batch][H_q][d], lse, own_lse [batch][H_q]."""
+    torch, dev, stream = _where(stream)
+    bf16, f32 = torch.bfloat16, torch.float32
+    ph, pd = plan.pointers(dev)
+    shape = plan.q_shape
+    if pool.numel() < pool_pages * plan.page_values:
+        raise ValueError(f"pool holds {pool.numel()} values, fewer than {pool_pages} pages")
+    _check(load().tg_prefix_attn(
+        stream, ph, pd, _arg(q, bf16, shape, "q", dev), _arg(pool, bf16, None, "pool", dev), pool_pages,
+        _arg(pt_off, torch.int64, (plan.lists,), "pt_off", dev), _arg(pt_ids, torch.int32, None, "pt_ids", dev), scale,
+        _opt(own_out, bf16, shape, "own_out", dev), _opt(own_lse, f32, shape[:2], "own_lse", dev),
+        _opt(workspace, torch.uint8, None, "workspace", dev), 0 if workspace is None else workspace.numel(),
+        _arg(out, bf16, shape, "out", dev), _opt(lse, f32, shape[:2], "lse", dev),
+        _opt(dev_status, torch.int32, None, "dev_status", dev)))
 
 
 def tg_check_status(dev_status) -> int:

@@ -24,8 +24,8 @@ import torch
 from . import (tg_build_pages, tg_split_map, tg_query_ncta, tg_plan_decode, tg_decode_attn,
                tg_compact_topk, tg_compact_topk_workspace, tg_build_minmax, tg_page_score_topk, tg_page_score_workspace,
                tg_page_score_topk_rows, tg_rerank_rows, tg_plan_set_flags, PLAN_WAIT_TABLES,
-               SCORE_LET_NEXT_START, tg_tier_promote, tg_compact_chunk, tg_compact_chunk_workspace,
-               tg_sparse_layer)
+               SCORE_LET_NEXT_START, TilePlan, tg_plan_prefill, tg_prefill_attn, tg_plan_prefix, tg_prefix_attn, tg_tier_promote, tg_compact_chunk, tg_compact_chunk_workspace,
+               tg_sparse_layer, tg_qk_norm_rope)
 
 BYTES_BF16 = 2
 
@@ -395,6 +395,81 @@ class TieredSparseDecoder:
 
     def dense_kv_bytes(self) -> int:
         return self.batch * self.H * self.n_pages * self.page_bytes
+
+
+def _sm_count(dev) -> int:
+    return torch.cuda.get_device_properties(dev).multi_processor_count
+
+
+class PrefillPass:
+    """One packed prefill pass over a batch of contexts: request b brings q_len[b] tokens, the last
+    of its kv_len[b] context rows (whole prompts, chunks, follow-up turns or single tokens).
+    Owns the plan, shared by every layer of the pass, its workspace, and the device arrays that
+    place the tokens (cu_q, start) for tg_qk_norm_rope.  One pass runs on one stream at a time."""
+
+    def __init__(self, H, H_q, d, q_len, kv_len, window=0, n_cta=None, device="cuda"):
+        self.device = torch.device(device)
+        self.q_len = np.asarray(q_len, np.int32).reshape(-1)
+        self.kv_len = np.asarray(kv_len, np.int32).reshape(-1)
+        self.n_cta = int(n_cta) if n_cta else _sm_count(self.device)
+        plan, self.workspace_bytes = tg_plan_prefill(self.q_len, self.kv_len, H, H_q, d, self.n_cta, window)
+        self.plan = TilePlan(plan, torch.from_numpy(plan).to(self.device))
+        cu = np.concatenate([[0], np.cumsum(self.q_len, dtype=np.int64)])
+        self.rows = int(cu[-1])
+        self.cu_q = torch.from_numpy(cu.astype(np.int32)).to(self.device)
+        self.start = torch.from_numpy(self.kv_len - self.q_len).to(self.device)
+        self.workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=self.device) \
+            if self.workspace_bytes else None
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self.scale = 1.0 / math.sqrt(d)
+
+    def place(self, qkv, cos_sin, q, K, V, q_weight=None, k_weight=None, eps=1e-6, pairs=False, positions=None,
+              stream=None):
+        """Norm, rotate and place the pass's projections (tg_qk_norm_rope)."""
+        tg_qk_norm_rope(qkv, self.cu_q, self.start, cos_sin, q, K, V, q_weight=q_weight, k_weight=k_weight, eps=eps,
+                        pairs=pairs, positions=positions, dev_status=self.status, stream=stream)
+
+    def attend(self, q, K, V, out, lse=None, scale=None, stream=None):
+        """Causal attention of the pass's queries over their contexts, one layer (tg_prefill_attn)."""
+        tg_prefill_attn(self.plan, q, K, V, self.scale if scale is None else scale, out, lse=lse,
+                        workspace=self.workspace, dev_status=self.status, stream=stream)
+
+
+class SharedPrefix:
+    """Retained tokens shared by groups of requests of a decode batch: group r is the requests
+    [req_off[r], req_off[r+1]) and its tokens are the page lists of request r of a RaggedCache
+    (or tg_build_pages) built for the prefixes.  order int32 [H] or [L][H], ntok int32
+    [groups][H] or [L][groups][H].  One workspace serves all layers, on one stream at a time."""
+
+    def __init__(self, H_q, H_p, P, d, req_off, order, ntok, n_cta=None, device="cuda"):
+        self.device = torch.device(device)
+        ntok = np.asarray(ntok, np.int32)
+        ntok = ntok[None] if ntok.ndim == 2 else ntok
+        order = np.asarray(order, np.int32)
+        order = np.broadcast_to(order, (ntok.shape[0], ntok.shape[2])) if order.ndim == 1 else order
+        self.n_cta = int(n_cta) if n_cta else _sm_count(self.device)
+        self.plans, most = [], 0
+        for l in range(ntok.shape[0]):
+            plan, ws = tg_plan_prefix(req_off, order[l], ntok[l], H_q, H_p, P, d, self.n_cta)
+            self.plans.append(TilePlan(plan, torch.from_numpy(plan).to(self.device)))
+            most = max(most, ws)
+        self.workspace = torch.empty(most, dtype=torch.uint8, device=self.device) if most else None
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self.scale = 1.0 / math.sqrt(d)
+
+    @classmethod
+    def of_cache(cls, cache, req_off, n_cta=None):
+        """The prefixes held by a RaggedCache, its request r for group r."""
+        return cls(cache.H_q, cache.H_p, cache.P, cache.d, req_off, cache.pages["order"], cache.pages["ntok"],
+                   n_cta=n_cta, device=cache.device)
+
+    def attend(self, layer, q, pool, pool_pages, pt_off, pt_ids, out, lse=None, own_out=None, own_lse=None, scale=None,
+               stream=None):
+        """One layer's attention over the shared tokens, merged with the requests' own (tg_prefix_attn);
+        pt_off: this layer's lists (RaggedCache.list_offsets)."""
+        tg_prefix_attn(self.plans[layer], q, pool, pool_pages, pt_off, pt_ids, self.scale if scale is None else scale,
+                       out, lse=lse, own_out=own_out, own_lse=own_lse, workspace=self.workspace, dev_status=self.status,
+                       stream=stream)
 
 
 class RerankSchedule:
