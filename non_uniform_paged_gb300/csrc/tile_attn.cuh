@@ -17,7 +17,8 @@
 // two tiles at d = 128 and one at d = 256: S (128 x 128 float32) twice and O (256 columns
 // in all) fill the 512 columns of tensor memory.
 //   warps 0-3 (4-7): softmax and output of tile 0 (1), one row per thread;
-//   the next warp issues the MMAs; the last streams Q, K and V by TMA.
+//   then a warp whose elected lane issues the MMAs, one that streams Q, K and V by TMA, and one
+//   that clears the V rows behind the end of a context.
 // K and V go through a ring of five 32 KB stages (128 keys x 128 columns each; d = 256
 // takes two per block).  P overwrites S in tensor memory and is the A operand of P V.
 // At d = 128 the two tiles alternate: while one is in softmax the tensor cores run
@@ -62,7 +63,8 @@ struct TileBars {
   // pv_done: each P V of a tile (d = 128) or of the tile (d = 256, [0]); there [1] is the last one
   // of an item, because an S of d = 256 is issued ahead of the P V before it, so that [0] may lag
   // two phases behind when an item ends
-  uint64_t q_full, q_empty, full[kStages], empty[kStages], s_full[2], p_ready[2], pv_done[2], drain;
+  // p_half: the first 64 keys' weights are in tensor memory; p_ready: all 128
+  uint64_t q_full, q_empty, full[kStages], empty[kStages], s_full[2], p_half[2], p_ready[2], pv_done[2], to_clear, cleared, drain;
   uint32_t tmem;
   int32_t abort;
 };
@@ -86,6 +88,12 @@ __device__ __forceinline__ bool tile_wait(uint64_t *bar, uint32_t parity, TileBa
   bool ok = mbar_try_wait(bar, parity);
   if (!ok) ok = tile_wait_slow(bar, parity, &b->abort, status);
   return __all_sync(0xffffffffu, ok);
+}
+
+// the same for a role that one lane plays
+__device__ __forceinline__ bool lane_wait(uint64_t *bar, uint32_t parity, TileBars *b, int32_t *status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return tile_wait_slow(bar, parity, &b->abort, status);
 }
 
 // The items of a thread block; the next one's line is fetched ahead into L1.
@@ -114,11 +122,11 @@ struct ItemList {
 
 // ------------------------------------------------------------------ softmax and output warps
 template <int D, bool PAGED>
-__device__ __forceinline__ void softmax_role(const TileArgs &a, TileBars *bar, uint32_t tmem, int tile) {
+__device__ __forceinline__ void softmax_role(const TileArgs &a, TileBars *bar, int tile) {
   const int r = threadIdx.x & 127;             // row of the tile = lane of tensor memory
   const int tok = r / a.g, head = r - tok * a.g;
   const uint32_t lanes = (uint32_t)(r & ~31) << 16;
-  const uint32_t o_base = tmem + 256 + (D == 128 ? tile * 128 : 0) + lanes;
+  const uint32_t o_base = 256 + (D == 128 ? tile * 128 : 0) + lanes;
   const float sl2 = a.scale_log2;
   uint32_t s_count = 0, pv_count = 0, item_count = 0;
   ItemList list;
@@ -145,7 +153,7 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, TileBars *bar, u
       const int buf = D == 128 ? tile : (int)(s_count & 1);
       const uint32_t phase = (D == 128 ? s_count : s_count >> 1) & 1;
       ++s_count;
-      const uint32_t s_addr = tmem + buf * 128 + lanes;
+      const uint32_t s_addr = buf * 128 + lanes;
       if (!tile_wait(&bar->s_full[buf], phase, bar, a.status)) return;
       tc_fence_after();
       float s[128];
@@ -201,6 +209,12 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, TileBars *bar, u
           p[k] = pack_bf16x2(x.x, x.y);
         }
         tmem_st16(s_addr + c * 16, p);
+        if (c == 1) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if ((threadIdx.x & 31) == 0) mbar_arrive(&bar->p_half[buf]);
+        }
       }
       tmem_wait_st();
       tc_fence_before();
@@ -291,24 +305,34 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, TileBars *bar, u
   }
 }
 
-// ------------------------------------------------------------------ MMA warp
+// ------------------------------------------------------------------ MMA lane
 struct RingPos {
   uint32_t stage = 0, phase = 0;
   __device__ __forceinline__ void next() {
     if (++stage == kStages) stage = 0, phase ^= 1;
   }
+  __device__ __forceinline__ void skip(uint32_t n) {
+    const uint32_t s = stage + n;
+    phase ^= (s / kStages) & 1;
+    stage = s % kStages;
+  }
 };
 
-// zero the rows [from, 128) of a V stage: keys past the end contribute 0 whatever memory holds
-__device__ __forceinline__ void zero_tail(uint32_t stage, int from) {
-  const int lane = threadIdx.x & 31;
-  for (int i = from * 8 + lane; i < 128 * 8; i += 32) {
-    const uint32_t at = stage + (uint32_t)i * 16;
-    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
-    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + kHalfBytes), "r"(0) : "memory");
-  }
-  fence_proxy_async_smem();
-  __syncwarp();
+// the key blocks [b, e) that an item's tiles need together (empty: none)
+template <int D, bool PAGED>
+__device__ __forceinline__ tgi::TileRange item_range(const tg_tile_item &it, const TileArgs &a, tgi::TileRange *r0,
+                                                     tgi::TileRange *r1) {
+  *r0 = tgi::tile_range(it, 0, a.tq, a.window, !PAGED);
+  *r1 = {0, 0};
+  if (D == 128) *r1 = tgi::tile_range(it, 1, a.tq, a.window, !PAGED);
+  if (r1->b >= r1->e) return *r0;
+  if (r0->b >= r0->e) return *r1;
+  return {min(r0->b, r1->b), max(r0->e, r1->e)};
+}
+// rows of the last block behind the context's end have to be cleared (pages hold finite rows)
+template <bool PAGED>
+__device__ __forceinline__ bool has_tail(const tg_tile_item &it, int j1) {
+  return !PAGED && j1 * 128 > it.kv_len;
 }
 
 // S = Q K^T over one 128-column piece
@@ -320,45 +344,42 @@ __device__ __forceinline__ void issue_qk(uint32_t s, uint32_t q, uint32_t k, boo
     mma_ss(s, smem_desc(q + at, 16, 1024), smem_desc(k + at, 16, 1024), idesc, accumulate || i > 0);
   }
 }
-// O += P V over one stage of 128 keys x 128 columns
-__device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p, uint32_t v, bool accumulate) {
+// O += P V over 64 of a stage's 128 keys x 128 columns
+__device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p, uint32_t v, int half, bool accumulate) {
   constexpr uint32_t idesc = mma_desc(128, 128, true);
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    mma_ts(o, p + i * 8, smem_desc(v + i * 2048, kHalfBytes, 1024), idesc, accumulate || i > 0);
+  for (int i = 0; i < 4; ++i) {
+    const int k = half * 4 + i;
+    mma_ts(o, p + k * 8, smem_desc(v + k * 2048, kHalfBytes, 1024), idesc, accumulate || i > 0);
+  }
 }
 
 template <int D, bool PAGED>
-__device__ __forceinline__ bool mma_items(const TileArgs &a, TileBars *bar, uint32_t tmem, uint32_t q_at,
-                                          uint32_t ring_at) {
-  const bool lead = (threadIdx.x & 31) == 0;
+__device__ __forceinline__ bool mma_items(const TileArgs &a, TileBars *bar, uint32_t q_at, uint32_t ring_at) {
   RingPos rp;
-  uint32_t q_phase = 0, p_count[2] = {0, 0};
+  uint32_t q_phase = 0, p_count[2] = {0, 0}, c_phase = 0;
   ItemList list;
   list.start(a);
   while (list.advance()) {
     const tg_tile_item &it = list.cur;
-    const tgi::TileRange r0 = tgi::tile_range(it, 0, a.tq, a.window, !PAGED);
-    tgi::TileRange r1 = {0, 0};
-    if (D == 128) r1 = tgi::tile_range(it, 1, a.tq, a.window, !PAGED);
-    const bool has0 = r0.b < r0.e, has1 = D == 128 && r1.b < r1.e;
-    if (!has0 && !has1) continue;
-    const int j0 = has0 ? (has1 ? min(r0.b, r1.b) : r0.b) : r1.b;
-    const int j1 = has0 ? (has1 ? max(r0.e, r1.e) : r0.e) : r1.e;
-    if (!tile_wait(&bar->q_full, q_phase, bar, a.status)) return false;
+    tgi::TileRange r0, r1;
+    const tgi::TileRange rg = item_range<D, PAGED>(it, a, &r0, &r1);
+    const int j0 = rg.b, j1 = rg.e;
+    if (j0 >= j1) continue;
+    const bool tail = has_tail<PAGED>(it, j1);
+    if (!lane_wait(&bar->q_full, q_phase, bar, a.status)) return false;
     q_phase ^= 1;
-    tc_fence_after();
     if (D == 128) {
       // K of the first block for both tiles, then per block and tile: P V, next Q K^T
-      if (!tile_wait(&bar->full[rp.stage], rp.phase, bar, a.status)) return false;
+      if (!lane_wait(&bar->full[rp.stage], rp.phase, bar, a.status)) return false;
       const uint32_t k = ring_at + rp.stage * kStageBytes;
-      if (lead) {
-        if (has0 && r0.b == j0) issue_qk(tmem, q_at, k, false), mma_commit(&bar->s_full[0]);
-        if (has1 && r1.b == j0) issue_qk(tmem + 128, q_at + kStageBytes, k, false), mma_commit(&bar->s_full[1]);
-        mma_commit(&bar->empty[rp.stage]);
-        if (j1 - j0 == 1) mma_commit(&bar->q_empty);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const tgi::TileRange r = i ? r1 : r0;
+        if (r.b == j0 && r.b < r.e) issue_qk(i * 128, q_at + i * kStageBytes, k, false), mma_commit(&bar->s_full[i]);
       }
-      __syncwarp();
+      mma_commit(&bar->empty[rp.stage]);
+      if (j1 - j0 == 1) mma_commit(&bar->q_empty);
       rp.next();
       for (int j = j0; j < j1; ++j) {
         const RingPos vp = rp;
@@ -367,37 +388,37 @@ __device__ __forceinline__ bool mma_items(const TileArgs &a, TileBars *bar, uint
         const bool more = j + 1 < j1;
         if (more) rp.next();
         const uint32_t v = ring_at + vp.stage * kStageBytes, kn = ring_at + kp.stage * kStageBytes;
-        if (!tile_wait(&bar->full[vp.stage], vp.phase, bar, a.status)) return false;
-        if ((j + 1) * 128 > it.kv_len) zero_tail(v, it.kv_len - j * 128);
+        if (!lane_wait(&bar->full[vp.stage], vp.phase, bar, a.status)) return false;
+        if (!more && tail) {
+          mbar_arrive(&bar->to_clear);
+          if (!lane_wait(&bar->cleared, c_phase, bar, a.status)) return false;
+          c_phase ^= 1;
+        }
         bool k_there = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const tgi::TileRange r = i ? r1 : r0;
           if (j >= r.b && j < r.e) {
-            if (!tile_wait(&bar->p_ready[i], p_count[i] & 1, bar, a.status)) return false;
+            const uint32_t o = 256 + i * 128, p = i * 128;
+            if (!lane_wait(&bar->p_half[i], p_count[i] & 1, bar, a.status)) return false;
+            tc_fence_after();
+            issue_pv(o, p, v, 0, j > r.b);
+            if (!lane_wait(&bar->p_ready[i], p_count[i] & 1, bar, a.status)) return false;
             ++p_count[i];
             tc_fence_after();
-            if (lead) {
-              issue_pv(tmem + 256 + i * 128, tmem + i * 128, v, j > r.b);
-              mma_commit(&bar->pv_done[i]);
-            }
+            issue_pv(o, p, v, 1, true);
+            mma_commit(&bar->pv_done[i]);
           }
           if (more && j + 1 >= r.b && j + 1 < r.e) {
-            if (!k_there && !tile_wait(&bar->full[kp.stage], kp.phase, bar, a.status)) return false;
+            if (!k_there && !lane_wait(&bar->full[kp.stage], kp.phase, bar, a.status)) return false;
             k_there = true;
-            if (lead) {
-              issue_qk(tmem + i * 128, q_at + i * kStageBytes, kn, false);
-              mma_commit(&bar->s_full[i]);
-            }
+            issue_qk(i * 128, q_at + i * kStageBytes, kn, false);
+            mma_commit(&bar->s_full[i]);
           }
-          __syncwarp();
         }
-        if (lead) {
-          mma_commit(&bar->empty[vp.stage]);
-          if (more) mma_commit(&bar->empty[kp.stage]);
-          if (j + 2 == j1) mma_commit(&bar->q_empty);
-        }
-        __syncwarp();
+        mma_commit(&bar->empty[vp.stage]);
+        if (more) mma_commit(&bar->empty[kp.stage]);
+        if (j + 2 == j1) mma_commit(&bar->q_empty);
       }
     } else {
       // ring order: K(j0), K(j0+1), V(j0), K(j0+2), V(j0+1), ...
@@ -407,38 +428,41 @@ __device__ __forceinline__ bool mma_items(const TileArgs &a, TileBars *bar, uint
           ++p_count[1];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            if (!tile_wait(&bar->full[rp.stage], rp.phase, bar, a.status)) return false;
-            if (lead) {
-              issue_qk(tmem + buf * 128, q_at + c * kStageBytes, ring_at + rp.stage * kStageBytes, c > 0);
-              mma_commit(&bar->empty[rp.stage]);
-              if (c == 1) {
-                mma_commit(&bar->s_full[buf]);
-                if (j + 2 == j1) mma_commit(&bar->q_empty);
-              }
-            }
-            __syncwarp();
+            if (!lane_wait(&bar->full[rp.stage], rp.phase, bar, a.status)) return false;
+            issue_qk(buf * 128, q_at + c * kStageBytes, ring_at + rp.stage * kStageBytes, c > 0);
+            mma_commit(&bar->empty[rp.stage]);
             rp.next();
           }
+          mma_commit(&bar->s_full[buf]);
+          if (j + 2 == j1) mma_commit(&bar->q_empty);
         }
         if (j >= j0) {
-          const uint32_t buf = p_count[0] & 1;
-          if (!tile_wait(&bar->p_ready[buf], (p_count[0] >> 1) & 1, bar, a.status)) return false;
+          const uint32_t buf = p_count[0] & 1, phase = (p_count[0] >> 1) & 1;
           ++p_count[0];
-          tc_fence_after();
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            if (!tile_wait(&bar->full[rp.stage], rp.phase, bar, a.status)) return false;
-            const uint32_t v = ring_at + rp.stage * kStageBytes;
-            if ((j + 1) * 128 > it.kv_len) zero_tail(v, it.kv_len - j * 128);
-            if (lead) {
-              issue_pv(tmem + 256 + c * 128, tmem + buf * 128, v, j > j0);
-              mma_commit(&bar->empty[rp.stage]);
-              if (c == 1) mma_commit(&bar->pv_done[0]);
-              if (c == 1 && j + 1 == j1) mma_commit(&bar->pv_done[1]);
-            }
-            __syncwarp();
-            rp.next();
+          const RingPos v0 = rp;
+          rp.next();
+          const RingPos v1 = rp;
+          rp.next();
+          const uint32_t s0 = ring_at + v0.stage * kStageBytes, s1 = ring_at + v1.stage * kStageBytes;
+          if (!lane_wait(&bar->full[v0.stage], v0.phase, bar, a.status)) return false;
+          if (!lane_wait(&bar->full[v1.stage], v1.phase, bar, a.status)) return false;
+          if (j + 1 == j1 && tail) {
+            mbar_arrive(&bar->to_clear);
+          if (!lane_wait(&bar->cleared, c_phase, bar, a.status)) return false;
+            c_phase ^= 1;
           }
+          if (!lane_wait(&bar->p_half[buf], phase, bar, a.status)) return false;
+          tc_fence_after();
+          issue_pv(256, buf * 128, s0, 0, j > j0);
+          issue_pv(384, buf * 128, s1, 0, j > j0);
+          if (!lane_wait(&bar->p_ready[buf], phase, bar, a.status)) return false;
+          tc_fence_after();
+          issue_pv(256, buf * 128, s0, 1, true);
+          mma_commit(&bar->empty[v0.stage]);
+          issue_pv(384, buf * 128, s1, 1, true);
+          mma_commit(&bar->empty[v1.stage]);
+          mma_commit(&bar->pv_done[0]);
+          if (j + 1 == j1) mma_commit(&bar->pv_done[1]);
         }
       }
     }
@@ -446,7 +470,46 @@ __device__ __forceinline__ bool mma_items(const TileArgs &a, TileBars *bar, uint
   return true;
 }
 
+// ------------------------------------------------------------------ clearing warp
+// Zeroes the rows of an item's last V block that lie behind the context: P is 0 there, and must
+// meet 0 whatever memory holds.  It finds the block's stages by counting the ring; the MMA lane
+// tells it that they have landed and waits for it.
+template <int D>
+__device__ __forceinline__ void clear_tails(const TileArgs &a, TileBars *bar, uint32_t ring_at) {
+  constexpr int NP = D / 128;
+  const int lane = threadIdx.x & 31;
+  uint32_t phase = 0;
+  RingPos rp;
+  ItemList list;
+  list.start(a);
+  while (list.advance()) {
+    tgi::TileRange r0, r1;
+    const tgi::TileRange rg = item_range<D, false>(list.cur, a, &r0, &r1);
+    if (rg.b >= rg.e) continue;
+    rp.skip((rg.e - rg.b) * 2 * NP - NP);  // the item's last V block ends its stages
+    if (!has_tail<false>(list.cur, rg.e)) {
+      rp.skip(NP);
+      continue;
+    }
+    const int from = list.cur.kv_len - (rg.e - 1) * 128;
+    if (!tile_wait(&bar->to_clear, phase, bar, a.status)) return;
+    phase ^= 1;
+    for (int c = 0; c < NP; ++c) {
+      for (int i = from * 8 + lane; i < 128 * 8; i += 32) {
+        const uint32_t at = ring_at + rp.stage * kStageBytes + (uint32_t)i * 16;
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + kHalfBytes), "r"(0) : "memory");
+      }
+      rp.next();
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar->cleared);
+  }
+}
+
 // ------------------------------------------------------------------ loader warp
+// The lanes look up the pages of a block's boxes, one block ahead; an elected lane issues the copies.
 template <int D, bool PAGED>
 __device__ __forceinline__ void load_items(const CUtensorMap *qm, const CUtensorMap *km, const CUtensorMap *vm,
                                            const TileArgs &a, TileBars *bar, uint32_t q_at, uint32_t ring_at) {
@@ -456,33 +519,29 @@ __device__ __forceinline__ void load_items(const CUtensorMap *qm, const CUtensor
   uint32_t filled = 0, q_count = 0;  // stages filled, Q loads
   bool ok = true;
   const uint32_t q_box = (uint32_t)a.tq * a.g * 128;  // bytes of one 64-column box of Q
+  const int outside = PAGED ? (int)(a.pool_pages * a.H_p * 2) : 0;  // a block past the pool: reads as zeros
+  const int boxes = PAGED ? 128 / a.R : 0;
   ItemList list;
   list.start(a);
   while (ok && list.advance()) {
-    const tg_tile_item it = list.cur;
-    const tgi::TileRange r0 = tgi::tile_range(it, 0, a.tq, a.window, !PAGED);
-    tgi::TileRange r1 = {0, 0};
-    if (D == 128) r1 = tgi::tile_range(it, 1, a.tq, a.window, !PAGED);
-    const bool has0 = r0.b < r0.e, has1 = D == 128 && r1.b < r1.e;
-    if (!has0 && !has1) continue;
-    const int j0 = has0 ? (has1 ? min(r0.b, r1.b) : r0.b) : r1.b;
-    const int j1 = has0 ? (has1 ? max(r0.e, r1.e) : r0.e) : r1.e;
-    int64_t off0 = 0, off1 = 0;
-    if (PAGED) off0 = a.pt_off[it.src], off1 = a.pt_off[it.src + 1];
-    const int outside = PAGED ? (int)(a.pool_pages * a.H_p * 2) : 0;  // a block past the pool: reads as zeros
-    // this lane's box of block j: its (page block, row); lanes past the boxes do nothing
-    const int boxes = PAGED ? 128 / a.R : 0;
+    const tg_tile_item &it = list.cur;
+    tgi::TileRange r0, r1;
+    const tgi::TileRange rg = item_range<D, PAGED>(it, a, &r0, &r1);
+    const int j0 = rg.b, j1 = rg.e;
+    if (j0 >= j1) continue;
+    int64_t off0 = 0;
+    int lists = 0;  // pages of the list
+    if (PAGED) {
+      off0 = a.pt_off[it.src];
+      lists = (int)(a.pt_off[it.src + 1] - off0);
+    }
+    // lane i: the page block (K's; V's is the next) and first row of box i of block j
     auto place = [&](int j, int *row) -> int {
       const int t = j * 128 + lane * a.R;
-      *row = 0;
-      if (lane >= boxes || t >= it.kv_len || j >= j1) return outside;
       const int pg = t / a.P;
       *row = t - pg * a.P;
-      if (off0 + pg >= off1) {
-        report(a.status, TG_STATUS_BAD_PAGE);
-        return outside;
-      }
-      const int32_t id = __ldg(a.pt_ids + off0 + pg);
+      if (lane >= boxes || t >= it.kv_len || j >= j1) return outside;
+      const int32_t id = pg < lists ? __ldg(a.pt_ids + off0 + pg) : -1;
       if (id < 0 || id >= a.pool_pages) {
         report(a.status, TG_STATUS_BAD_PAGE);
         return outside;
@@ -496,16 +555,31 @@ __device__ __forceinline__ void load_items(const CUtensorMap *qm, const CUtensor
         if (filled >= kStages && !tile_wait(&bar->empty[rp.stage], rp.phase ^ 1, bar, a.status)) return false;
         const uint32_t dst = ring_at + rp.stage * kStageBytes;
         uint64_t *full = &bar->full[rp.stage];
-        if (lane == 0) mbar_arrive_expect_tx(full, kStageBytes);
-        __syncwarp();
         if (PAGED) {
-          if (lane < boxes) {
-            const int zz = z == outside ? z : z + kv;
-            tma_load_3d(dst + lane * a.R * 128, km, full, c * 128, row, zz);
-            tma_load_3d(dst + kHalfBytes + lane * a.R * 128, km, full, c * 128 + 64, row, zz);
+          int zs[8], rows[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int zi = __shfl_sync(0xffffffffu, z, i);
+            zs[i] = zi == outside ? zi : zi + kv;
+            rows[i] = __shfl_sync(0xffffffffu, row, i);
           }
-        } else if (lane < 2) {
-          tma_load_3d(dst + lane * kHalfBytes, kv ? vm : km, full, c * 128 + lane * 64, j * 128, it.src * a.H + it.h);
+          if (elect_one()) {
+            mbar_arrive_expect_tx(full, kStageBytes);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (i < boxes) {
+                const uint32_t to = dst + i * a.R * 128;
+                tma_load_3d(to, km, full, c * 128, rows[i], zs[i]);
+                tma_load_3d(to + kHalfBytes, km, full, c * 128 + 64, rows[i], zs[i]);
+              }
+            }
+          }
+        } else if (elect_one()) {
+          const CUtensorMap *m = kv ? vm : km;
+          const int context = it.src * a.H + it.h;
+          mbar_arrive_expect_tx(full, kStageBytes);
+          tma_load_3d(dst, m, full, c * 128, j * 128, context);
+          tma_load_3d(dst + kHalfBytes, m, full, c * 128 + 64, j * 128, context);
         }
         __syncwarp();
         ++filled;
@@ -513,68 +587,60 @@ __device__ __forceinline__ void load_items(const CUtensorMap *qm, const CUtensor
       }
       return true;
     };
-    int row_next = 0, z_next = 0;
-    if (PAGED) z_next = place(j0, &row_next);
+    int z = 0, row = 0, z_next = 0, row_next = 0, z_before = 0, row_before = 0;
+    if (PAGED) z = place(j0, &row);
     if (q_count > 0 && !tile_wait(&bar->q_empty, (q_count - 1) & 1, bar, a.status)) {
       ok = false;
       break;
     }
     ++q_count;
-    const uint32_t n_boxes = D == 128 ? (has0 ? 2 : 0) + (has1 ? 2 : 0) : 4;
-    if (lane == 0) mbar_arrive_expect_tx(&bar->q_full, n_boxes * q_box);
-    __syncwarp();
-    if (lane < 4) {
+    if (elect_one()) {
       if (D == 128) {
-        const int i = lane >> 1;
-        if (i ? has1 : has0)
-          tma_load_3d(q_at + lane * kHalfBytes, qm, &bar->q_full, (lane & 1) * 64, it.h * a.g, it.row0 + i * a.tq);
+        const bool has0 = r0.b < r0.e, has1 = r1.b < r1.e;
+        mbar_arrive_expect_tx(&bar->q_full, ((has0 ? 2 : 0) + (has1 ? 2 : 0)) * q_box);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if ((c >> 1) ? has1 : has0)
+            tma_load_3d(q_at + c * kHalfBytes, qm, &bar->q_full, (c & 1) * 64, it.h * a.g, it.row0 + (c >> 1) * a.tq);
       } else {
-        tma_load_3d(q_at + lane * kHalfBytes, qm, &bar->q_full, lane * 64, it.h * a.g, it.row0);
+        mbar_arrive_expect_tx(&bar->q_full, 4 * q_box);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tma_load_3d(q_at + c * kHalfBytes, qm, &bar->q_full, c * 64, it.h * a.g, it.row0);
       }
     }
     __syncwarp();
-    int z_before = 0, row_before = 0;
     for (int j = j0; ok && j < j1; ++j) {
-      const int z = z_next, row = row_next;
-      if (PAGED && j + 1 < j1) z_next = place(j + 1, &row_next);
+      if (PAGED) z_next = place(j + 1, &row_next);
       ok = fill(j, 0, z, row);
       if (D == 128) {
         if (ok) ok = fill(j, 1, z, row);
       } else {
         if (ok && j > j0) ok = fill(j - 1, 1, z_before, row_before);
-        z_before = z, row_before = row;
         if (ok && j + 1 == j1) ok = fill(j, 1, z, row);
+        z_before = z, row_before = row;
       }
+      z = z_next, row = row_next;
     }
   }
   // leave nothing in flight: every stage used and Q must have been consumed, or, after a
   // give-up, at least have landed
-  if (ok) {
-    for (int i = 0; ok && i < kStages; ++i) {
-      if (filled >= (uint32_t)kStages || (uint32_t)i < filled) {
-        const uint32_t uses = (filled - 1 - i) / kStages + 1;  // fills of stage i
-        ok = tile_wait(&bar->empty[i], (uses - 1) & 1, bar, a.status);
-      }
-    }
-    if (ok && q_count) ok = tile_wait(&bar->q_empty, (q_count - 1) & 1, bar, a.status);
-  }
+  for (uint32_t i = 0; ok && i < kStages && i < filled; ++i)
+    ok = tile_wait(&bar->empty[i], ((filled - 1 - i) / kStages) & 1, bar, a.status);
+  if (ok && q_count) ok = tile_wait(&bar->q_empty, (q_count - 1) & 1, bar, a.status);
   if (!ok) {
-    for (int i = 0; i < kStages; ++i) {
-      if ((uint32_t)i >= filled) continue;
-      const uint32_t uses = (filled - 1 - i) / kStages + 1;
-      mbar_wait(&bar->full[i], (uses - 1) & 1, 100000000ull);
-    }
+    for (uint32_t i = 0; i < kStages && i < filled; ++i)
+      mbar_wait(&bar->full[i], ((filled - 1 - i) / kStages) & 1, 100000000ull);
     if (q_count) mbar_wait(&bar->q_full, (q_count - 1) & 1, 100000000ull);
     __syncwarp();
   }
 }
 
-// d = 128: two softmax warpgroups and a third of the MMA warp, the loader and two idle warps, so
-// that registers can move from the third to the first two (168 each at launch: 384 x 168 =
-// 256 x 216 + 128 x 72); d = 256: six warps, 255 registers each at most.
+// d = 128: two softmax warpgroups and a third of the MMA, loader and clearing warps and an idle
+// one, so that registers can move from the third to the first two (168 each at launch: 384 x 168
+// = 256 x 216 + 128 x 72); d = 256: seven warps, 255 registers each at most.
 template <int D>
 constexpr int tile_threads() {
-  return D == 128 ? 384 : 192;
+  return D == 128 ? 384 : 224;
 }
 
 template <int D, bool PAGED>
@@ -592,7 +658,12 @@ __global__ void __launch_bounds__(tile_threads<D>(), 1)
     mbar_init(&bar->q_full, 1);
     mbar_init(&bar->q_empty, 1);
     for (int i = 0; i < kStages; ++i) mbar_init(&bar->full[i], 1), mbar_init(&bar->empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&bar->s_full[i], 1), mbar_init(&bar->p_ready[i], 4), mbar_init(&bar->pv_done[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar->s_full[i], 1), mbar_init(&bar->pv_done[i], 1);
+      mbar_init(&bar->p_half[i], 4), mbar_init(&bar->p_ready[i], 4);
+    }
+    mbar_init(&bar->to_clear, 1);
+    mbar_init(&bar->cleared, 1);
     mbar_init(&bar->drain, 1);
     bar->abort = 0;
     fence_barrier_init();
@@ -600,33 +671,33 @@ __global__ void __launch_bounds__(tile_threads<D>(), 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bar->tmem;
+  // all 512 columns are this block's, so they start at column 0: the MMAs and the softmax
+  // address them by constants
   if (warp < SW) {
     if (D == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    softmax_role<D, PAGED>(a, bar, tmem, warp >> 2);
-  } else if (warp == SW) {
+    softmax_role<D, PAGED>(a, bar, warp >> 2);
+  } else {
     if (D == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (!mma_items<D, PAGED>(a, bar, tmem, q_at, ring_at)) {
-      // gave up: what was issued must finish before tensor memory is freed
-      __syncwarp();
-      if ((threadIdx.x & 31) == 0) {
+    if (warp == SW) {
+      if (elect_one() && !mma_items<D, PAGED>(a, bar, q_at, ring_at)) {
+        // gave up: what was issued must finish before tensor memory is freed
         mma_commit(&bar->drain);
         mbar_wait(&bar->drain, 0, 100000000ull);
       }
+    } else if (warp == SW + 1) {
+      if (elect_one()) prefetch_tensormap(&qm), prefetch_tensormap(&km), prefetch_tensormap(&vm);
       __syncwarp();
+      load_items<D, PAGED>(&qm, &km, &vm, a, bar, q_at, ring_at);
+    } else if (warp == SW + 2) {
+      if (!PAGED) clear_tails<D>(a, bar, ring_at);
     }
-  } else if (warp > SW + 1) {
-    if (D == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-  } else {
-    if (D == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if ((threadIdx.x & 31) == 0) prefetch_tensormap(&qm), prefetch_tensormap(&km), prefetch_tensormap(&vm);
-    load_items<D, PAGED>(&qm, &km, &vm, a, bar, q_at, ring_at);
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
   if (a.signal) griddep_launch_dependents();
   tc_fence_after();
-  if (warp == SW) tmem_free(tmem, 512);
+  if (warp == SW) tmem_free(bar->tmem, 512);
 }
 
 // ------------------------------------------------------------------ merge of cut runs
