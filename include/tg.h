@@ -592,7 +592,7 @@ typedef struct tg_tile_header {
   int32_t window;            /* prefill only */
   int32_t max_kv;            /* longest context (prefill) or retained run (prefix) */
   int32_t N_CTA, n_items, n_merge, n_slots;
-  int32_t reserved;
+  int32_t block;             /* keys of a block */
   int64_t plan_bytes, workspace_bytes;
   int64_t lead, items, merges;
 } tg_tile_header;
@@ -604,7 +604,7 @@ typedef struct tg_tile_item {
   int32_t hpos;       /* prefix: the head's place in its page group */
   int32_t pos0;       /* prefill: context position of row0 (may be negative: it sees no key) */
   int32_t kv_len;     /* keys [0, kv_len) exist */
-  int32_t blk0, blk1; /* key blocks [blk0, blk1) of 128 */
+  int32_t blk0, blk1; /* key blocks [blk0, blk1) */
   int32_t slot;       /* partial slot, -1: the item finishes its rows alone */
   int32_t reserved[2];
 } tg_tile_item;

@@ -607,7 +607,7 @@ def tg_plan_prefix(req_off, head_order, ntok, H_q: int, H_p: int, P: int, d: int
 
 _TILE_HEADER_DTYPE = np.dtype([("magic", "<u4")] + [(n, "<i4") for n in (
     "version", "kind", "batch", "groups", "rows", "H", "H_q", "H_p", "P", "d", "window", "max_kv", "N_CTA", "n_items",
-    "n_merge", "n_slots", "reserved")] + [(n, "<i8") for n in ("plan_bytes", "workspace_bytes", "lead", "items", "merges")])
+    "n_merge", "n_slots", "block")] + [(n, "<i8") for n in ("plan_bytes", "workspace_bytes", "lead", "items", "merges")])
 TILE_ITEM_DTYPE = np.dtype([(n, "<i4") for n in ("row0", "nrow", "h", "src", "hpos", "pos0", "kv_len", "blk0", "blk1",
                                                  "slot")] + [("reserved", "<i4", (2,))])
 

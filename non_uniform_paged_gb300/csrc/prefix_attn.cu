@@ -28,13 +28,11 @@ extern "C" int tg_prefix_attn(tg_stream_t stream, const void *plan_host, const v
   if (rc) return rc;
   a.P = hd->P;
   a.H_p = hd->H_p;
-  a.R = tgi::kTileKeys;  // the largest power of two that divides P and 128 (P % 16 == 0)
-  while (hd->P % a.R) a.R /= 2;
   if (hd->max_kv > 0) {
     if (!pool || !pt_off || !pt_ids) return tgi::fail(TG_ERR_INVALID_ARG, "%s: NULL pool or page table", fn);
     if (pool_pages <= 0 || pool_pages > INT32_MAX / (2 * hd->H_p) - 1)
       return tgi::fail(TG_ERR_CAPACITY, "%s: pool_pages=%lld", fn, (long long)pool_pages);
-    rc = tile_map(&pm, fn, "pool", pool, hd->d, hd->P, pool_pages * hd->H_p * 2, a.R, 1);
+    rc = tile_map(&pm, fn, "pool", pool, hd->d, hd->P, pool_pages * hd->H_p * 2, 16, 1);
     if (rc) return rc;
   } else {
     pm = qm;  // nothing is shared: never read

@@ -8,7 +8,7 @@
 namespace tgi {
 
 constexpr int kTileRows = 128;  // rows of one MMA tile: tokens (or requests) x the g heads of a KV head
-constexpr int kTileKeys = 128;  // keys of one block
+constexpr int kTileKeys = 80;   // keys of one block (three S buffers fit beside O in tensor memory)
 constexpr int kPrefillPlan = 0, kPrefixPlan = 1;
 
 // tiles of one item: two at d = 128, one at d = 256 (their outputs fill tensor memory)
@@ -44,7 +44,7 @@ inline
   return r;
 }
 
-// workspace: m, l float32 [slots][256][2] | o float32 [slots][256 x 128 or 128 x 256]
+// workspace: m, l float32 [slots][256][2] | o float32 [slots][d / 4][32768 / d rows][4]
 constexpr int64_t kSlotMl = 256 * 2 * 4;
 constexpr int64_t kSlotO = 32768 * 4;
 

@@ -96,9 +96,17 @@ int launch_tiles(const char *fn, tg_stream_t stream, const tg_tile_header *hd, c
   cudaError_t e = cudaFuncSetAttribute(tile_attn_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)kTileSmem);
   if (e != cudaSuccess) return tgi::fail(TG_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", fn, cudaGetErrorString(e));
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  tile_attn_kernel<D, PAGED><<<hd->N_CTA, tile_threads<D>(), kTileSmem, s>>>(qm, km, vm, a);
-  e = cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)hd->N_CTA);
+  cfg.blockDim = dim3(tile_threads<D>());
+  cfg.dynamicSmemBytes = kTileSmem;
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, tile_attn_kernel<D, PAGED>, qm, km, vm, a);
   if (e != cudaSuccess) return tgi::fail(TG_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
   if (!hd->n_merge) return tgi::ok();
   MergeArgs m;
@@ -106,15 +114,9 @@ int launch_tiles(const char *fn, tg_stream_t stream, const tg_tile_header *hd, c
   m.ws_ml = a.ws_ml, m.ws_o = a.ws_o, m.out = a.out, m.lse = a.lse;
   m.own_out = a.own_out, m.own_lse = a.own_lse;
   m.H_q = a.H_q, m.g = a.g, m.tq = a.tq;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)hd->n_merge * (256 / kMergeWarps));
-  cfg.blockDim = dim3(kMergeWarps * 32);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)(hd->n_merge * merge_blocks(D)));
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, tile_merge_kernel<D>, m);
   if (e != cudaSuccess) return tgi::fail(TG_ERR_CUDA, "%s: merge launch failed: %s", fn, cudaGetErrorString(e));
   return tgi::ok();

@@ -23,9 +23,9 @@ namespace {
 
 using tgi::fail;
 
-// Cost model in units of one 128-key block of an item: an item's start and end, a piece's
+// Cost model in units of one 80-key block of an item (about 0.75 us): an item's start and end, a piece's
 // partial (written and read again), and the second kernel of a plan that has any.
-constexpr double kItemCost = 2.0, kPieceCost = 1.0, kMergeCost = 2.0;
+constexpr double kItemCost = 3.0, kPieceCost = 1.5, kMergeCost = 4.0;
 
 double item_cost(const tg_tile_item &it, bool piece) {
   return (it.blk1 - it.blk0) + kItemCost + (piece ? kPieceCost : 0.0);
@@ -137,6 +137,7 @@ int finish(const char *fn, tg_tile_header hd, std::vector<tg_tile_item> &base, v
   hd.items = hd.lead + (int64_t)n_cta * sizeof(tg_tile_item);
   hd.merges = hd.items + (int64_t)items.size() * sizeof(tg_tile_item);
   hd.plan_bytes = hd.merges + (int64_t)merges.size() * sizeof(tg_tile_merge);
+  hd.block = tgi::kTileKeys;
   hd.workspace_bytes = slots * (tgi::kSlotMl + tgi::kSlotO);
   if (plan_bytes) *plan_bytes = hd.plan_bytes;
   if (workspace_bytes) *workspace_bytes = hd.workspace_bytes;

@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 
-def _needed(row0, nrow, pos0, kv_len, tq, tiles, window, causal):
+def _needed(row0, nrow, pos0, kv_len, tq, tiles, window, causal, block):
     """Key blocks that each 128-row tile of an item needs, by brute force over its rows."""
     out = []
     for i in range(tiles):
@@ -16,7 +16,7 @@ def _needed(row0, nrow, pos0, kv_len, tq, tiles, window, causal):
             hi = min(kv_len, pos0 + r + 1) if causal else kv_len
             lo = max(0, pos0 + r - window + 1) if causal and window else 0
             if hi > lo:
-                blocks.update(range(lo // 128, (hi - 1) // 128 + 1))
+                blocks.update(range(lo // block, (hi - 1) // block + 1))
         out.append(blocks)
     return out
 
@@ -46,7 +46,7 @@ def _check_plan(lib, plan, ws, want, tq, tiles, window, causal):
         assert all((int(p["nrow"]), int(p["kv_len"]), int(p["hpos"])) == (nrow, kv_len, hpos) for p in parts)
         if causal:
             assert all(int(p["pos0"]) == pos0 for p in parts)
-        need = _needed(key[2], nrow, pos0, kv_len, tq, tiles, window, causal)
+        need = _needed(key[2], nrow, pos0, kv_len, tq, tiles, window, causal, hd["block"])
         every = set().union(*need)
         covered = [b for p in parts for b in range(int(p["blk0"]), int(p["blk1"]))]
         assert len(covered) == len(set(covered)) and every <= set(covered)
@@ -110,7 +110,7 @@ def test_one_long_run_is_cut_over_the_blocks(lib):
     hd = lib.tile_header(plan)
     _, items = lib.tile_items(plan)
     assert hd["n_merge"] == 1 and 100 <= hd["n_items"] <= 152 and ws > 0
-    assert (items["blk1"] - items["blk0"]).max() <= 2 * 782 // 152 + 1
+    assert (items["blk1"] - items["blk0"]).max() <= 2 * (100000 // hd["block"]) // 152 + 1
     plan, ws = lib.tg_plan_prefill([16384], [16384], 8, 32, 128, 152)
     assert lib.tile_header(plan)["n_merge"] == 0 and ws == 0
 
