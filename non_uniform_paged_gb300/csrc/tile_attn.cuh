@@ -20,14 +20,15 @@
 //   then two warps whose elected lanes issue the MMAs, one that streams Q, K and V by TMA, and
 //   one that clears the V rows behind the end of a context.
 // K and V go through a ring of eight 20 KB stages (80 keys x 128 columns each; d = 256
-// takes two per block).  P overwrites S in tensor memory and is the A operand of P V.
+// takes two per block).
 //
-// Why 80 keys: O takes 256 of the 512 columns of tensor memory, and the rest holds three S
-// buffers of 80.  With three, the Q K^T of a tile's next block is issued before the P V of its
-// last, so a softmax warp finds its next S ready when it has handed over its weights, and the
-// tensor cores always have a product to do: the way from "weights ready" to the next S (about
-// 250 clocks to the MMA lane, 1024 of MMAs and 400 back) is off the critical path.  With two
-// buffers of 128 that way and the softmax (1500 clocks) alternated, 3100 clocks for 2048 of MMAs.
+// Why 80 keys: O takes 256 of the 512 columns of tensor memory; two S of 80 columns and two P of
+// 40 (bf16, the A operand of P V) fit in the rest.  A softmax warp reads its S into registers at
+// once and gives the buffer back, so the next Q K^T runs while it computes, and P V of a block
+// runs while it computes the next: no product waits for the other, and the way over the barriers
+// (about 300 clocks each time) is off the critical path.  At d = 128 each tile has an S and a P of
+// its own, at d = 256 the blocks of the tile alternate between them.  With S of 128 columns and P
+// in their place the softmax and both products alternated: 3100 clocks for 2048 of MMAs.
 // Items of the plan follow one another without a break: the loader runs ahead into the next.
 #pragma once
 
@@ -44,7 +45,7 @@ constexpr uint32_t kStageBytes = 2 * kHalfBytes;  // 80 rows x 128 bf16
 constexpr uint32_t kQPiece = 32768;               // 128 rows x 128 columns
 constexpr uint32_t kQBytes = 2 * kQPiece;         // 256 x 128 or 128 x 256
 constexpr uint32_t kTileSmem = kQBytes + kStages * kStageBytes + 1024 + 1024;  // + barriers, + alignment
-constexpr int kBufs = 3;           // S buffers, at columns 0, 80 and 160
+constexpr uint32_t kWeights = 160;  // first column of P (S: 0 and 80)
 constexpr uint32_t kOut = 256;     // first column of O
 constexpr uint64_t kTileWaitNs = 2000000000ull;
 constexpr float kTileLn2 = 0.69314718055994531f;
@@ -70,13 +71,12 @@ struct TileArgs {
 
 // Barriers and flags, by byte offset from their shared-memory address (32-bit addresses keep the
 // MMA lanes' code short: one lane runs an instruction every few clocks only).
-//   s_full: S written, by tile and turn (three S at most are ahead of the softmax, all of one tile
-//   perhaps); p_ready: its weights stored, and pv_done: multiplied with V and added to O, by S
-//   buffer; o_done: an item's last P V of a tile.  No phase that somebody waits for can be
-//   overtaken by the next one of its barrier.
+//   by S and P buffer -- s_full: S written; s_free: read; p_ready: P written; pv_done: multiplied
+//   with V and added to O.  Whoever waits for a phase of one of them takes part in the next, so none
+//   is overtaken.
 constexpr uint32_t kQFull = 0, kQEmpty = 8, kFull = 16, kEmpty = kFull + 8 * kStages, kSFull = kEmpty + 8 * kStages,
-                   kPReady = kSFull + 16 * kBufs, kPvDone = kPReady + 8 * kBufs, kODone = kPvDone + 8 * kBufs, kToClear = kODone + 16,
-                   kCleared = kToClear + 8, kDrain = kCleared + 8, kTmemSlot = kDrain + 16, kAbort = kTmemSlot + 4;
+                   kPvDone = kSFull + 16, kToClear = kPvDone + 16, kCleared = kToClear + 8, kDrain = kCleared + 8,
+                   kSFree = kDrain + 16, kPReady = kSFree + 16, kTmemSlot = kPReady + 16, kAbort = kTmemSlot + 4;
 
 __device__ __forceinline__ void bar_init(uint32_t at, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(at), "r"(count) : "memory");
@@ -190,20 +190,21 @@ __device__ __forceinline__ bool needs(const tgi::TileRange &r, int j) { return j
 // ------------------------------------------------------------------ softmax and output warps
 template <int D, bool PAGED>
 __device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, int tile) {
-  constexpr int TILES = D == 128 ? 2 : 1, ROWS = D == 128 ? 256 : 128;
+  constexpr int ROWS = D == 128 ? 256 : 128;
   const int r = threadIdx.x & 127;             // row of the tile = lane of tensor memory
   const int tok = r / a.g, head = r - tok * a.g;
   const uint32_t lanes = (uint32_t)(r & ~31) << 16;
   const uint32_t o_base = kOut + (D == 128 ? tile * 128 : 0) + lanes;
   const float sl2 = a.scale_log2;
-  uint32_t item_count = 0;
-  Cycle<kBufs> turn;
-  Cycle<kBufs> sc;  // S buffers go round over the blocks of both tiles
+  uint32_t count = 0;  // blocks done
+  // block n of this warp uses buffer slot_of(n), for the turn_of(n)-th time
+  auto slot_of = [&](uint32_t n) -> uint32_t { return D == 128 ? (uint32_t)tile : n & 1; };
+  auto phase_of = [&](uint32_t n) -> uint32_t { return (D == 128 ? n : n >> 1) & 1; };
   ItemList list;
   list.start(a);
   while (list.advance()) {
     const tg_tile_item &it = list.cur;
-    const ItemRange rg = item_range<D, PAGED>(it, a);
+    const tgi::TileRange rg = tgi::tile_range(it, tile, a.tq, a.window, !PAGED);
     const int first = tile * a.tq;
     const int n = min(it.nrow - first, a.tq);
     int lo = 0, hi = it.kv_len;            // keys [lo, hi) that this row sees
@@ -218,27 +219,20 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, i
       }
     }
     float m = -INFINITY, l = 0.f;
-    bool some = false;
-    uint32_t last_buf = 0, last_phase = 0;
-    const tgi::TileRange ours = tile ? rg.tile[1] : rg.tile[0], other = tile ? rg.tile[0] : rg.tile[1];
-    for (int j = rg.b; j < rg.e; ++j) {
-      if (TILES == 2 && tile == 1 && needs(other, j)) sc.next();
-      if (!needs(ours, j)) {
-        if (TILES == 2 && tile == 0 && needs(other, j)) sc.next();
-        continue;
-      }
-      const uint32_t buf = sc.at, phase = sc.phase;
-      sc.next();
-      if (TILES == 2 && tile == 0 && needs(other, j)) sc.next();
-      const uint32_t s_addr = buf * kKeys + lanes;
-      if (!tile_wait(bars, kSFull + 8 * (kBufs * tile + turn.at), turn.phase, a.status)) return;
-      turn.next();
+    const bool some = rg.b < rg.e;
+    for (int j = rg.b; j < rg.e; ++j, ++count) {
+      const uint32_t slot = slot_of(count);
+      if (!tile_wait(bars, kSFull + 8 * slot, phase_of(count), a.status)) return;
       tc_fence_after();
       float s[kKeys];
+      const uint32_t s_addr = slot * kKeys + lanes;
       tmem_ld32(s_addr, reinterpret_cast<uint32_t *>(s));
       tmem_ld32(s_addr + 32, reinterpret_cast<uint32_t *>(s) + 32);
       tmem_ld16(s_addr + 64, reinterpret_cast<uint32_t *>(s) + 64);
       tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) bar_arrive(bars + kSFree + 8 * slot);
       const int k0 = j * kKeys;
       if (k0 + kKeys > hi_first || k0 < lo_last) {
         const int h1 = hi - k0, l1 = lo - k0;
@@ -261,11 +255,11 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, i
         if (m == -INFINITY) m = mx;
       }
       float part;
+      uint32_t p[kKeys / 2];
 #pragma unroll 1
       for (bool again = false;; again = true) {
         const float neg = m == -INFINITY ? 0.f : -m * sl2;
         float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
-        uint32_t p[kKeys / 2];
 #pragma unroll
         for (int k = 0; k < kKeys / 2; ++k) {
           float2 x = fma2(make_float2(s[2 * k], s[2 * k + 1]), make_float2(sl2, sl2), make_float2(neg, neg));
@@ -273,18 +267,15 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, i
           x.y = ex2(x.y);
           sum[k & 1] = add2(sum[k & 1], x);
           p[k] = pack_bf16x2(x.x, x.y);
-          if (k == 15) tmem_st16(s_addr, p);
-          if (k == 31) tmem_st16(s_addr + 16, p + 16);
         }
-        tmem_st8(s_addr + 32, p + 32);
         part = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         if (again || !__any_sync(0xffffffffu, part > kMost)) break;
         const float m_new = fmaxf(m, find_max());
         const float f = m_new == -INFINITY ? 1.f : ex2((m - m_new) * sl2);
         m = m_new;
         l *= f;
-        if (some) {  // scale O, once the block before has been added to it
-          if (!tile_wait(bars, kPvDone + 8 * last_buf, last_phase, a.status)) return;
+        if (j > rg.b) {  // scale O, once the block before has been added to it
+          if (!tile_wait(bars, kPvDone + 8 * slot_of(count - 1), phase_of(count - 1), a.status)) return;
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -297,13 +288,20 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, i
           }
         }
       }
+      l += part;
+      // P of this buffer's block before has been multiplied
+      constexpr uint32_t back = D == 128 ? 1 : 2;
+      if (count >= back) {
+        if (!tile_wait(bars, kPvDone + 8 * slot, phase_of(count - back), a.status)) return;
+        tc_fence_after();
+      }
+      const uint32_t p_addr = kWeights + slot * (kKeys / 2) + lanes;
+      tmem_st32(p_addr, p);
+      tmem_st8(p_addr + 32, p + 32);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if ((threadIdx.x & 31) == 0) bar_arrive(bars + kPReady + 8 * buf);
-      last_buf = buf, last_phase = phase;
-      l += part;
-      some = true;
+      if ((threadIdx.x & 31) == 0) bar_arrive(bars + kPReady + 8 * slot);
     }
     if (n <= 0) continue;
 
@@ -311,7 +309,7 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, i
     const bool mine = tok < n && r < a.tq * a.g;
     const int64_t row = ((int64_t)(it.row0 + first + tok)) * a.H_q + it.h * a.g + head;
     if (some) {
-      if (!tile_wait(bars, kODone + 8 * tile, item_count++ & 1, a.status)) return;
+      if (!tile_wait(bars, kPvDone + 8 * slot_of(count - 1), phase_of(count - 1), a.status)) return;
       tc_fence_after();
     }
     const float mo = m == -INFINITY ? -INFINITY : m * sl2;  // base-2 reference
@@ -418,8 +416,7 @@ template <int D, bool PAGED>
 __device__ __forceinline__ bool qk_items(const TileArgs &a, uint32_t bars, uint32_t q_at, uint32_t ring_at) {
   constexpr int NP = D / 128, TILES = 2 / NP;
   Cycle<kStages> ring;
-  Cycle<kBufs> sc, turn[2];
-  uint32_t q_phase = 0, seq = 0;
+  uint32_t q_phase = 0, count[2] = {0, 0};
   ItemList list;
   list.start(a);
   while (list.advance()) {
@@ -440,14 +437,14 @@ __device__ __forceinline__ bool qk_items(const TileArgs &a, uint32_t bars, uint3
 #pragma unroll
       for (int i = 0; i < TILES; ++i) {
         if (!needs(rg.tile[i], j)) continue;
-        if (seq >= kBufs && !lane_wait(bars, kPvDone + 8 * sc.at, sc.phase ^ 1, a.status)) return false;
-        ++seq;
+        const uint32_t slot = D == 128 ? i : count[0] & 1, uses = D == 128 ? count[i] : count[0] >> 1;
+        if (uses > 0 && !lane_wait(bars, kSFree + 8 * slot, (uses - 1) & 1, a.status)) return false;
+        tc_fence_after();
+        ++count[i];
 #pragma unroll
         for (int c = 0; c < NP; ++c)
-          issue_qk(sc.at * kKeys, q_at + (D == 128 ? i : c) * kQPiece, ring_at + ks[c].at * kStageBytes, c > 0);
-        mma_commit(bars + kSFull + 8 * (kBufs * i + turn[i].at));
-        turn[i].next();
-        sc.next();
+          issue_qk(slot * kKeys, q_at + (D == 128 ? i : c) * kQPiece, ring_at + ks[c].at * kStageBytes, c > 0);
+        mma_commit(bars + kSFull + 8 * slot);
       }
 #pragma unroll
       for (int c = 0; c < NP; ++c) mma_commit(bars + kEmpty + 8 * ks[c].at);
@@ -463,8 +460,7 @@ template <int D, bool PAGED>
 __device__ __forceinline__ bool pv_items(const TileArgs &a, uint32_t bars, uint32_t ring_at) {
   constexpr int NP = D / 128, TILES = 2 / NP;
   Cycle<kStages> ring;
-  Cycle<kBufs> pc;
-  uint32_t c_phase = 0;
+  uint32_t c_phase = 0, count[2] = {0, 0};
   ItemList list;
   list.start(a);
   while (list.advance()) {
@@ -489,14 +485,15 @@ __device__ __forceinline__ bool pv_items(const TileArgs &a, uint32_t bars, uint3
 #pragma unroll
       for (int i = 0; i < TILES; ++i) {
         if (!needs(rg.tile[i], j)) continue;
-        if (!lane_wait(bars, kPReady + 8 * pc.at, pc.phase, a.status)) return false;
+        const uint32_t slot = D == 128 ? i : count[0] & 1, uses = D == 128 ? count[i] : count[0] >> 1;
+        if (!lane_wait(bars, kPReady + 8 * slot, uses & 1, a.status)) return false;
         tc_fence_after();
+        ++count[i];
 #pragma unroll
         for (int c = 0; c < NP; ++c)
-          issue_pv(kOut + (D == 128 ? i : c) * 128, pc.at * kKeys, ring_at + vs[c].at * kStageBytes, j > rg.tile[i].b);
-        mma_commit(bars + kPvDone + 8 * pc.at);
-        if (j + 1 == rg.tile[i].e) mma_commit(bars + kODone + 8 * i);
-        pc.next();
+          issue_pv(kOut + (D == 128 ? i : c) * 128, kWeights + slot * (kKeys / 2), ring_at + vs[c].at * kStageBytes,
+                   j > rg.tile[i].b);
+        mma_commit(bars + kPvDone + 8 * slot);
       }
 #pragma unroll
       for (int c = 0; c < NP; ++c) mma_commit(bars + kEmpty + 8 * vs[c].at);
@@ -678,7 +675,7 @@ __global__ void __launch_bounds__(tile_threads<D>(), 1)
   if (warp == SW) tmem_alloc(reinterpret_cast<uint32_t *>(base + kQBytes + kStages * kStageBytes + kTmemSlot), 512);
   if (warp == SW + 2 && elect_one()) prefetch_tensormap(&qm), prefetch_tensormap(&km), prefetch_tensormap(&vm);
   if (threadIdx.x == 0) {
-    for (uint32_t at = 0; at < kTmemSlot; at += 8) bar_init(bars + at, at >= kPReady && at < kPvDone ? 4 : 1);
+    for (uint32_t at = 0; at < kTmemSlot; at += 8) bar_init(bars + at, at >= kSFree ? 4 : 1);
     asm volatile("st.volatile.shared.s32 [%0], %1;" ::"r"(bars + kAbort), "r"(0) : "memory");
     fence_barrier_init();
   }
