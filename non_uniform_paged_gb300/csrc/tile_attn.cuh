@@ -16,7 +16,7 @@
 // heads of one KV head, so a key is read once for all heads that share it, and one query
 // token still fills g rows.  A thread block (one per SM, 227 KB of shared memory) works on
 // two tiles at d = 128 and one at d = 256.
-//   warps 0-3 (4-7): softmax and output of tile 0 (1), one row per thread;
+//   warps 0-7: softmax and output, a thread per row at d = 128, two at d = 256;
 //   then two warps whose elected lanes issue the MMAs, one that streams Q, K and V by TMA, and
 //   one that clears the V rows behind the end of a context.
 // K and V go through a ring of eight 20 KB stages (80 keys x 128 columns each; d = 256
@@ -46,6 +46,7 @@ constexpr uint32_t kQPiece = 32768;               // 128 rows x 128 columns
 constexpr uint32_t kQBytes = 2 * kQPiece;         // 256 x 128 or 128 x 256
 constexpr uint32_t kTileSmem = kQBytes + kStages * kStageBytes + 1024 + 1024;  // + barriers, + alignment
 constexpr uint32_t kWeights = 160;  // first column of P (S: 0 and 80)
+constexpr uint32_t kSwap = 240;    // columns through which two warps exchange row values
 constexpr uint32_t kOut = 256;     // first column of O
 constexpr uint64_t kTileWaitNs = 2000000000ull;
 constexpr float kTileLn2 = 0.69314718055994531f;
@@ -188,16 +189,47 @@ __device__ __forceinline__ ItemRange item_range(const tg_tile_item &it, const Ti
 __device__ __forceinline__ bool needs(const tgi::TileRange &r, int j) { return j >= r.b && j < r.e; }
 
 // ------------------------------------------------------------------ softmax and output warps
+// d = 128: a warp has 32 rows of its tile.  d = 256, one tile: two warps share 32 rows, each with 40
+// of a block's 80 keys and half of the output's columns; a row's reference is common to both, its
+// sum l is joined at the end, and a warp that gave up waiting goes on without waiting, so that its
+// partner finds it at their barrier.  (Two warps at d = 128 as well would be sixteen: what a block costs a
+// warp beside its keys then weighs more than the keys, 1.71 against 1.38 ms for 16384 tokens; at
+// d = 256, 0.34 against 0.36 ms for 8192.)
+template <int D>
+constexpr int halves() {
+  return D == 128 ? 1 : 2;
+}
 template <int D, bool PAGED>
-__device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, int tile) {
-  constexpr int ROWS = D == 128 ? 256 : 128;
+__device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, int tile, int half) {
+  constexpr int HALVES = halves<D>(), ROWS = D == 128 ? 256 : 128, N = kKeys / HALVES, COLS = D / HALVES;
   const int r = threadIdx.x & 127;             // row of the tile = lane of tensor memory
+  const int pair = 1 + (r >> 5);               // named barrier of two warps that share rows
   const int tok = r / a.g, head = r - tok * a.g;
   const uint32_t lanes = (uint32_t)(r & ~31) << 16;
-  const uint32_t o_base = kOut + (D == 128 ? tile * 128 : 0) + lanes;
+  const uint32_t o_base = kOut + (D == 128 ? tile * 128 : 0) + half * COLS + lanes;
+  const uint32_t swap = kSwap + lanes;
   const float sl2 = a.scale_log2;
+  bool alive = true;
+  auto wait = [&](uint32_t at, uint32_t parity) -> bool {
+    bool ok = true;
+    if (HALVES == 1) ok = tile_wait(bars, at, parity, a.status);
+    if (HALVES == 2 && alive) alive = tile_wait(bars, at, parity, a.status);
+    tc_fence_after();
+    return ok;
+  };
+  // both warps' values of a row, through tensor memory
+  auto exchange = [&](int column, float v) -> float {
+    tmem_st1(swap + column + half, v);
+    tmem_wait_st();
+    tc_fence_before();
+    pair_sync(pair);
+    tc_fence_after();
+    const float other = tmem_ld1(swap + column + 1 - half);
+    tmem_wait_ld();
+    return other;
+  };
   uint32_t count = 0;  // blocks done
-  // block n of this warp uses buffer slot_of(n), for the turn_of(n)-th time
+  // block n of this warp uses buffer slot_of(n), in the phase_of(n) of its barriers
   auto slot_of = [&](uint32_t n) -> uint32_t { return D == 128 ? (uint32_t)tile : n & 1; };
   auto phase_of = [&](uint32_t n) -> uint32_t { return (D == 128 ? n : n >> 1) & 1; };
   ItemList list;
@@ -222,46 +254,47 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, i
     const bool some = rg.b < rg.e;
     for (int j = rg.b; j < rg.e; ++j, ++count) {
       const uint32_t slot = slot_of(count);
-      if (!tile_wait(bars, kSFull + 8 * slot, phase_of(count), a.status)) return;
-      tc_fence_after();
-      float s[kKeys];
-      const uint32_t s_addr = slot * kKeys + lanes;
-      tmem_ld32(s_addr, reinterpret_cast<uint32_t *>(s));
-      tmem_ld32(s_addr + 32, reinterpret_cast<uint32_t *>(s) + 32);
-      tmem_ld16(s_addr + 64, reinterpret_cast<uint32_t *>(s) + 64);
+      if (!wait(kSFull + 8 * slot, phase_of(count))) return;
+      float s[N];
+      const uint32_t s_addr = slot * kKeys + half * N + lanes;
+      uint32_t *sr = reinterpret_cast<uint32_t *>(s);
+      tmem_ld32(s_addr, sr);
+      if (HALVES == 1) tmem_ld32(s_addr + 32, sr + 32), tmem_ld16(s_addr + 64, sr + 64);
+      if (HALVES == 2) tmem_ld8(s_addr + 32, sr + 32);
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
       if ((threadIdx.x & 31) == 0) bar_arrive(bars + kSFree + 8 * slot);
       const int k0 = j * kKeys;
       if (k0 + kKeys > hi_first || k0 < lo_last) {
-        const int h1 = hi - k0, l1 = lo - k0;
+        const int h1 = hi - k0 - half * N, l1 = lo - k0 - half * N;
 #pragma unroll
-        for (int c = 0; c < kKeys; ++c) s[c] = (c < h1 && c >= l1) ? s[c] : -INFINITY;
+        for (int c = 0; c < N; ++c) s[c] = (c < h1 && c >= l1) ? s[c] : -INFINITY;
       }
       // A row's reference is the maximum of the first block in which it sees a key.  Later blocks are
-      // weighted by it as it stands; only where a block's weights sum to more than kMost is the
+      // weighted by it as it stands; only where a half block's weights sum to more than kMost is the
       // block's maximum taken and the block done again.
-      auto find_max = [&]() {
+      auto find_max = [&]() -> float {
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < kKeys; c += 8)
+        for (int c = 0; c < N; c += 8)
 #pragma unroll
           for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], s[c + k]), s[c + 4 + k]);
-        return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const float v = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        return HALVES == 1 ? v : fmaxf(v, exchange(0, v));
       };
-      if (__any_sync(0xffffffffu, m == -INFINITY)) {
+      if (__any_sync(0xffffffffu, m == -INFINITY)) {  // the same rows, so the same answer, in both warps
         const float mx = find_max();
         if (m == -INFINITY) m = mx;
       }
       float part;
-      uint32_t p[kKeys / 2];
+      uint32_t p[N / 2];
 #pragma unroll 1
       for (bool again = false;; again = true) {
         const float neg = m == -INFINITY ? 0.f : -m * sl2;
         float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-        for (int k = 0; k < kKeys / 2; ++k) {
+        for (int k = 0; k < N / 2; ++k) {
           float2 x = fma2(make_float2(s[2 * k], s[2 * k + 1]), make_float2(sl2, sl2), make_float2(neg, neg));
           x.x = ex2(x.x);
           x.y = ex2(x.y);
@@ -269,16 +302,15 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, i
           p[k] = pack_bf16x2(x.x, x.y);
         }
         part = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        if (again || !__any_sync(0xffffffffu, part > kMost)) break;
+        if (again || !(HALVES == 1 ? __any_sync(0xffffffffu, part > kMost) : pair_any(pair, part > kMost))) break;
         const float m_new = fmaxf(m, find_max());
         const float f = m_new == -INFINITY ? 1.f : ex2((m - m_new) * sl2);
         m = m_new;
         l *= f;
         if (j > rg.b) {  // scale O, once the block before has been added to it
-          if (!tile_wait(bars, kPvDone + 8 * slot_of(count - 1), phase_of(count - 1), a.status)) return;
-          tc_fence_after();
+          if (!wait(kPvDone + 8 * slot_of(count - 1), phase_of(count - 1))) return;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = 0; c < COLS / 32; ++c) {
             uint32_t o[32];
             tmem_ld32(o_base + c * 32, o);
             tmem_wait_ld();
@@ -291,13 +323,10 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, i
       l += part;
       // P of this buffer's block before has been multiplied
       constexpr uint32_t back = D == 128 ? 1 : 2;
-      if (count >= back) {
-        if (!tile_wait(bars, kPvDone + 8 * slot, phase_of(count - back), a.status)) return;
-        tc_fence_after();
-      }
-      const uint32_t p_addr = kWeights + slot * (kKeys / 2) + lanes;
-      tmem_st32(p_addr, p);
-      tmem_st8(p_addr + 32, p + 32);
+      if (count >= back && !wait(kPvDone + 8 * slot, phase_of(count - back))) return;
+      const uint32_t p_addr = kWeights + slot * (kKeys / 2) + half * (N / 2) + lanes;
+      if (HALVES == 1) tmem_st32(p_addr, p), tmem_st8(p_addr + 32, p + 32);
+      if (HALVES == 2) tmem_st16(p_addr, p), tmem_st4(p_addr + 16, p + 16);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -305,21 +334,21 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, i
     }
     if (n <= 0) continue;
 
-    // output: this row's O / l, or the piece's (m, l, O)
+    // output: this row's O / l, or the piece's (m, l, O); half of the columns each
     const bool mine = tok < n && r < a.tq * a.g;
     const int64_t row = ((int64_t)(it.row0 + first + tok)) * a.H_q + it.h * a.g + head;
     if (some) {
-      if (!tile_wait(bars, kPvDone + 8 * slot_of(count - 1), phase_of(count - 1), a.status)) return;
-      tc_fence_after();
+      if (HALVES == 2) l += exchange(2, l);
+      if (!wait(kPvDone + 8 * slot_of(count - 1), phase_of(count - 1))) return;
     }
     const float mo = m == -INFINITY ? -INFINITY : m * sl2;  // base-2 reference
     if (it.slot >= 0) {
       // [D / 4][ROWS][4]: a warp stores 512 contiguous bytes at a time
       const int at = tile * 128 + r;
-      if (mine) *reinterpret_cast<float2 *>(a.ws_ml + ((int64_t)it.slot * 256 + at) * 2) = make_float2(mo, l);
-      float *dst = a.ws_o + (int64_t)it.slot * 32768 + at * 4;
+      if (mine && half == 0) *reinterpret_cast<float2 *>(a.ws_ml + ((int64_t)it.slot * 256 + at) * 2) = make_float2(mo, l);
+      float *dst = a.ws_o + (int64_t)it.slot * 32768 + half * COLS * ROWS + at * 4;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; c < COLS / 32; ++c) {
         uint32_t o[32];
         if (some) {
           tmem_ld32(o_base + c * 32, o);
@@ -348,9 +377,11 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, i
       } else {
         f1 = total == 0.f ? 0.f : 1.f / total;
       }
-      if (mine && a.lse) a.lse[row] = total == 0.f ? -INFINITY : (top + log2f(total)) * kTileLn2;
+      // own_lse may be lse itself: both warps read it before one writes
+      if (HALVES == 2 && PAGED && a.own_lse) pair_sync(pair);
+      if (mine && half == 0 && a.lse) a.lse[row] = total == 0.f ? -INFINITY : (top + log2f(total)) * kTileLn2;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; c < COLS / 32; ++c) {
         uint32_t o[32];
         if (some) {
           tmem_ld32(o_base + c * 32, o);
@@ -360,8 +391,9 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, i
           for (int k = 0; k < 32; ++k) o[k] = 0;
         }
         if (mine) {
-          uint16_t *dst = a.out + row * D + c * 32;
-          const uint4 *src = PAGED && f2 != 0.f ? reinterpret_cast<const uint4 *>(a.own_out + row * D + c * 32) : nullptr;
+          const int64_t at = row * D + half * COLS + c * 32;
+          uint16_t *dst = a.out + at;
+          const uint4 *src = PAGED && f2 != 0.f ? reinterpret_cast<const uint4 *>(a.own_out + at) : nullptr;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             float v[8];
@@ -657,28 +689,31 @@ __device__ __forceinline__ void load_items(const CUtensorMap *qm, const CUtensor
   }
 }
 
-// d = 128: twelve warps, 168 registers each at most; d = 256: eight, 255.
-template <int D>
-constexpr int tile_threads() {
-  return D == 128 ? 384 : 256;
-}
+constexpr int kTileThreads = 384;  // twelve warps, 168 registers each at most
 
 template <int D, bool PAGED>
-__global__ void __launch_bounds__(tile_threads<D>(), 1)
+__global__ void __launch_bounds__(kTileThreads, 1)
     tile_attn_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap km,
                      const __grid_constant__ CUtensorMap vm, const TileArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  constexpr int SW = D == 128 ? 8 : 4;  // softmax warps
+  constexpr int SW = 8;  // softmax warps
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t q_at = smem_addr(base), ring_at = q_at + kQBytes, bars = ring_at + kStages * kStageBytes;
   const int warp = threadIdx.x >> 5;
   if (warp == SW) tmem_alloc(reinterpret_cast<uint32_t *>(base + kQBytes + kStages * kStageBytes + kTmemSlot), 512);
   if (warp == SW + 2 && elect_one()) prefetch_tensormap(&qm), prefetch_tensormap(&km), prefetch_tensormap(&vm);
   if (threadIdx.x == 0) {
-    for (uint32_t at = 0; at < kTmemSlot; at += 8) bar_init(bars + at, at >= kSFree ? 4 : 1);
+    for (uint32_t at = 0; at < kTmemSlot; at += 8) bar_init(bars + at, at >= kSFree ? SW * D / 256 : 1);
     asm volatile("st.volatile.shared.s32 [%0], %1;" ::"r"(bars + kAbort), "r"(0) : "memory");
     fence_barrier_init();
   }
+  // rows behind the last whole group of heads get no query: zeros, once
+  const int spare = 128 - a.tq * a.g;
+  for (int i = threadIdx.x; i < 4 * spare * 8; i += kTileThreads) {
+    const int box = i / (spare * 8), k = i - box * spare * 8;
+    *reinterpret_cast<uint4 *>(base + box * 16384 + (128 - spare) * 128 + k * 16) = make_uint4(0, 0, 0, 0);
+  }
+  if (spare) fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -688,7 +723,7 @@ __global__ void __launch_bounds__(tile_threads<D>(), 1)
   // all 512 columns are this block's, so they start at column 0: the MMAs and the softmax
   // address them by constants
   if (warp < SW) {
-    softmax_role<D, PAGED>(a, bars, D == 128 ? warp >> 2 : 0);
+    softmax_role<D, PAGED>(a, bars, D == 128 ? warp >> 2 : 0, D == 128 ? 0 : warp >> 2);
   } else if (warp <= SW + 1) {
     if (elect_one()) {
       const bool done = warp == SW ? qk_items<D, PAGED>(a, bars, q_at, ring_at) : pv_items<D, PAGED>(a, bars, ring_at);

@@ -101,7 +101,7 @@ int launch_tiles(const char *fn, tg_stream_t stream, const tg_tile_header *hd, c
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)hd->N_CTA);
-  cfg.blockDim = dim3(tile_threads<D>());
+  cfg.blockDim = dim3(kTileThreads);
   cfg.dynamicSmemBytes = kTileSmem;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
