@@ -637,8 +637,8 @@ int tg_plan_prefill(int batch, int H, int H_q, int d, int N_CTA, const int32_t *
  *   K, V bf16 [batch][H][Nmax][d], Nmax >= every kv_len, rows [0, kv_len) of each request
  *   finite (rows behind them may hold anything); scale > 0; workspace 256-byte
  *   aligned, no initial contents (may be NULL if the plan needs none), one per stream;
- *   out bf16 [rows][H_q][d]; lse float32 [rows][H_q] (may be NULL).  q, K, V, out
- *   16-byte aligned.  batch * H and Nmax fit TMA coordinates (int32). */
+ *   out bf16 [rows][H_q][d]; lse float32 [rows][H_q] (may be NULL).  q, K, V
+ *   16-byte aligned, out 32-byte.  batch * H and Nmax fit TMA coordinates (int32). */
 int tg_prefill_attn(tg_stream_t stream, const void *plan_host, const void *plan_dev, const uint16_t *q,
                     const uint16_t *K, const uint16_t *V, int Nmax, float scale, void *workspace,
                     int64_t workspace_bytes, uint16_t *out, float *lse, int32_t *dev_status);
@@ -668,7 +668,7 @@ int tg_plan_prefix(int groups, int H, int H_q, int H_p, int P, int d, int N_CTA,
  *   tg_decode_attn's out and lse over the requests' own tokens; out and lse (may be
  *   NULL) the results, which may be the same buffers as own_out and own_lse; workspace
  *   as tg_prefill_attn.  A page id outside [0, pool_pages) sets TG_STATUS_BAD_PAGE and
- *   reads as zeros.  q, pool, own_out, out 16-byte aligned. */
+ *   reads as zeros.  q, pool and own_out 16-byte aligned, out 32-byte. */
 int tg_prefix_attn(tg_stream_t stream, const void *plan_host, const void *plan_dev, const uint16_t *q,
                    const uint16_t *pool, int64_t pool_pages, const int64_t *pt_off, const int32_t *pt_ids,
                    float scale, const uint16_t *own_out, const float *own_lse, void *workspace,

@@ -395,21 +395,21 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, i
           uint16_t *dst = a.out + at;
           const uint4 *src = PAGED && f2 != 0.f ? reinterpret_cast<const uint4 *>(a.own_out + at) : nullptr;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(o[8 * k + e]) * f1;
+          for (int k = 0; k < 2; ++k) {  // 16 columns: a whole 32-byte sector of a lane's row
+            uint32_t w[8];
             if (src) {
-              const uint4 w = src[k];
-              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                v[2 * e] += f2 * __uint_as_float(ww[e] << 16);
-                v[2 * e + 1] += f2 * __uint_as_float(ww[e] & 0xffff0000u);
-              }
+              const uint4 x = src[2 * k], y = src[2 * k + 1];
+              w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
             }
-            *reinterpret_cast<uint4 *>(dst + 8 * k) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                                 pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float v0 = __uint_as_float(o[16 * k + 2 * e]) * f1, v1 = __uint_as_float(o[16 * k + 2 * e + 1]) * f1;
+              if (src) v0 += f2 * __uint_as_float(w[e] << 16), v1 += f2 * __uint_as_float(w[e] & 0xffff0000u);
+              w[e] = pack_bf16x2(v0, v1);
+            }
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 16 * k), "r"(w[0]),
+                         "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                         : "memory");
           }
         }
       }

@@ -54,8 +54,8 @@ inline int check_tile_call(const char *fn, int kind, const void *plan_host, cons
   if (h->rows > 0 && (!q || !out)) return tgi::fail(TG_ERR_INVALID_ARG, "%s: NULL q or out", fn);
   if (!std::isfinite(scale)) return tgi::fail(TG_ERR_NONFINITE, "%s: scale is not finite", fn);
   if (scale <= 0.f) return tgi::fail(TG_ERR_INVALID_ARG, "%s: scale=%g must be positive", fn, (double)scale);
-  if (misaligned(plan_dev, 16) || misaligned(q, 16) || misaligned(out, 16) || misaligned(lse, 4))
-    return tgi::fail(TG_ERR_INVALID_ARG, "%s: plan_dev, q and out must be 16-byte aligned", fn);
+  if (misaligned(plan_dev, 16) || misaligned(q, 16) || misaligned(out, 32) || misaligned(lse, 4))
+    return tgi::fail(TG_ERR_INVALID_ARG, "%s: plan_dev and q must be 16-byte, out 32-byte aligned", fn);
   if (h->workspace_bytes > 0) {
     if (!workspace) return tgi::fail(TG_ERR_INVALID_ARG, "%s: the plan needs a workspace", fn);
     if (workspace_bytes < h->workspace_bytes)
