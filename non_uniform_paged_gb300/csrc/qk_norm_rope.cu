@@ -4,11 +4,17 @@
 // pair by the table's (cos, sin).  Every value is read once and written once: the kernel is
 // bound by memory, and for a decode step by its own latency.
 //
-// A head is d / 8 lanes of 8 values (16 bytes each way): half a warp at d = 128, a warp at
-// d = 256.  A warp takes one token and 8 steps of heads, with all 8 loads in flight before
-// the first is used, so its table row (up to 64 bytes per lane) and the norm weights are
-// loaded once per 8 (d = 256) or 16 (d = 128) heads.  Pairs (i, i + rot/2) sit rot/16 lanes
-// apart and are exchanged by shuffles; pairs (2i, 2i+1) lie in one lane.
+// A head is d / 8 lanes: half a warp at d = 128, a warp at d = 256.  A lane has two groups of 4
+// values: of the pairs (i, i + rot/2), 4 first and the 4 second values, so that a rotation needs
+// no exchange between lanes (a group of 4 is still 128 contiguous bytes over half a warp); of
+// the pairs (2i, 2i+1) and behind rot, 8 consecutive ones.  A warp takes one token and walks over
+// its heads in batches of 8 loads, each batch queries, keys or values only, the next one in
+// flight while one is worked on; the request's row and the table row are looked up once.
+// What bounds it beside memory is instructions (at 4400 a token the issue slots would take as
+// long as the bytes): the weights are multiplied into the token's rotation once a batch, and
+// the arithmetic is two values an instruction.  Where there are few tokens, a token's batches
+// go to different warps.
+#include "packed.cuh"
 #include "ptx.cuh"
 #include "tg_internal.h"
 
@@ -20,7 +26,7 @@ namespace {
 
 using namespace tgk;
 
-constexpr int kSteps = 8;     // heads in flight per lane group
+constexpr int kSteps = 8;  // loads of a batch: heads at d = 256, pairs of heads at d = 128
 constexpr int kWarps = 4;
 
 struct RopeArgs {
@@ -31,27 +37,51 @@ struct RopeArgs {
   const float *table;
   uint16_t *q, *K, *V;
   int32_t *status;
-  int batch, T, H_q, H, Nmax, rot, max_pos, chunks;
+  int batch, T, H_q, H, Nmax, rot, max_pos;
+  int q_batches, kv_batches;  // batches of the query heads, and of the key (and of the value) heads
+  int split;                  // 1: every batch has a warp of its own
   float eps;
 };
 
+struct Head8 {  // a lane's 8 values of a head
+  uint2 a, b;
+};
+
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+
 template <int D, bool PAIRS>
-__global__ void __launch_bounds__(kWarps * 32) qk_norm_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 4) qk_norm_rope_kernel(const RopeArgs a) {
   constexpr int LANES = D / 8, PER = 32 / LANES;  // lanes of a head, heads side by side
   const int lane = threadIdx.x & 31, sub = lane % LANES, side = lane / LANES;
+  const int all = a.q_batches + 2 * a.kv_batches;
   const int64_t task = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int t = (int)(task / a.chunks);
-  const int head0 = (int)(task - (int64_t)t * a.chunks) * kSteps * PER + side;
-  if (t >= a.T) return;
-  const int heads = a.H_q + 2 * a.H;
-  // the loads do not wait for the request's lookup
-  uint4 raw[kSteps];
-  const uint16_t *src = a.qkv + (int64_t)t * a.stride + sub * 8;
+  const int t = a.split ? (int)(task / all) : (int)task;
+  if (task >= (a.split ? (int64_t)a.T * all : (int64_t)a.T)) return;
+  const int first = a.split ? (int)(task - (int64_t)t * all) : 0, last = a.split ? first + 1 : all;
+  // the two groups of this lane
+  const bool turned = sub * 8 < a.rot;
+  const int ga = !PAIRS && turned ? sub * 4 : sub * 8, gb = !PAIRS && turned ? sub * 4 + a.rot / 2 : sub * 8 + 4;
+  const uint16_t *src = a.qkv + (int64_t)t * a.stride;
+  // batch k: kind (0 queries, 1 keys, 2 values), first head of its kind, heads of its kind
+  auto kind_of = [&](int k) { return k < a.q_batches ? 0 : k < a.q_batches + a.kv_batches ? 1 : 2; };
+  auto head_of = [&](int k, int kind) {
+    return (k - (kind == 0 ? 0 : kind == 1 ? a.q_batches : a.q_batches + a.kv_batches)) * kSteps * PER;
+  };
+  auto load = [&](Head8 *x, int k) {
+    const int kind = kind_of(k), h0 = head_of(k, kind) + side, n = kind == 0 ? a.H_q : a.H;
+    const uint16_t *p = src + ((kind == 0 ? 0 : kind == 1 ? a.H_q : a.H_q + a.H) + h0) * D;
 #pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    const int h = head0 + s * PER;
-    raw[s] = h < heads ? __ldcs(reinterpret_cast<const uint4 *>(src + h * D)) : make_uint4(0, 0, 0, 0);
-  }
+    for (int s = 0; s < kSteps; ++s) {
+      if (h0 + s * PER < n) {
+        x[s].a = __ldcs(reinterpret_cast<const uint2 *>(p + s * PER * D + ga));
+        x[s].b = __ldcs(reinterpret_cast<const uint2 *>(p + s * PER * D + gb));
+      }
+    }
+  };
+  Head8 x0[kSteps] = {}, x1[kSteps] = {};
+  load(x0, first);  // does not wait for the request's lookup
   // the request: how many end at or before t
   int b = 0;
   for (int i = 0; i < a.batch; i += 32) {
@@ -67,76 +97,89 @@ __global__ void __launch_bounds__(kWarps * 32) qk_norm_rope_kernel(const RopeArg
     if (lane == 0) report(a.status, TG_STATUS_BAD_INPUT);
     return;
   }
-  // this lane's rotation: pair indices [i0, i0 + 8) (or 4 pairs), identity behind rot
-  const bool turned = sub * 8 < a.rot;
-  float c[8], sn[8];
-  int partner = lane;
+  // this lane's four pairs
+  float c[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
   if (turned) {
-    const float *tb = a.table + pos * a.rot;  // [rot/2][2]
-    if (PAIRS) {
-      const float4 *p = reinterpret_cast<const float4 *>(tb + sub * 8);
+    const float4 *p = reinterpret_cast<const float4 *>(a.table + pos * a.rot + sub * 8);  // [rot/2][2]
+    const float4 u = __ldg(p), v = __ldg(p + 1);
+    c[0] = u.x, sn[0] = u.y, c[1] = u.z, sn[1] = u.w, c[2] = v.x, sn[2] = v.y, c[3] = v.z, sn[3] = v.w;
+  }
+  const int64_t kv_row = ((int64_t)b * a.H * a.Nmax + row) * D, kv_head = (int64_t)a.Nmax * D;
+
+  auto work = [&](const Head8 *in, int k) {
+    const int kind = kind_of(k), h0 = head_of(k, kind) + side, n = kind == 0 ? a.H_q : a.H;
+    const int64_t step = kind == 0 ? PER * D : PER * kv_head;
+    uint16_t *dst = kind == 0 ? a.q + ((int64_t)t * a.H_q + h0) * D : (kind == 1 ? a.K : a.V) + kv_row + h0 * kv_head;
+    if (kind == 2) {
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s, dst += step) {
+        if (h0 + s * PER < n) {
+          *reinterpret_cast<uint2 *>(dst + ga) = in[s].a;
+          *reinterpret_cast<uint2 *>(dst + gb) = in[s].b;
+        }
+      }
+      return;
+    }
+    // z_u = uc x_u - vs x_v, z_v = vc x_v + us x_u, the weights multiplied in; u, v: a lane's first and
+    // second values of its pairs
+    const float *w = kind == 0 ? a.qw : a.kw;
+    float wu[4] = {1.f, 1.f, 1.f, 1.f}, wv[4] = {1.f, 1.f, 1.f, 1.f};
+    if (w) {
+      const float4 p = __ldg(reinterpret_cast<const float4 *>(w + ga)), q = __ldg(reinterpret_cast<const float4 *>(w + gb));
+      const float e[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) wu[i] = e[PAIRS ? 2 * i : i], wv[i] = e[PAIRS ? 2 * i + 1 : i + 4];
+    }
+    float2 uc[2], us[2], vc[2], vs[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 cc = {c[2 * i], c[2 * i + 1]}, ss = {sn[2 * i], sn[2 * i + 1]};
+      const float2 u = {wu[2 * i], wu[2 * i + 1]}, v = {wv[2 * i], wv[2 * i + 1]};
+      uc[i] = mul2(u, cc), us[i] = mul2(u, ss), vc[i] = mul2(v, cc), vs[i] = mul2(v, make_float2(-ss.x, -ss.y));
+    }
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s, dst += step) {
+      if (h0 - side + s * PER >= n) break;
+      const float2 x[4] = {unpack2(in[s].a.x), unpack2(in[s].a.y), unpack2(in[s].b.x), unpack2(in[s].b.y)};
+      float2 xu[2], xv[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float4 v = __ldg(p + i);
-        c[4 * i] = c[4 * i + 1] = v.x, c[4 * i + 2] = c[4 * i + 3] = v.z;
-        sn[4 * i] = -v.y, sn[4 * i + 1] = v.y, sn[4 * i + 2] = -v.w, sn[4 * i + 3] = v.w;
+        xu[i] = PAIRS ? make_float2(x[2 * i].x, x[2 * i + 1].x) : x[i];
+        xv[i] = PAIRS ? make_float2(x[2 * i].y, x[2 * i + 1].y) : x[i + 2];
       }
-    } else {
-      const int half = a.rot / 16;  // lanes of half a rotation
-      const bool low = sub < half;
-      partner = low ? lane + half : lane - half;
-      const float4 *p = reinterpret_cast<const float4 *>(tb + (low ? sub : sub - half) * 16);
+      float2 zu[2], zv[2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 v = __ldg(p + i);
-        c[2 * i] = v.x, c[2 * i + 1] = v.z;
-        sn[2 * i] = low ? -v.y : v.y, sn[2 * i + 1] = low ? -v.w : v.w;
+      for (int i = 0; i < 2; ++i) zu[i] = fma2(vs[i], xv[i], mul2(uc[i], xu[i])), zv[i] = fma2(us[i], xu[i], mul2(vc[i], xv[i]));
+      if (w) {
+        float2 sq = mul2(xu[0], xu[0]);
+        sq = fma2(xu[1], xu[1], sq), sq = fma2(xv[0], xv[0], sq), sq = fma2(xv[1], xv[1], sq);
+        float ss = sq.x + sq.y;
+#pragma unroll
+        for (int d = LANES / 2; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+        const float f = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+        const float2 ff = {f, f};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) zu[i] = mul2(zu[i], ff), zv[i] = mul2(zv[i], ff);
       }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = 1.f, sn[i] = 0.f;
-  }
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    const int h = head0 + s * PER;
-    const bool is_q = h < a.H_q, is_v = h >= a.H_q + a.H;
-    const float *w = is_q ? a.qw : a.kw;
-    const uint32_t in[4] = {raw[s].x, raw[s].y, raw[s].z, raw[s].w};
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(in[i] << 16), x[2 * i + 1] = __uint_as_float(in[i] & 0xffff0000u);
-    if (a.qw || a.kw) {
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-      for (int d = LANES / 2; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-      if (w && !is_v) {
-        const float f = rsqrtf(ss * (1.f / D) + a.eps);
-        const float4 w0 = __ldg(reinterpret_cast<const float4 *>(w + sub * 8));
-        const float4 w1 = __ldg(reinterpret_cast<const float4 *>(w + sub * 8 + 4));
-        x[0] *= f * w0.x, x[1] *= f * w0.y, x[2] *= f * w0.z, x[3] *= f * w0.w;
-        x[4] *= f * w1.x, x[5] *= f * w1.y, x[6] *= f * w1.z, x[7] *= f * w1.w;
+      if (h0 + s * PER >= n) continue;
+      Head8 o;
+      if (PAIRS) {
+        o.a = make_uint2(pack_bf16x2(zu[0].x, zv[0].x), pack_bf16x2(zu[0].y, zv[0].y));
+        o.b = make_uint2(pack_bf16x2(zu[1].x, zv[1].x), pack_bf16x2(zu[1].y, zv[1].y));
+      } else {
+        o.a = make_uint2(pack_bf16x2(zu[0].x, zu[0].y), pack_bf16x2(zu[1].x, zu[1].y));
+        o.b = make_uint2(pack_bf16x2(zv[0].x, zv[0].y), pack_bf16x2(zv[1].x, zv[1].y));
       }
+      *reinterpret_cast<uint2 *>(dst + ga) = o.a;
+      *reinterpret_cast<uint2 *>(dst + gb) = o.b;
     }
-    float z[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float other = PAIRS ? x[i ^ 1] : __shfl_sync(0xffffffffu, x[i], partner);
-      z[i] = turned ? fmaf(other, sn[i], x[i] * c[i]) : x[i];
-    }
-    if (h >= heads) continue;
-    uint4 v = make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]), pack_bf16x2(z[6], z[7]));
-    uint16_t *dst;
-    if (is_q) {
-      dst = a.q + ((int64_t)t * a.H_q + h) * D;
-    } else {
-      const int hk = is_v ? h - a.H_q - a.H : h - a.H_q;
-      dst = (is_v ? a.V : a.K) + (((int64_t)b * a.H + hk) * a.Nmax + row) * D;
-      if (is_v) v = raw[s];
-    }
-    *reinterpret_cast<uint4 *>(dst + sub * 8) = v;
+  };
+  for (int k = first; k < last; k += 2) {
+    if (k + 1 < last) load(x1, k + 1);
+    work(x0, k);
+    if (k + 1 >= last) break;
+    if (k + 2 < last) load(x0, k + 2);
+    work(x1, k + 1);
   }
 }
 
@@ -173,9 +216,13 @@ extern "C" int tg_qk_norm_rope(tg_stream_t stream, int batch, int T, int H_q, in
   a.cu_q = cu_q, a.start = start, a.positions = positions, a.qkv = qkv, a.stride = qkv_stride;
   a.qw = q_weight, a.kw = k_weight, a.table = cos_sin, a.q = q, a.K = K, a.V = V, a.status = dev_status;
   a.batch = batch, a.T = T, a.H_q = H_q, a.H = H, a.Nmax = Nmax, a.rot = rot, a.max_pos = max_pos, a.eps = eps;
+  // one warp a token, or, below 4096 tokens (27 warps for each of 152 SMs), one for each of its batches
   const int per = kSteps * (d == 128 ? 2 : 1);
-  a.chunks = (int)((heads + per - 1) / per);
-  const int64_t blocks = ((int64_t)T * a.chunks + kWarps - 1) / kWarps;
+  a.q_batches = (H_q + per - 1) / per;
+  a.kv_batches = (H + per - 1) / per;
+  a.split = T < 4096;
+  const int64_t tasks = (int64_t)T * (a.split ? a.q_batches + 2 * a.kv_batches : 1);
+  const int64_t blocks = (tasks + kWarps - 1) / kWarps;
   if (blocks > INT32_MAX) return fail(TG_ERR_SHAPE, "%s: T=%d with %lld heads", fn, T, (long long)heads);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool pairs = flags & TG_ROPE_PAIRS;
