@@ -59,7 +59,7 @@ struct TileArgs {
   float *lse;
   const uint16_t *own_out;
   const float *own_lse;
-  float *ws_ml, *ws_o;
+  float *ws_ml, *ws_own, *ws_o;
   const int64_t *pt_off;
   const int32_t *pt_ids;
   int64_t pool_pages;
@@ -345,7 +345,11 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, i
     if (it.slot >= 0) {
       // [D / 4][ROWS][4]: a warp stores 512 contiguous bytes at a time
       const int at = tile * 128 + r;
-      if (mine && half == 0) *reinterpret_cast<float2 *>(a.ws_ml + ((int64_t)it.slot * 256 + at) * 2) = make_float2(mo, l);
+      if (mine && half == 0) {
+        *reinterpret_cast<float2 *>(a.ws_ml + ((int64_t)it.slot * 256 + at) * 2) = make_float2(mo, l);
+        // kept for the merge, whose blocks may write lse over own_lse
+        if (PAGED && a.own_lse) a.ws_own[(int64_t)it.slot * 256 + at] = a.own_lse[row];
+      }
       float *dst = a.ws_o + (int64_t)it.slot * 32768 + half * COLS * ROWS + at * 4;
 #pragma unroll 1
       for (int c = 0; c < COLS / 32; ++c) {
@@ -720,6 +724,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   // Launched as the programmatic dependent of the kernel before it: what came so far overlapped that
   // kernel's end; everything from here may read what it wrote.
   griddep_wait();
+  // the merge may be set up from now on; its blocks find room when this kernel's leave
+  if (a.signal) griddep_launch_dependents();
   // all 512 columns are this block's, so they start at column 0: the MMAs and the softmax
   // address them by constants
   if (warp < SW) {
@@ -741,7 +747,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (a.signal) griddep_launch_dependents();
   tc_fence_after();
   if (warp == SW) tmem_free(0, 512);
 }
@@ -749,67 +754,71 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // ------------------------------------------------------------------ merge of cut runs
 struct MergeArgs {
   const tg_tile_merge *merges;
-  const float *ws_ml, *ws_o;
+  const float *ws_ml, *ws_own, *ws_o;
   uint16_t *out;
   float *lse;
-  const uint16_t *own_out;
-  const float *own_lse;
+  const uint16_t *own_out;  // NULL: nothing to merge with
   int H_q, g, tq;
 };
 
 constexpr int kMergeThreads = 128;
-// blocks of one merge: 32 rows x 32 columns each
-constexpr int merge_blocks(int d) { return (32768 / d / 32) * (d / 32); }
+// blocks of one merge: 32 rows x 16 columns each
+constexpr int merge_blocks(int d) { return (32768 / d / 32) * (d / 16); }
 
 // out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p over the pieces (and the request's own result).
-// A lane is a row and a warp 8 columns, so every load of a piece is 512 contiguous bytes; the
-// pieces, written just before, come out of L2.
+// A lane is a row and a warp 4 columns, so every load of a piece is 512 contiguous bytes.  What
+// counts is latency: eight pieces' (m, l) and O are loaded together, and joined to what came before
+// by their own maximum, so that a run of up to eight pieces waits for memory once.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) tile_merge_kernel(const MergeArgs a) {
-  constexpr int ROWS = 32768 / D, COLS = D / 32;
-  griddep_wait();
+  constexpr int ROWS = 32768 / D, COLS = D / 16, AT_ONCE = 8;
+  // the plan is there: the kernel before let this one start after it had waited for its own
   const tg_tile_merge mg = a.merges[blockIdx.x / merge_blocks(D)];
   const int chunk = blockIdx.x % merge_blocks(D);
   const int at = (chunk / COLS) * 32 + (threadIdx.x & 31);            // row of the slot
-  const int c8 = (chunk % COLS) * 4 + (threadIdx.x >> 5);             // which 8 columns
+  const int c4 = (chunk % COLS) * 4 + (threadIdx.x >> 5);             // which 4 columns
   const int tile = at >> 7, r = at & 127, tok = r / a.g, head = r - tok * a.g;
   const int n = min(mg.nrow - tile * a.tq, a.tq);
-  if (!__any_sync(0xffffffffu, tok < n)) return;
   const bool mine = tok < n && r < a.tq * a.g;
   const int64_t row = (int64_t)(mg.row0 + tile * a.tq + tok) * a.H_q + mg.h * a.g + head;
-  const float2 *ml = reinterpret_cast<const float2 *>(a.ws_ml) + (int64_t)mg.slot0 * 256 + at;
-  const float4 *po = reinterpret_cast<const float4 *>(a.ws_o) + (int64_t)mg.slot0 * 8192 + c8 * 2 * ROWS + at;
+  griddep_wait();
   if (!mine) return;
-  const float w = a.own_lse ? a.own_lse[row] * kTileLog2e : -INFINITY;
-  float M = w;
-#pragma unroll 8
-  for (int p = 0; p < mg.nparts; ++p) M = fmaxf(M, __ldcg(&ml[p * 256].x));
-  float o[8] = {}, total = 0.f;
-#pragma unroll 8
-  for (int p = 0; p < mg.nparts; ++p) {
-    const float2 v = __ldcg(ml + p * 256);
-    const float4 x = __ldcg(po + (int64_t)p * 8192), y = __ldcg(po + (int64_t)p * 8192 + ROWS);
-    const float f = v.x == -INFINITY ? 0.f : ex2(v.x - M);
-    total += f * v.y;
-    o[0] += f * x.x, o[1] += f * x.y, o[2] += f * x.z, o[3] += f * x.w;
-    o[4] += f * y.x, o[5] += f * y.y, o[6] += f * y.z, o[7] += f * y.w;
-  }
-  const float e2 = w == -INFINITY ? 0.f : ex2(w - M);
-  total += e2;
-  const float inv = total == 0.f ? 0.f : 1.f / total;
-  if (e2 != 0.f) {
-    const uint4 v = *reinterpret_cast<const uint4 *>(a.own_out + row * D + c8 * 8);
-    const uint32_t vv[4] = {v.x, v.y, v.z, v.w};
+  const float2 *ml = reinterpret_cast<const float2 *>(a.ws_ml) + (int64_t)mg.slot0 * 256 + at;
+  const float4 *po = reinterpret_cast<const float4 *>(a.ws_o) + (int64_t)mg.slot0 * 8192 + c4 * ROWS + at;
+  const float w = a.own_out ? __ldcg(a.ws_own + (int64_t)mg.slot0 * 256 + at) * kTileLog2e : -INFINITY;
+  uint2 own = make_uint2(0, 0);
+  if (a.own_out) own = *reinterpret_cast<const uint2 *>(a.own_out + row * D + c4 * 4);
+  float M = w, total = w == -INFINITY ? 0.f : 1.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (total != 0.f)
+    o = make_float4(__uint_as_float(own.x << 16), __uint_as_float(own.x & 0xffff0000u), __uint_as_float(own.y << 16),
+                    __uint_as_float(own.y & 0xffff0000u));
+  for (int p0 = 0; p0 < mg.nparts; p0 += AT_ONCE) {
+    float2 v[AT_ONCE];
+    float4 x[AT_ONCE];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      o[2 * e] += e2 * __uint_as_float(vv[e] << 16);
-      o[2 * e + 1] += e2 * __uint_as_float(vv[e] & 0xffff0000u);
+    for (int p = 0; p < AT_ONCE; ++p) {
+      const int k = min(p0 + p, mg.nparts - 1);
+      v[p] = __ldcg(ml + k * 256);
+      x[p] = __ldcg(po + (int64_t)k * 8192);
+      if (p0 + p >= mg.nparts) v[p].x = -INFINITY;
+    }
+    float top = M;
+#pragma unroll
+    for (int p = 0; p < AT_ONCE; ++p) top = fmaxf(top, v[p].x);
+    const float f0 = M == -INFINITY ? 0.f : ex2(M - top);
+    M = top;
+    total *= f0, o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
+#pragma unroll
+    for (int p = 0; p < AT_ONCE; ++p) {
+      const float f = v[p].x == -INFINITY ? 0.f : ex2(v[p].x - top);
+      if (f != 0.f) total += f * v[p].y, o.x += f * x[p].x, o.y += f * x[p].y, o.z += f * x[p].z, o.w += f * x[p].w;
     }
   }
-  *reinterpret_cast<uint4 *>(a.out + row * D + c8 * 8) =
-      make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
-                 pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
-  if (c8 == 0 && a.lse) a.lse[row] = total == 0.f ? -INFINITY : (M + log2f(total)) * kTileLn2;
+  const float inv = total == 0.f ? 0.f : 1.f / total;
+  *reinterpret_cast<uint2 *>(a.out + row * D + c4 * 4) =
+      make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  if (c4 == 0 && a.lse) a.lse[row] = total == 0.f ? -INFINITY : (M + log2f(total)) * kTileLn2;
 }
 
 }  // namespace tgk

@@ -44,8 +44,9 @@ inline
   return r;
 }
 
-// workspace: m, l float32 [slots][256][2] | o float32 [slots][d / 4][32768 / d rows][4]
-constexpr int64_t kSlotMl = 256 * 2 * 4;
+// workspace: m, l float32 [slots][256][2] | own lse float32 [slots][256] |
+// o float32 [slots][d / 4][32768 / d rows][4]
+constexpr int64_t kSlotMl = 256 * 3 * 4;
 constexpr int64_t kSlotO = 32768 * 4;
 
 }  // namespace tgi

@@ -75,9 +75,12 @@ inline TileArgs tile_args(const tg_tile_header *hd, const void *plan_dev, float 
   a.items = reinterpret_cast<const tg_tile_item *>(pd + hd->items);
   a.out = out;
   a.lse = lse;
-  a.ws_ml = static_cast<float *>(workspace);
-  a.ws_o = hd->n_slots ? reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + hd->n_slots * tgi::kSlotMl)
-                       : nullptr;
+  if (hd->n_slots) {
+    float *ws = static_cast<float *>(workspace);
+    a.ws_ml = ws;
+    a.ws_own = ws + (int64_t)hd->n_slots * 512;
+    a.ws_o = ws + (int64_t)hd->n_slots * 768;
+  }
   a.status = status;
   a.H = hd->H;
   a.H_q = hd->H_q;
@@ -111,8 +114,8 @@ int launch_tiles(const char *fn, tg_stream_t stream, const tg_tile_header *hd, c
   if (!hd->n_merge) return tgi::ok();
   MergeArgs m;
   m.merges = reinterpret_cast<const tg_tile_merge *>(static_cast<const uint8_t *>(plan_dev) + hd->merges);
-  m.ws_ml = a.ws_ml, m.ws_o = a.ws_o, m.out = a.out, m.lse = a.lse;
-  m.own_out = a.own_out, m.own_lse = a.own_lse;
+  m.ws_ml = a.ws_ml, m.ws_own = a.ws_own, m.ws_o = a.ws_o, m.out = a.out, m.lse = a.lse;
+  m.own_out = a.own_out;
   m.H_q = a.H_q, m.g = a.g, m.tq = a.tq;
   cfg.gridDim = dim3((unsigned)(hd->n_merge * merge_blocks(D)));
   cfg.blockDim = dim3(kMergeThreads);

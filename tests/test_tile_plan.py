@@ -27,7 +27,7 @@ def _check_plan(lib, plan, ws, want, tq, tiles, window, causal):
     lead, items = lib.tile_items(plan)
     assert hd["plan_bytes"] == plan.size and hd["workspace_bytes"] == ws
     assert 1 <= hd["N_CTA"] <= max(1, hd["n_items"]) and items.size == hd["n_items"]
-    assert ws == hd["n_slots"] * (256 * 8 + 32768 * 4)
+    assert ws == hd["n_slots"] * (256 * 12 + 32768 * 4)
     at = 0
     for c in range(hd["N_CTA"]):
         assert tuple(lead[c]["reserved"]) [1] == at
