@@ -2,7 +2,7 @@
 
 Argument marshalling only: every function below has the name of the C entry
 point it calls (include/tg.h), turns numpy arrays / torch tensors into
-pointers, allocates host-side outputs of the planning calls, and raises
+pointers (in _calls, a compiled module, where the host's time counts), allocates host-side outputs of the planning calls, and raises
 ``TGError`` when the C call returns an error.  All device work runs in the
 library's CUDA kernels; nothing here computes a result itself.  There is no
 fallback: if libtg.so cannot be built or loaded, the import of a function
@@ -505,38 +505,28 @@ class PageAllocator:
 
 
 # ------------------------------------------------------------------ prompt side and shared prefixes
-# These calls sit on the latency path of a decode step, so their checks are lean: one pass per tensor.
+# These calls sit on the latency path of a decode step, where the host's time counts: the compiled
+# module _calls checks their tensors and makes the call.
 
-def _arg(t, dtype, shape, name, dev):
-    """Pointer of a contiguous tensor of that type and shape on device `dev`."""
-    try:
-        at = t.get_device()
-    except AttributeError:
-        raise TypeError(f"{name} must be a CUDA torch.Tensor") from None
-    if at != dev:
-        if at < 0:
-            raise TypeError(f"{name} must be a CUDA torch.Tensor")
-        raise ValueError(f"{name} is on cuda:{at}, the current device is cuda:{dev}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+_fast = None
 
 
-def _opt(t, dtype, shape, name, dev):
-    return None if t is None else _arg(t, dtype, shape, name, dev)
+def _setup():
+    """(current device, its current stream, _calls), looked up once."""
+    global _fast
+    if _fast is None:
+        import torch
+        torch.cuda.init()
+        lib = load()
+        from . import _calls
+        _calls.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
+                      for n in ("tg_qk_norm_rope", "tg_prefill_attn", "tg_prefix_attn")))
+        _fast = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, _calls)
+    return _fast
 
 
-def _where(stream):
-    """(torch, current device, stream handle); the library launches on the current device."""
-    import torch
-    dev = torch.cuda.current_device()
-    if stream is None:
-        return torch, dev, torch._C._cuda_getCurrentRawStream(dev)
-    return torch, dev, stream if isinstance(stream, int) else stream.cuda_stream
+def _raw_stream(stream):
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def tg_qk_norm_rope(qkv, cu_q, start, cos_sin, q, K, V, q_weight=None, k_weight=None, eps=1e-6, pairs=False,
@@ -544,30 +534,12 @@ def tg_qk_norm_rope(qkv, cu_q, start, cos_sin, q, K, V, q_weight=None, k_weight=
     """RMS norm and rotation of queries and keys, and placement of K and V rows (tg.h:
     tg_qk_norm_rope).  qkv [T][H_q + 2H][d] (rows may be strided), q [T][H_q][d],
     K, V [batch][H][Nmax][d], cos_sin [max_pos][rot/2][2] (None: no rotation)."""
-    torch, dev, stream = _where(stream)
-    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
-    try:
-        T, H_q, d = q.shape
-        batch, H, Nmax, _ = K.shape
-        max_pos, half, two = (0, 0, 2) if cos_sin is None else cos_sin.shape
-    except (AttributeError, ValueError):
-        raise ValueError("q must be [T][H_q][d], K [batch][H][Nmax][d] and cos_sin [max_pos][rot/2][2] tensors") from None
-    heads = H_q + 2 * H
-    if qkv.shape != (T, heads, d) or two != 2:
-        raise ValueError(f"qkv has shape {tuple(qkv.shape)}, not {(T, heads, d)}" if two == 2 else "cos_sin must end in 2")
-    if qkv.dtype is not bf16 or qkv.get_device() != dev:
-        raise TypeError(f"qkv must be a bfloat16 tensor on cuda:{dev}")
-    stride, inner, last = qkv.stride()
-    if T and (inner != d or last != 1):
-        raise ValueError("qkv must have contiguous token rows")
-    _check(load().tg_qk_norm_rope(
-        stream, batch, T, H_q, H, d, Nmax, 2 * half, max_pos, ROPE_PAIRS if pairs else 0,
-        _arg(cu_q, i32, (batch + 1,), "cu_q", dev), _arg(start, i32, (batch,), "start", dev), qkv.data_ptr(),
-        stride if T > 1 else heads * d, _opt(q_weight, f32, (d,), "q_weight", dev),
-        _opt(k_weight, f32, (d,), "k_weight", dev), eps, _opt(positions, i32, (T,), "positions", dev),
-        _opt(cos_sin, f32, None, "cos_sin", dev), _arg(q, bf16, None, "q", dev),
-        _arg(K, bf16, (batch, H, Nmax, d), "K", dev), _arg(V, bf16, K.shape, "V", dev),
-        _opt(dev_status, i32, None, "dev_status", dev)))
+    device, current, calls = _fast or _setup()
+    dev = device()
+    rc = calls.qk_norm_rope(current(dev) if stream is None else _raw_stream(stream), dev, qkv, cu_q, start, cos_sin, q, K,
+                            V, q_weight, k_weight, eps, pairs, positions, dev_status)
+    if rc:
+        _check(rc)
 
 
 def _tile_plan(call):
@@ -640,56 +612,43 @@ class TilePlan:
         if hd["plan_bytes"] != plan.size:
             raise ValueError(f"plan has {plan.size} bytes, its header says {hd['plan_bytes']}")
         import torch
-        self._host, self.plan_dev, self._at = plan, plan_dev, plan_dev.get_device()
-        self.host_ptr, self.dev_ptr = plan.ctypes.data, _arg(plan_dev, torch.uint8, (plan.size,), "plan_dev", self._at)
-        if self._at < 0:
-            raise TypeError("plan_dev must be a CUDA torch.Tensor")
+        self.dev_ptr = _dev(plan_dev, torch.uint8, "plan_dev")
+        if plan_dev is None or plan_dev.numel() != plan.size:
+            raise ValueError(f"plan_dev must hold the plan's {plan.size} bytes")
+        self._host, self.plan_dev, self.device = plan, plan_dev, plan_dev.get_device()
+        self.host_ptr = plan.ctypes.data
         self.header = hd
-        self.q_shape = (hd["rows"], hd["H_q"], hd["d"])
-        self.kv_lead = (hd["batch"], hd["H"])
-        self.lists = hd["groups"] * (hd["H"] // max(1, hd["H_p"])) + 1
-        self.page_values = hd["H_p"] * 2 * hd["P"] * hd["d"]
 
-    def pointers(self, dev):
-        if self._at != dev:
-            raise ValueError(f"the plan is on cuda:{self._at}, the current device is cuda:{dev}")
-        return self.host_ptr, self.dev_ptr
+
+def _plan_elsewhere(plan, dev):
+    return ValueError(f"the plan is on cuda:{plan.device}, the current device is cuda:{dev}")
 
 
 def tg_prefill_attn(plan: TilePlan, q, K, V, scale: float, out, lse=None, workspace=None, dev_status=None, stream=None):
     """Causal attention of a packed prefill pass (tg.h: tg_prefill_attn); asynchronous.
     q, out [rows][H_q][d], K, V [batch][H][Nmax][d], lse [rows][H_q]."""
-    torch, dev, stream = _where(stream)
-    bf16 = torch.bfloat16
-    ph, pd = plan.pointers(dev)
-    shape = plan.q_shape
-    kv = K.shape
-    if len(kv) != 4 or kv[:2] != plan.kv_lead or kv[3] != shape[2]:
-        raise ValueError(f"K has shape {tuple(kv)}, not [batch][H][Nmax][d] = {plan.kv_lead} x [Nmax] x {shape[2]}")
-    _check(load().tg_prefill_attn(
-        stream, ph, pd, _arg(q, bf16, shape, "q", dev), _arg(K, bf16, None, "K", dev), _arg(V, bf16, kv, "V", dev), kv[2],
-        scale, _opt(workspace, torch.uint8, None, "workspace", dev), 0 if workspace is None else workspace.numel(),
-        _arg(out, bf16, shape, "out", dev), _opt(lse, torch.float32, shape[:2], "lse", dev),
-        _opt(dev_status, torch.int32, None, "dev_status", dev)))
+    device, current, calls = _fast or _setup()
+    dev = device()
+    if plan.device != dev:
+        raise _plan_elsewhere(plan, dev)
+    rc = calls.prefill_attn(current(dev) if stream is None else _raw_stream(stream), dev, plan.host_ptr, plan.dev_ptr, q, K,
+                            V, scale, out, lse, workspace, dev_status)
+    if rc:
+        _check(rc)
 
 
 def tg_prefix_attn(plan: TilePlan, q, pool, pool_pages: int, pt_off, pt_ids, scale: float, out, lse=None, own_out=None,
                    own_lse=None, workspace=None, dev_status=None, stream=None):
     """Decode attention over a shared prefix, merged with the requests' own results (tg.h:
     tg_prefix_attn); asynchronous.  q, out, own_out [batch][H_q][d], lse, own_lse [batch][H_q]."""
-    torch, dev, stream = _where(stream)
-    bf16, f32 = torch.bfloat16, torch.float32
-    ph, pd = plan.pointers(dev)
-    shape = plan.q_shape
-    if pool.numel() < pool_pages * plan.page_values:
-        raise ValueError(f"pool holds {pool.numel()} values, fewer than {pool_pages} pages")
-    _check(load().tg_prefix_attn(
-        stream, ph, pd, _arg(q, bf16, shape, "q", dev), _arg(pool, bf16, None, "pool", dev), pool_pages,
-        _arg(pt_off, torch.int64, (plan.lists,), "pt_off", dev), _arg(pt_ids, torch.int32, None, "pt_ids", dev), scale,
-        _opt(own_out, bf16, shape, "own_out", dev), _opt(own_lse, f32, shape[:2], "own_lse", dev),
-        _opt(workspace, torch.uint8, None, "workspace", dev), 0 if workspace is None else workspace.numel(),
-        _arg(out, bf16, shape, "out", dev), _opt(lse, f32, shape[:2], "lse", dev),
-        _opt(dev_status, torch.int32, None, "dev_status", dev)))
+    device, current, calls = _fast or _setup()
+    dev = device()
+    if plan.device != dev:
+        raise _plan_elsewhere(plan, dev)
+    rc = calls.prefix_attn(current(dev) if stream is None else _raw_stream(stream), dev, plan.host_ptr, plan.dev_ptr, q,
+                           pool, pool_pages, pt_off, pt_ids, scale, own_out, own_lse, out, lse, workspace, dev_status)
+    if rc:
+        _check(rc)
 
 
 def tg_check_status(dev_status) -> int:

@@ -767,11 +767,11 @@ constexpr int merge_blocks(int d) { return (32768 / d / 32) * (d / 16); }
 
 // out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p over the pieces (and the request's own result).
 // A lane is a row and a warp 4 columns, so every load of a piece is 512 contiguous bytes.  What
-// counts is latency: eight pieces' (m, l) and O are loaded together, and joined to what came before
-// by their own maximum, so that a run of up to eight pieces waits for memory once.
+// counts is latency: ten pieces' (m, l) and O are loaded together, and joined to what came before
+// by their own maximum, so that a run of up to ten pieces waits for memory once.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) tile_merge_kernel(const MergeArgs a) {
-  constexpr int ROWS = 32768 / D, COLS = D / 16, AT_ONCE = 8;
+  constexpr int ROWS = 32768 / D, COLS = D / 16, AT_ONCE = 10;
   // the plan is there: the kernel before let this one start after it had waited for its own
   const tg_tile_merge mg = a.merges[blockIdx.x / merge_blocks(D)];
   const int chunk = blockIdx.x % merge_blocks(D);
