@@ -80,6 +80,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) qk_norm_rope_kernel(const Rope
       }
     }
   };
+  griddep_wait();  // a programmatic dependent of the kernel before it: set up while that one ends
   Head8 x0[kSteps] = {}, x1[kSteps] = {};
   load(x0, first);  // does not wait for the request's lookup
   // the request: how many end at or before t
@@ -226,15 +227,19 @@ extern "C" int tg_qk_norm_rope(tg_stream_t stream, int batch, int T, int H_q, in
   if (blocks > INT32_MAX) return fail(TG_ERR_SHAPE, "%s: T=%d with %lld heads", fn, T, (long long)heads);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool pairs = flags & TG_ROPE_PAIRS;
-  const dim3 grid((unsigned)blocks), block(kWarps * 32);
-  if (d == 128) {
-    if (pairs) qk_norm_rope_kernel<128, true><<<grid, block, 0, s>>>(a);
-    else qk_norm_rope_kernel<128, false><<<grid, block, 0, s>>>(a);
-  } else {
-    if (pairs) qk_norm_rope_kernel<256, true><<<grid, block, 0, s>>>(a);
-    else qk_norm_rope_kernel<256, false><<<grid, block, 0, s>>>(a);
-  }
-  const cudaError_t e = cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = d == 128 ? (pairs ? cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<128, true>, a)
+                                          : cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<128, false>, a))
+                                 : (pairs ? cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<256, true>, a)
+                                          : cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<256, false>, a));
   if (e != cudaSuccess) return fail(TG_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
   return tgi::ok();
 }
