@@ -762,59 +762,77 @@ struct MergeArgs {
 };
 
 constexpr int kMergeThreads = 128;
-// blocks of one merge: 32 rows x 16 columns each
-constexpr int merge_blocks(int d) { return (32768 / d / 32) * (d / 16); }
+// blocks of one merge: 16 rows x 16 columns each
+constexpr int merge_blocks(int d) { return (32768 / d / 16) * (d / 16); }
 
 // out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p over the pieces (and the request's own result).
-// A lane is a row and a warp 4 columns, so every load of a piece is 512 contiguous bytes.  What
-// counts is latency: ten pieces' (m, l) and O are loaded together, and joined to what came before
-// by their own maximum, so that a run of up to ten pieces waits for memory once.
+// A warp has 4 columns of 16 rows, its halves the even and the odd pieces: a piece's loads are 256
+// contiguous bytes.  What counts is latency: ten pieces' (m, l) and O are loaded together and
+// joined to what came before by their own maximum, so that a run of up to twenty pieces, the
+// usual cut over an idle device, waits for memory once.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) tile_merge_kernel(const MergeArgs a) {
   constexpr int ROWS = 32768 / D, COLS = D / 16, AT_ONCE = 10;
   // the plan is there: the kernel before let this one start after it had waited for its own
   const tg_tile_merge mg = a.merges[blockIdx.x / merge_blocks(D)];
   const int chunk = blockIdx.x % merge_blocks(D);
-  const int at = (chunk / COLS) * 32 + (threadIdx.x & 31);            // row of the slot
+  const int lane = threadIdx.x & 31, odd = lane >> 4;
+  const int at = (chunk / COLS) * 16 + (lane & 15);                   // row of the slot
   const int c4 = (chunk % COLS) * 4 + (threadIdx.x >> 5);             // which 4 columns
   const int tile = at >> 7, r = at & 127, tok = r / a.g, head = r - tok * a.g;
   const int n = min(mg.nrow - tile * a.tq, a.tq);
   const bool mine = tok < n && r < a.tq * a.g;
+  if (!__any_sync(0xffffffffu, mine)) return;
   const int64_t row = (int64_t)(mg.row0 + tile * a.tq + tok) * a.H_q + mg.h * a.g + head;
   griddep_wait();
-  if (!mine) return;
   const float2 *ml = reinterpret_cast<const float2 *>(a.ws_ml) + (int64_t)mg.slot0 * 256 + at;
   const float4 *po = reinterpret_cast<const float4 *>(a.ws_o) + (int64_t)mg.slot0 * 8192 + c4 * ROWS + at;
-  const float w = a.own_out ? __ldcg(a.ws_own + (int64_t)mg.slot0 * 256 + at) * kTileLog2e : -INFINITY;
-  uint2 own = make_uint2(0, 0);
-  if (a.own_out) own = *reinterpret_cast<const uint2 *>(a.own_out + row * D + c4 * 4);
-  float M = w, total = w == -INFINITY ? 0.f : 1.f;
+  float M = -INFINITY, total = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (total != 0.f)
-    o = make_float4(__uint_as_float(own.x << 16), __uint_as_float(own.x & 0xffff0000u), __uint_as_float(own.y << 16),
-                    __uint_as_float(own.y & 0xffff0000u));
-  for (int p0 = 0; p0 < mg.nparts; p0 += AT_ONCE) {
+  if (mine && !odd && a.own_out) {
+    const float w = __ldcg(a.ws_own + (int64_t)mg.slot0 * 256 + at) * kTileLog2e;
+    const uint2 own = *reinterpret_cast<const uint2 *>(a.own_out + row * D + c4 * 4);
+    if (w != -INFINITY) {
+      M = w, total = 1.f;
+      o = make_float4(__uint_as_float(own.x << 16), __uint_as_float(own.x & 0xffff0000u),
+                      __uint_as_float(own.y << 16), __uint_as_float(own.y & 0xffff0000u));
+    }
+  }
+  // a state (M, total, o) scaled to another maximum
+  auto scale_to = [&](float top) {
+    const float f = M == -INFINITY ? 0.f : ex2(M - top);
+    M = top;
+    total *= f, o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+  };
+  for (int p0 = odd; p0 < mg.nparts; p0 += 2 * AT_ONCE) {
     float2 v[AT_ONCE];
     float4 x[AT_ONCE];
 #pragma unroll
     for (int p = 0; p < AT_ONCE; ++p) {
-      const int k = min(p0 + p, mg.nparts - 1);
-      v[p] = __ldcg(ml + k * 256);
-      x[p] = __ldcg(po + (int64_t)k * 8192);
-      if (p0 + p >= mg.nparts) v[p].x = -INFINITY;
+      const int k = p0 + 2 * p;
+      v[p] = make_float2(-INFINITY, 0.f);
+      if (mine && k < mg.nparts) {
+        v[p] = __ldcg(ml + k * 256);
+        x[p] = __ldcg(po + (int64_t)k * 8192);
+      }
     }
     float top = M;
 #pragma unroll
     for (int p = 0; p < AT_ONCE; ++p) top = fmaxf(top, v[p].x);
-    const float f0 = M == -INFINITY ? 0.f : ex2(M - top);
-    M = top;
-    total *= f0, o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
+    scale_to(top);
 #pragma unroll
     for (int p = 0; p < AT_ONCE; ++p) {
-      const float f = v[p].x == -INFINITY ? 0.f : ex2(v[p].x - top);
-      if (f != 0.f) total += f * v[p].y, o.x += f * x[p].x, o.y += f * x[p].y, o.z += f * x[p].z, o.w += f * x[p].w;
+      if (v[p].x == -INFINITY) continue;
+      const float f = ex2(v[p].x - top);
+      total += f * v[p].y, o.x += f * x[p].x, o.y += f * x[p].y, o.z += f * x[p].z, o.w += f * x[p].w;
     }
   }
+  // the even pieces' state and the odd ones', in that order in both halves
+  scale_to(fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16)));
+  total += __shfl_xor_sync(0xffffffffu, total, 16);
+  o.x += __shfl_xor_sync(0xffffffffu, o.x, 16), o.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
+  o.z += __shfl_xor_sync(0xffffffffu, o.z, 16), o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
+  if (!mine || odd) return;
   const float inv = total == 0.f ? 0.f : 1.f / total;
   *reinterpret_cast<uint2 *>(a.out + row * D + c4 * 4) =
       make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
