@@ -23,12 +23,17 @@
 // takes two per block).
 //
 // Why 80 keys: O takes 256 of the 512 columns of tensor memory; two S of 80 columns and two P of
-// 40 (bf16, the A operand of P V) fit in the rest.  A softmax warp reads its S into registers at
-// once and gives the buffer back, so the next Q K^T runs while it computes, and P V of a block
-// runs while it computes the next: no product waits for the other, and the way over the barriers
-// (about 300 clocks each time) is off the critical path.  At d = 128 each tile has an S and a P of
-// its own, at d = 256 the blocks of the tile alternate between them.  With S of 128 columns and P
-// in their place the softmax and both products alternated: 3100 clocks for 2048 of MMAs.
+// 40 (bf16, the A operand of P V) fit in the rest.
+//
+// Who waits for whom.  At d = 128 each tile has an S and a P and goes in steps: in step t the lanes
+// issue Q K^T of block t and P V of block t - 2, and the softmax, which has the weights of block
+// t - 1 in registers by then, waits for both products at once, stores P(t - 1), reads S(t) and
+// says so; then it computes on while the products of step t + 1 run.  One wait and one arrival a
+// block: each costs 60 to 200 clocks on an SM whose special-function queue is full.  At d = 256 the
+// blocks of the one tile alternate between two S and two P, each with barriers of its own, because
+// a step would leave the tensor cores idle while the softmax turns round.
+// With S of 128 columns and P in their place the softmax and both products alternated: 3100 clocks
+// for 2048 of MMAs.
 // Items of the plan follow one another without a break: the loader runs ahead into the next.
 #pragma once
 
@@ -72,12 +77,14 @@ struct TileArgs {
 
 // Barriers and flags, by byte offset from their shared-memory address (32-bit addresses keep the
 // MMA lanes' code short: one lane runs an instruction every few clocks only).
-//   by S and P buffer -- s_full: S written; s_free: read; p_ready: P written; pv_done: multiplied
-//   with V and added to O.  Whoever waits for a phase of one of them takes part in the next, so none
-//   is overtaken.
+//   d = 128, by tile -- made: a step's products are done (both lanes arrive); taken: P stored and S
+//   read (the four softmax warps).  d = 256, by S and P buffer -- s_full: S written; s_free: read;
+//   p_ready: P written; pv_done: multiplied with V and added to O.  Whoever waits for a phase of one
+//   of them takes part in the next, so none is overtaken.
 constexpr uint32_t kQFull = 0, kQEmpty = 8, kFull = 16, kEmpty = kFull + 8 * kStages, kSFull = kEmpty + 8 * kStages,
                    kPvDone = kSFull + 16, kToClear = kPvDone + 16, kCleared = kToClear + 8, kDrain = kCleared + 8,
                    kSFree = kDrain + 16, kPReady = kSFree + 16, kTmemSlot = kPReady + 16, kAbort = kTmemSlot + 4;
+constexpr uint32_t kMade = kSFull, kTaken = kSFree;  // d = 128
 
 __device__ __forceinline__ void bar_init(uint32_t at, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(at), "r"(count) : "memory");
@@ -228,10 +235,10 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, i
     tmem_wait_ld();
     return other;
   };
-  uint32_t count = 0;  // blocks done
-  // block n of this warp uses buffer slot_of(n), in the phase_of(n) of its barriers
+  uint32_t count = 0;  // d = 128: steps done; d = 256: blocks done
+  // block n uses buffer slot_of(n), at d = 256 in the phase_of(n) of its barriers
   auto slot_of = [&](uint32_t n) -> uint32_t { return D == 128 ? (uint32_t)tile : n & 1; };
-  auto phase_of = [&](uint32_t n) -> uint32_t { return (D == 128 ? n : n >> 1) & 1; };
+  auto phase_of = [&](uint32_t n) -> uint32_t { return (n >> 1) & 1; };
   ItemList list;
   list.start(a);
   while (list.advance()) {
@@ -252,19 +259,34 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, i
     }
     float m = -INFINITY, l = 0.f;
     const bool some = rg.b < rg.e;
-    for (int j = rg.b; j < rg.e; ++j, ++count) {
-      const uint32_t slot = slot_of(count);
-      if (!wait(kSFull + 8 * slot, phase_of(count))) return;
-      float s[N];
-      const uint32_t s_addr = slot * kKeys + half * N + lanes;
+    float s[N];
+    auto read_s = [&](uint32_t slot) {
+      const uint32_t at = slot * kKeys + half * N + lanes;
       uint32_t *sr = reinterpret_cast<uint32_t *>(s);
-      tmem_ld32(s_addr, sr);
-      if (HALVES == 1) tmem_ld32(s_addr + 32, sr + 32), tmem_ld16(s_addr + 64, sr + 64);
-      if (HALVES == 2) tmem_ld8(s_addr + 32, sr + 32);
-      tmem_wait_ld();
+      tmem_ld32(at, sr);
+      if (HALVES == 1) tmem_ld32(at + 32, sr + 32), tmem_ld16(at + 64, sr + 64);
+      if (HALVES == 2) tmem_ld8(at + 32, sr + 32);
+    };
+    // what this warp read and wrote in tensor memory is done
+    auto arrive = [&](uint32_t at) {
       tc_fence_before();
       __syncwarp();
-      if ((threadIdx.x & 31) == 0) bar_arrive(bars + kSFree + 8 * slot);
+      if ((threadIdx.x & 31) == 0) bar_arrive(bars + at);
+    };
+    if (HALVES == 1 && some) {  // step 0: the first S
+      if (!wait(kMade + 8 * tile, count++ & 1)) return;
+      read_s(tile);
+      tmem_wait_ld();
+      if (rg.e - rg.b > 1) arrive(kTaken + 8 * tile);
+    }
+    for (int j = rg.b; j < rg.e; ++j, ++count) {
+      const uint32_t slot = slot_of(count);
+      if (HALVES == 2) {
+        wait(kSFull + 8 * slot, phase_of(count));
+        read_s(slot);
+        tmem_wait_ld();
+        arrive(kSFree + 8 * slot);
+      }
       const int k0 = j * kKeys;
       if (k0 + kKeys > hi_first || k0 < lo_last) {
         const int h1 = hi - k0 - half * N, l1 = lo - k0 - half * N;
@@ -308,7 +330,8 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, i
         m = m_new;
         l *= f;
         if (j > rg.b) {  // scale O, once the block before has been added to it
-          if (!wait(kPvDone + 8 * slot_of(count - 1), phase_of(count - 1))) return;
+          if (HALVES == 1 && !wait(kMade + 8 * tile, count & 1)) return;
+          if (HALVES == 2) wait(kPvDone + 8 * slot_of(count - 1), phase_of(count - 1));
 #pragma unroll 1
           for (int c = 0; c < COLS / 32; ++c) {
             uint32_t o[32];
@@ -321,25 +344,38 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, i
         }
       }
       l += part;
-      // P of this buffer's block before has been multiplied
-      constexpr uint32_t back = D == 128 ? 1 : 2;
-      if (count >= back && !wait(kPvDone + 8 * slot, phase_of(count - back))) return;
       const uint32_t p_addr = kWeights + slot * (kKeys / 2) + half * (N / 2) + lanes;
-      if (HALVES == 1) tmem_st32(p_addr, p), tmem_st8(p_addr + 32, p + 32);
-      if (HALVES == 2) tmem_st16(p_addr, p), tmem_st4(p_addr + 16, p + 16);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if ((threadIdx.x & 31) == 0) bar_arrive(bars + kPReady + 8 * slot);
+      if (HALVES == 1) {
+        // the step after: S of the next block is there, P of the block before has been multiplied
+        if (rg.e - rg.b == 1)
+          --count;  // there is none: P goes with the step before
+        else if (!wait(kMade + 8 * tile, count & 1))
+          return;
+        if (j + 1 < rg.e) read_s(tile);
+        tmem_st32(p_addr, p), tmem_st8(p_addr + 32, p + 32);
+        tmem_wait_ld();
+        tmem_wait_st();
+        arrive(kTaken + 8 * tile);
+      } else {
+        // P of this buffer's block before has been multiplied
+        if (count >= 2) wait(kPvDone + 8 * slot, phase_of(count - 2));
+        tmem_st16(p_addr, p), tmem_st4(p_addr + 16, p + 16);
+        tmem_wait_st();
+        arrive(kPReady + 8 * slot);
+      }
+    }
+    if (HALVES == 1 && some) {  // the step that adds the last block; the next item's first Q K^T may follow
+      if (!wait(kMade + 8 * tile, count++ & 1)) return;
+      arrive(kTaken + 8 * tile);
     }
     if (n <= 0) continue;
 
     // output: this row's O / l, or the piece's (m, l, O); half of the columns each
     const bool mine = tok < n && r < a.tq * a.g;
     const int64_t row = ((int64_t)(it.row0 + first + tok)) * a.H_q + it.h * a.g + head;
-    if (some) {
-      if (HALVES == 2) l += exchange(2, l);
-      if (!wait(kPvDone + 8 * slot_of(count - 1), phase_of(count - 1))) return;
+    if (HALVES == 2 && some) {
+      l += exchange(2, l);
+      wait(kPvDone + 8 * slot_of(count - 1), phase_of(count - 1));
     }
     const float mo = m == -INFINITY ? -INFINITY : m * sl2;  // base-2 reference
     if (it.slot >= 0) {
@@ -445,12 +481,25 @@ __device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p, uint32_t v, boo
     mma_ts(o, p + i * 8, smem_desc(v + i * 2048, kHalfBytes, 1024), idesc, accumulate || i > 0);
 }
 
+// d = 128: a tile with blocks [b, e) has the steps b .. e + 1, Q K^T of block j in step j and P V in
+// step j + 2; a lane takes part in every step, with its products or by arriving for nothing.  Of
+// a single block the step without either is left out.
+__device__ __forceinline__ bool in_steps(const tgi::TileRange &r, int j) {
+  return r.b < r.e && j >= r.b && j < r.e + 2 && !(r.e - r.b == 1 && j == r.e);
+}
+// the softmax has taken what the step before made (n: steps of the tile so far)
+__device__ __forceinline__ bool next_step(uint32_t bars, int tile, uint32_t n, int32_t *status) {
+  if (n > 0 && !lane_wait(bars, kTaken + 8 * tile, (n - 1) & 1, status)) return false;
+  tc_fence_after();
+  return true;
+}
+
 // Two lanes issue: one the Q K^T, the other the P V.  The tensor pipe takes a few MMAs ahead only,
 // about 200 clocks of work; a lane alone left it empty while it waited for the next barrier
 // (2390 clocks a block of both tiles against 1800 with two, 1456 of MMAs).
 template <int D, bool PAGED>
 __device__ __forceinline__ bool qk_items(const TileArgs &a, uint32_t bars, uint32_t q_at, uint32_t ring_at) {
-  constexpr int NP = D / 128, TILES = 2 / NP;
+  constexpr int NP = D / 128;
   Cycle<kStages> ring;
   uint32_t q_phase = 0, count[2] = {0, 0};
   ItemList list;
@@ -470,16 +519,25 @@ __device__ __forceinline__ bool qk_items(const TileArgs &a, uint32_t bars, uint3
         ring.next();
         if (!lane_wait(bars, kFull + 8 * ks[c].at, ks[c].phase, a.status)) return false;
       }
+      if (D == 128) {
 #pragma unroll
-      for (int i = 0; i < TILES; ++i) {
-        if (!needs(rg.tile[i], j)) continue;
-        const uint32_t slot = D == 128 ? i : count[0] & 1, uses = D == 128 ? count[i] : count[0] >> 1;
+        for (int i = 0; i < 2; ++i) {
+          if (!in_steps(rg.tile[i], j)) continue;
+          if (!next_step(bars, i, count[i]++, a.status)) return false;
+          if (j < rg.tile[i].e) {
+            issue_qk(i * kKeys, q_at + i * kQPiece, ring_at + ks[0].at * kStageBytes, false);
+            mma_commit(bars + kMade + 8 * i);
+          } else {
+            bar_arrive(bars + kMade + 8 * i);
+          }
+        }
+      } else {
+        const uint32_t slot = count[0] & 1, uses = count[0] >> 1;
         if (uses > 0 && !lane_wait(bars, kSFree + 8 * slot, (uses - 1) & 1, a.status)) return false;
         tc_fence_after();
-        ++count[i];
+        ++count[0];
 #pragma unroll
-        for (int c = 0; c < NP; ++c)
-          issue_qk(slot * kKeys, q_at + (D == 128 ? i : c) * kQPiece, ring_at + ks[c].at * kStageBytes, c > 0);
+        for (int c = 0; c < NP; ++c) issue_qk(slot * kKeys, q_at + c * kQPiece, ring_at + ks[c].at * kStageBytes, c > 0);
         mma_commit(bars + kSFull + 8 * slot);
       }
 #pragma unroll
@@ -488,13 +546,23 @@ __device__ __forceinline__ bool qk_items(const TileArgs &a, uint32_t bars, uint3
     }
     mma_commit(bars + kQEmpty);
     ring.skip(NP);  // V(e-1)
+    if (D == 128) {  // the two steps that only P V takes part in
+      for (int j = rg.e; j < rg.e + 2; ++j) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (!in_steps(rg.tile[i], j)) continue;
+          if (!next_step(bars, i, count[i]++, a.status)) return false;
+          bar_arrive(bars + kMade + 8 * i);
+        }
+      }
+    }
   }
   return true;
 }
 
 template <int D, bool PAGED>
 __device__ __forceinline__ bool pv_items(const TileArgs &a, uint32_t bars, uint32_t ring_at) {
-  constexpr int NP = D / 128, TILES = 2 / NP;
+  constexpr int NP = D / 128;
   Cycle<kStages> ring;
   uint32_t c_phase = 0, count[2] = {0, 0};
   ItemList list;
@@ -504,6 +572,16 @@ __device__ __forceinline__ bool pv_items(const TileArgs &a, uint32_t bars, uint3
     const ItemRange rg = item_range<D, PAGED>(it, a);
     if (rg.b >= rg.e) continue;
     ring.skip(NP);  // K(b)
+    if (D == 128) {  // the two steps ahead of a tile's first P V
+      for (int j = rg.b; j < rg.b + 2; ++j) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (!in_steps(rg.tile[i], j)) continue;
+          if (!next_step(bars, i, count[i]++, a.status)) return false;
+          bar_arrive(bars + kMade + 8 * i);
+        }
+      }
+    }
     for (int j = rg.b; j < rg.e; ++j) {
       if (j + 1 < rg.e) ring.skip(NP);  // K(j+1)
       Cycle<kStages> vs[NP];
@@ -518,17 +596,26 @@ __device__ __forceinline__ bool pv_items(const TileArgs &a, uint32_t bars, uint3
         if (!lane_wait(bars, kCleared, c_phase, a.status)) return false;
         c_phase ^= 1;
       }
+      if (D == 128) {
 #pragma unroll
-      for (int i = 0; i < TILES; ++i) {
-        if (!needs(rg.tile[i], j)) continue;
-        const uint32_t slot = D == 128 ? i : count[0] & 1, uses = D == 128 ? count[i] : count[0] >> 1;
+        for (int i = 0; i < 2; ++i) {
+          if (!in_steps(rg.tile[i], j + 2)) continue;
+          if (!next_step(bars, i, count[i]++, a.status)) return false;
+          if (j >= rg.tile[i].b) {
+            issue_pv(kOut + i * 128, kWeights + i * (kKeys / 2), ring_at + vs[0].at * kStageBytes, j > rg.tile[i].b);
+            mma_commit(bars + kMade + 8 * i);
+          } else {
+            bar_arrive(bars + kMade + 8 * i);
+          }
+        }
+      } else {
+        const uint32_t slot = count[0] & 1, uses = count[0] >> 1;
         if (!lane_wait(bars, kPReady + 8 * slot, uses & 1, a.status)) return false;
         tc_fence_after();
-        ++count[i];
+        ++count[0];
 #pragma unroll
         for (int c = 0; c < NP; ++c)
-          issue_pv(kOut + (D == 128 ? i : c) * 128, kWeights + slot * (kKeys / 2), ring_at + vs[c].at * kStageBytes,
-                   j > rg.tile[i].b);
+          issue_pv(kOut + c * 128, kWeights + slot * (kKeys / 2), ring_at + vs[c].at * kStageBytes, j > rg.b);
         mma_commit(bars + kPvDone + 8 * slot);
       }
 #pragma unroll
@@ -693,7 +780,9 @@ __device__ __forceinline__ void load_items(const CUtensorMap *qm, const CUtensor
   }
 }
 
-constexpr int kTileThreads = 384;  // twelve warps, 168 registers each at most
+// twelve warps, 168 registers each at launch; at d = 128 they move to the eight softmax warps
+// (384 x 168 = 256 x 208 + 128 x 88)
+constexpr int kTileThreads = 384;
 
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(kTileThreads, 1)
@@ -707,7 +796,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (warp == SW) tmem_alloc(reinterpret_cast<uint32_t *>(base + kQBytes + kStages * kStageBytes + kTmemSlot), 512);
   if (warp == SW + 2 && elect_one()) prefetch_tensormap(&qm), prefetch_tensormap(&km), prefetch_tensormap(&vm);
   if (threadIdx.x == 0) {
-    for (uint32_t at = 0; at < kTmemSlot; at += 8) bar_init(bars + at, at >= kSFree ? SW * D / 256 : 1);
+    for (uint32_t at = 0; at < kTmemSlot; at += 8) bar_init(bars + at, at >= kSFree ? SW * D / 256 : D == 128 && at >= kMade && at < kMade + 16 ? 2 : 1);
     asm volatile("st.volatile.shared.s32 [%0], %1;" ::"r"(bars + kAbort), "r"(0) : "memory");
     fence_barrier_init();
   }
@@ -728,6 +817,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (a.signal) griddep_launch_dependents();
   // all 512 columns are this block's, so they start at column 0: the MMAs and the softmax
   // address them by constants
+  if (D == 128 && warp < SW) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  if (D == 128 && warp >= SW) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp < SW) {
     softmax_role<D, PAGED>(a, bars, D == 128 ? warp >> 2 : 0, D == 128 ? 0 : warp >> 2);
   } else if (warp <= SW + 1) {

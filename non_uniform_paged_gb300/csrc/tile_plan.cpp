@@ -5,9 +5,11 @@
 // the work over the thread blocks is fixed ahead of the calls): here the unit is a tile of
 // query rows against a range of 128-key blocks, because many rows share each key.
 //
-// Items are sorted by cost and given, longest first, to the block with the least work.  When
-// one item is longer than an even share, runs of keys are cut: a few cut lengths around that
-// share are tried and the one whose longest block is shortest under the cost model is kept.
+// Items are sorted by cost and given, longest first, to the block with the least work.  Where
+// that leaves blocks idle -- an item is longer than an even share, or each block gets so few
+// items that they do not divide evenly -- runs of keys are cut: all of them, or only those of
+// the items that are left over when every block has had the same number; a few lengths of
+// piece are tried, and the one whose longest block is shortest under the cost model is kept.
 #include "tile_common.h"
 
 #include "tg_internal.h"
@@ -23,9 +25,10 @@ namespace {
 
 using tgi::fail;
 
-// Cost model in units of one 80-key block of an item (about 0.75 us): an item's start and end, a piece's
-// partial (written and read again), and the second kernel of a plan that has any.
-constexpr double kItemCost = 3.0, kPieceCost = 1.5, kMergeCost = 4.0;
+// Cost model in units of one 80-key block of an item (about 0.85 us): an item's start and end, a
+// piece's partial, and the second kernel of a plan that has any, alone and for each full piece it
+// reads.
+constexpr double kItemCost = 3.0, kPieceCost = 1.0, kMergeCost = 2.5, kMergePiece = 0.025;
 
 double item_cost(const tg_tile_item &it, bool piece) {
   return (it.blk1 - it.blk0) + kItemCost + (piece ? kPieceCost : 0.0);
@@ -33,18 +36,27 @@ double item_cost(const tg_tile_item &it, bool piece) {
 
 int64_t pieces_of(int nblk, int cut) { return nblk <= cut ? 1 : (nblk + cut - 1) / cut; }
 
-// longest block's work when every run is cut to at most `cut` blocks
-double makespan(const std::vector<tg_tile_item> &base, int cut, int n_cta) {
-  std::vector<double> cost;
-  bool any = false;
-  for (const tg_tile_item &it : base) {
-    const int n = it.blk1 - it.blk0;
-    const int64_t p = pieces_of(n, cut);
-    any |= p > 1;
-    for (int64_t k = 0; k < p; ++k)
-      cost.push_back((double)((k + 1) * n / p - k * n / p) + kItemCost + (p > 1 ? kPieceCost : 0.0));
+// how runs are cut: of the items behind the first `whole`, to at most `length` blocks
+struct Cut {
+  int length = INT32_MAX;
+  size_t whole = 0;
+  int64_t pieces(const std::vector<tg_tile_item> &sorted, size_t k) const {
+    return k < whole ? 1 : pieces_of(sorted[k].blk1 - sorted[k].blk0, length);
   }
-  std::sort(cost.begin(), cost.end(), std::greater<double>());
+};
+
+// longest block's work
+double makespan(const std::vector<tg_tile_item> &sorted, const Cut &cut, int n_cta, int full_rows) {
+  std::vector<double> cost;
+  double pieces = 0;  // in full ones
+  for (size_t k = 0; k < sorted.size(); ++k) {
+    const int n = sorted[k].blk1 - sorted[k].blk0;
+    const int64_t p = cut.pieces(sorted, k);
+    if (p > 1) pieces += (double)p * sorted[k].nrow / full_rows;
+    for (int64_t i = 0; i < p; ++i)
+      cost.push_back((double)((i + 1) * n / p - i * n / p) + kItemCost + (p > 1 ? kPieceCost : 0.0));
+  }
+  if (pieces > 0) std::sort(cost.begin(), cost.end(), std::greater<double>());
   std::priority_queue<double, std::vector<double>, std::greater<double>> load;
   for (int c = 0; c < n_cta; ++c) load.push(0.0);
   double worst = 0;
@@ -54,50 +66,60 @@ double makespan(const std::vector<tg_tile_item> &base, int cut, int n_cta) {
     load.push(l);
     worst = std::max(worst, l);
   }
-  return worst + (any ? kMergeCost : 0.0);
+  return worst + (pieces > 0 ? kMergeCost + kMergePiece * pieces : 0.0);
 }
 
-// the number of blocks that runs are cut to (INT32_MAX: none is cut)
-int choose_cut(const std::vector<tg_tile_item> &base, int n_cta) {
-  double total = 0, longest = 0;
-  int most = 0;
-  for (const tg_tile_item &it : base) {
-    total += item_cost(it, false);
-    longest = std::max(longest, item_cost(it, false));
-    most = std::max(most, it.blk1 - it.blk0);
-  }
+Cut choose_cut(const std::vector<tg_tile_item> &sorted, int n_cta, int full_rows) {
+  Cut best;
+  double total = 0;
+  for (const tg_tile_item &it : sorted) total += item_cost(it, false);
   const double share = total / n_cta;
-  if (most <= 1 || longest <= 1.1 * share) return INT32_MAX;
-  double best = makespan(base, INT32_MAX, n_cta);
-  int cut = INT32_MAX;
-  auto attempt = [&](int c) {
-    if (c < 1 || c >= most) return;
-    const double m = makespan(base, c, n_cta);
-    if (m < best - 1e-9) best = m, cut = c;
+  double least = makespan(sorted, best, n_cta, full_rows);
+  const int most = sorted[0].blk1 - sorted[0].blk0;
+  if (most <= 1 || least <= 1.03 * share) return best;
+  auto attempt = [&](int length, size_t whole) {
+    if (length < 1 || whole >= sorted.size() || length >= sorted[whole].blk1 - sorted[whole].blk0) return;
+    Cut c;
+    c.length = length, c.whole = whole;
+    const double m = makespan(sorted, c, n_cta, full_rows);
+    if (m < least - 1e-9) least = m, best = c;
   };
-  for (double f : {0.34, 0.5, 0.7, 1.0, 1.25, 1.6, 2.0, 3.0}) attempt(std::max(1, (int)(f * share)));
-  // the shortest cut whose pieces still start all at once, one per block
-  int lo = 1, hi = most;
-  while (lo < hi) {
-    const int mid = lo + (hi - lo) / 2;
-    int64_t n = 0;
-    for (const tg_tile_item &it : base) n += pieces_of(it.blk1 - it.blk0, mid);
-    if (n <= n_cta) hi = mid; else lo = mid + 1;
+  // every run to a fraction of the even share
+  for (double f : {0.25, 0.34, 0.42, 0.5, 0.6, 0.7, 0.85, 1.0, 1.25, 1.6, 2.0, 3.0}) attempt((int)std::min(1e9, std::max(1.0, f * share)), 0);
+  // the shortest pieces that still start all at once, one per block
+  if ((int64_t)sorted.size() <= n_cta) {
+    int lo = 1, hi = most;
+    while (lo < hi) {
+      const int mid = lo + (hi - lo) / 2;
+      int64_t n = 0;
+      for (const tg_tile_item &it : sorted) n += pieces_of(it.blk1 - it.blk0, mid);
+      if (n <= n_cta) hi = mid; else lo = mid + 1;
+    }
+    attempt(lo, 0);
   }
-  attempt(lo);
-  return cut;
+  // only the items left over when every block has had as many
+  const size_t whole = sorted.size() / n_cta * n_cta;
+  if (whole > 0 && whole < sorted.size()) {
+    const int n = sorted[whole].blk1 - sorted[whole].blk0;
+    for (int k = 2; k <= 16; ++k) attempt((n + k - 1) / k, whole);
+  }
+  return best;
 }
 
 // cut, order and serialise; hd carries the sizes
 int finish(const char *fn, tg_tile_header hd, std::vector<tg_tile_item> &base, void *plan, int64_t plan_cap,
            int64_t *plan_bytes, int64_t *workspace_bytes) {
-  const int cut = base.empty() ? INT32_MAX : choose_cut(base, hd.N_CTA);
+  auto longer = [](const tg_tile_item &a, const tg_tile_item &b) { return a.blk1 - a.blk0 > b.blk1 - b.blk0; };
+  std::stable_sort(base.begin(), base.end(), longer);
+  const int full_rows = tgi::tile_tokens(hd.H_q / hd.H) * tgi::tiles_per_item(hd.d);
+  const Cut cut = base.empty() ? Cut() : choose_cut(base, hd.N_CTA, full_rows);
   std::vector<tg_tile_item> items;
   std::vector<tg_tile_merge> merges;
   int64_t slots = 0;
-  for (const tg_tile_item &it : base) {
+  for (size_t at = 0; at < base.size(); ++at) {
+    const tg_tile_item &it = base[at];
     const int n = it.blk1 - it.blk0;
-    const int64_t p = pieces_of(n, cut);
+    const int64_t p = cut.pieces(base, at);
     if (p == 1) {
       items.push_back(it);
       continue;
@@ -113,9 +135,7 @@ int finish(const char *fn, tg_tile_header hd, std::vector<tg_tile_item> &base, v
     }
   }
   if (items.size() > INT32_MAX || slots > INT32_MAX) return fail(TG_ERR_SHAPE, "%s: too many work items", fn);
-  std::stable_sort(items.begin(), items.end(), [](const tg_tile_item &a, const tg_tile_item &b) {
-    return a.blk1 - a.blk0 > b.blk1 - b.blk0;
-  });
+  std::stable_sort(items.begin(), items.end(), longer);
   const int n_cta = (int)std::max<int64_t>(1, std::min<int64_t>(hd.N_CTA, (int64_t)items.size()));
   using Load = std::pair<double, int>;
   std::priority_queue<Load, std::vector<Load>, std::greater<Load>> load;
