@@ -8,7 +8,7 @@
 // values: of the pairs (i, i + rot/2), 4 first and the 4 second values, so that a rotation needs
 // no exchange between lanes (a group of 4 is still 128 contiguous bytes over half a warp); of
 // the pairs (2i, 2i+1) and behind rot, 8 consecutive ones.  A warp takes one token and walks over
-// its heads in batches of 8 loads, each batch queries, keys or values only, the next one in
+// its heads in batches of 4 loads, each batch queries, keys or values only, the next one in
 // flight while one is worked on; the request's row and the table row are looked up once.
 // What bounds it beside memory is instructions (at 4400 a token the issue slots would take as
 // long as the bytes): the weights are multiplied into the token's rotation once a batch, and
@@ -26,8 +26,11 @@ namespace {
 
 using namespace tgk;
 
-constexpr int kSteps = 8;  // loads of a batch: heads at d = 256, pairs of heads at d = 128
-constexpr int kWarps = 4;
+constexpr int kSteps = 4;  // loads of a batch: heads at d = 256, pairs of heads at d = 128
+// Blocks of one warp, 24 to an SM: a block's place is free when its token is done.  For 20000 tokens
+// of 32 + 16 heads of 128, blocks of 4 warps took 92 us, of one 88; batches of 4 instead of 8 loads,
+// with 24 instead of 16 warps to an SM, 81.
+constexpr int kBlocks = 24;
 
 struct RopeArgs {
   const int32_t *cu_q, *start, *positions;
@@ -52,13 +55,11 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
 }
 
 template <int D, bool PAIRS>
-__global__ void __launch_bounds__(kWarps * 32, 4) qk_norm_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(32, kBlocks) qk_norm_rope_kernel(const RopeArgs a) {
   constexpr int LANES = D / 8, PER = 32 / LANES;  // lanes of a head, heads side by side
-  const int lane = threadIdx.x & 31, sub = lane % LANES, side = lane / LANES;
+  const int lane = threadIdx.x, sub = lane % LANES, side = lane / LANES;
   const int all = a.q_batches + 2 * a.kv_batches;
-  const int64_t task = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int t = (int)(task / a.parts), part = (int)(task - (int64_t)t * a.parts);
-  if (t >= a.T) return;
+  const int t = blockIdx.x / a.parts, part = blockIdx.x - t * a.parts;
   const int first = all * part / a.parts, last = all * (part + 1) / a.parts;
   // the two groups of this lane
   const bool turned = sub * 8 < a.rot;
@@ -217,13 +218,13 @@ extern "C" int tg_qk_norm_rope(tg_stream_t stream, int batch, int T, int H_q, in
   a.cu_q = cu_q, a.start = start, a.positions = positions, a.qkv = qkv, a.stride = qkv_stride;
   a.qw = q_weight, a.kw = k_weight, a.table = cos_sin, a.q = q, a.K = K, a.V = V, a.status = dev_status;
   a.batch = batch, a.T = T, a.H_q = H_q, a.H = H, a.Nmax = Nmax, a.rot = rot, a.max_pos = max_pos, a.eps = eps;
-  // A warp a token, or, below 1024 tokens, one for each of its batches: 256 tokens of 32 + 16 heads of
-  // 128 take 6.3 us one way and 3.9 the other, 1024 tokens 7.1 both ways, 4096 tokens 19 and 24.
+  // A warp a token, or, below 2048 tokens, one for each of its batches: 256 tokens of 32 + 16 heads of
+  // 128 take 6.6 us one way and 3.2 the other, 2048 tokens 10.3 and 10.0, 4096 tokens 15.0 and 18.7.
   const int per = kSteps * (d == 128 ? 2 : 1);
   a.q_batches = (H_q + per - 1) / per;
   a.kv_batches = (H + per - 1) / per;
-  a.parts = T < 1024 ? a.q_batches + 2 * a.kv_batches : 1;
-  const int64_t blocks = ((int64_t)T * a.parts + kWarps - 1) / kWarps;
+  a.parts = T < 2048 ? a.q_batches + 2 * a.kv_batches : 1;
+  const int64_t blocks = (int64_t)T * a.parts;
   if (blocks > INT32_MAX) return fail(TG_ERR_SHAPE, "%s: T=%d with %lld heads", fn, T, (long long)heads);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool pairs = flags & TG_ROPE_PAIRS;
@@ -232,7 +233,7 @@ extern "C" int tg_qk_norm_rope(tg_stream_t stream, int batch, int T, int H_q, in
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(kWarps * 32);
+  cfg.blockDim = dim3(32);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
