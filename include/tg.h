@@ -619,7 +619,8 @@ typedef struct tg_tile_merge {
  *   tokens, the last q_len[b] of its kv_len[b] context tokens (kv_len counts them).
  *   q_len > kv_len is allowed: the rows before the context see no key.
  *   window 0: token at position p sees keys [0, p]; > 0: keys (p - window, p].
- *   d in {128, 256}; g = H_q / H in [1, 8]; N_CTA >= 1 (one per SM).
+ *   d in {128, 256}; g = H_q / H in [1, 8]; N_CTA in [1, 65536], the thread blocks to
+ *   plan for (one per SM).
  * Outputs (host): plan (NULL to query the size); *plan_bytes; *workspace_bytes = the
  *   device scratch a call needs (0 if no run is cut).  TG_ERR_CAPACITY if plan_cap is
  *   smaller. */

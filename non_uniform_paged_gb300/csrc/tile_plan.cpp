@@ -58,7 +58,7 @@ double makespan(const std::vector<tg_tile_item> &sorted, const Cut &cut, int n_c
   }
   if (pieces > 0) std::sort(cost.begin(), cost.end(), std::greater<double>());
   std::priority_queue<double, std::vector<double>, std::greater<double>> load;
-  for (int c = 0; c < n_cta; ++c) load.push(0.0);
+  for (size_t c = 0; c < cost.size() && c < (size_t)n_cta; ++c) load.push(0.0);
   double worst = 0;
   for (double c : cost) {
     const double l = load.top() + c;
@@ -134,7 +134,9 @@ int finish(const char *fn, tg_tile_header hd, std::vector<tg_tile_item> &base, v
       items.push_back(piece);
     }
   }
-  if (items.size() > INT32_MAX || slots > INT32_MAX) return fail(TG_ERR_SHAPE, "%s: too many work items", fn);
+  // (the merge's grid is 128 blocks a merge)
+  if (items.size() > INT32_MAX || slots > INT32_MAX || merges.size() > (1u << 23))
+    return fail(TG_ERR_SHAPE, "%s: too many work items", fn);
   std::stable_sort(items.begin(), items.end(), longer);
   const int n_cta = (int)std::max<int64_t>(1, std::min<int64_t>(hd.N_CTA, (int64_t)items.size()));
   using Load = std::pair<double, int>;
@@ -182,6 +184,7 @@ int finish(const char *fn, tg_tile_header hd, std::vector<tg_tile_item> &base, v
 
 int check_heads(const char *fn, int H, int H_q, int d, int N_CTA) {
   if (H <= 0 || H_q <= 0 || N_CTA <= 0) return fail(TG_ERR_INVALID_ARG, "%s: sizes must be positive", fn);
+  if (N_CTA > 65536) return fail(TG_ERR_INVALID_ARG, "%s: N_CTA=%d (1..65536; one per SM)", fn, N_CTA);
   if (H_q % H) return fail(TG_ERR_SHAPE, "%s: H_q=%d %% H=%d is not 0", fn, H_q, H);
   if (H_q / H > 8) return fail(TG_ERR_SHAPE, "%s: g=%d > 8 query heads per KV head", fn, H_q / H);
   if (d != 128 && d != 256) return fail(TG_ERR_SHAPE, "%s: d=%d (128 or 256)", fn, d);
@@ -208,6 +211,7 @@ int plan_prefill(int batch, int H, int H_q, int d, int N_CTA, const int32_t *q_l
   }
   if (rows > INT32_MAX || count > (1 << 24))
     return fail(TG_ERR_SHAPE, "%s: %lld query tokens, %lld work items", fn, (long long)rows, (long long)count);
+  if (window >= max_kv) window = 0;  // reaches back to every first key (and differences stay in int32)
   std::vector<tg_tile_item> base;
   base.reserve((size_t)count);
   int64_t row0 = 0;

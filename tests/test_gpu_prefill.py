@@ -149,6 +149,34 @@ def test_two_passes_on_two_streams(lib, cuda):
     assert all(torch.equal(o, ro) and torch.equal(l, rl) for o, l, ro, rl in got)
 
 
+def test_window_as_large_as_it_gets(lib, cuda):
+    for w in (130, 2**31 - 1):
+        _run(lib, cuda, [40, 200], [130, 60], 1, 4, 128, window=w)
+
+
+def test_more_blocks_than_the_device_has(lib, cuda):
+    """A plan for 1000 blocks on fewer SMs: they follow one another."""
+    p, *_ = _run(lib, cuda, [300, 700, 90], [3000, 700, 9000], 4, 4, 128, n_cta=1000)
+    assert p.plan.header["N_CTA"] > torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def test_keys_that_raise_the_reference_in_every_block(lib, cuda):
+    """Each block's logits tower over the ones before, by more than the weights may grow: the block
+    is done again with its own maximum, in all rows or in some of a warp's."""
+    from non_uniform_paged_gb300.ragged import PrefillPass
+    for d in (128, 256):
+        n = 500
+        q = torch.ones((n, 2, d), device=cuda).to(torch.bfloat16)
+        q[::3] = 0.01  # these rows' logits stay small
+        K = (torch.arange(n, device=cuda) // 40 * (400.0 / d))[None, None, :, None].expand(1, 1, n, d).to(torch.bfloat16).contiguous()
+        V = torch.randn((1, 1, n, d), generator=torch.Generator(device=cuda).manual_seed(4), device=cuda).to(torch.bfloat16)
+        p = PrefillPass(1, 2, d, [n], [n], device=cuda)
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device=cuda)
+        p.attend(q, K, V, out, lse, scale=1 / 16)
+        for j in range(2):
+            check(out[:, j], lse[:, j], attend64(q[:, j], K[0, 0], V[0, 0], 1 / 16, seen_keys(n, n, 0, cuda)), (d, j))
+
+
 def test_contexts_past_32_bit_offsets(lib, cuda):
     """2^31 and more values ahead of the rows that are read; a window keeps the work small."""
     from non_uniform_paged_gb300.ragged import PrefillPass

@@ -135,6 +135,49 @@ def test_offsets_past_32_bits(lib, cuda):
     assert torch.equal(K[0, 0, 0], qkv[0, 1]) and torch.equal(q, qkv[:, :1])
 
 
+@pytest.mark.parametrize("T", [16, 3000])
+def test_same_bits_in_a_graph_and_on_two_streams(lib, cuda, T):
+    ins, ref = [], []
+    for seed in (1, 2):
+        out = _run(lib, cuda, [T], [0], T, 8, 2, 128, 128, seed=seed)
+        qkv, w, tab, q, K, V, status, _ = out
+        assert status == 0
+        ins.append((qkv, w, tab)), ref.append((q.clone(), K.clone(), V.clone()))
+    cu = torch.tensor([0, T], dtype=torch.int32, device=cuda)
+    start = torch.zeros(1, dtype=torch.int32, device=cuda)
+    bufs = [tuple(torch.empty_like(t) for t in r) for r in ref]
+
+    def call(i):
+        (qkv, w, tab), (q, K, V) = ins[i], bufs[i]
+        lib.tg_qk_norm_rope(qkv, cu, start, tab, q, K, V, q_weight=w[0], k_weight=w[1])
+
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                call(i)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for x, y in zip(bufs, ref) for a, b in zip(x, y))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=streams[0]):
+        call(0), call(1), call(0)
+    for x in bufs:
+        for t in x:
+            t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for x, y in zip(bufs, ref) for a, b in zip(x, y))
+
+
+def test_long_rows_past_the_first_batches(lib, cuda):
+    """Head counts that leave batches and warps half filled, with more tokens than one warp each."""
+    for H_q, H, d, T in ((33, 3, 128, 2100), (9, 1, 256, 2050), (64, 8, 128, 70), (1, 1, 256, 5)):
+        out = _run(lib, cuda, [T], [0], T, H_q, H, d, d, seed=T)
+        assert out[6] == 0
+        _verify(out, [T], [0], H_q, H, d, False)
+
+
 def test_binding_refusals(lib, cuda):
     qkv = torch.zeros((2, 3, 128), dtype=torch.bfloat16, device=cuda)
     q, K = torch.zeros((2, 1, 128), dtype=torch.bfloat16, device=cuda), torch.zeros((1, 1, 4, 128), dtype=torch.bfloat16, device=cuda)

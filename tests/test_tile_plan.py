@@ -115,6 +115,31 @@ def test_one_long_run_is_cut_over_the_blocks(lib):
     assert lib.tile_header(plan)["n_merge"] == 0 and ws == 0
 
 
+def test_left_over_items_are_cut(lib):
+    """512 equal items on 152 blocks: three each, and the 56 left over are cut over all blocks."""
+    plan, ws = lib.tg_plan_prefill([4096], [100000], 8, 32, 128, 152)
+    hd = lib.tile_header(plan)
+    lead, items = lib.tile_items(plan)
+    load = [sum(int(it["blk1"] - it["blk0"]) for it in items[int(l["reserved"][1]):][:int(l["reserved"][0])]) for l in lead]
+    assert 0 < hd["n_merge"] <= 64 and ws > 0
+    assert max(load) <= 1.05 * sum(load) / len(load)
+
+
+def test_windows_that_reach_past_every_context_are_none(lib):
+    """A window of at least the longest context hides nothing, up to the largest int32."""
+    ref, _ = lib.tg_plan_prefill([300, 40], [300, 20], 2, 4, 128, 152)
+    for window in (300, 301, 2**31 - 1):
+        plan, _ = lib.tg_plan_prefill([300, 40], [300, 20], 2, 4, 128, 152, window)
+        assert plan.tobytes() == ref.tobytes()
+    plan, _ = lib.tg_plan_prefill([300, 40], [300, 20], 2, 4, 128, 152, 299)
+    assert lib.tile_header(plan)["window"] == 299
+
+
+def test_more_blocks_than_items(lib):
+    plan, _ = lib.tg_plan_prefill([5], [5], 1, 1, 128, 65536)
+    assert lib.tile_header(plan)["N_CTA"] == 1
+
+
 def test_longest_first_keeps_the_blocks_even(lib):
     plan, _ = lib.tg_plan_prefill([4096, 300, 17, 2000], [4096, 300, 17, 2000], 8, 32, 128, 152)
     lead, items = lib.tile_items(plan)
@@ -132,6 +157,7 @@ def test_plan_refusals(lib):
     assert code(lambda: lib.tg_plan_prefill([-1], [4], 1, 1, 128, 1)) == lib.ERR_INVALID_ARG
     assert code(lambda: lib.tg_plan_prefill([1], [-4], 1, 1, 128, 1)) == lib.ERR_INVALID_ARG
     assert code(lambda: lib.tg_plan_prefill([1], [4], 1, 1, 128, 0)) == lib.ERR_INVALID_ARG
+    assert code(lambda: lib.tg_plan_prefill([1], [4], 1, 1, 128, 65537)) == lib.ERR_INVALID_ARG
     assert code(lambda: lib.tg_plan_prefill([1], [4], 1, 1, 128, 1, -1)) == lib.ERR_INVALID_ARG
     assert code(lambda: lib.tg_plan_prefill([1], [4], 1, 1, 64, 1)) == lib.ERR_SHAPE
     assert code(lambda: lib.tg_plan_prefill([1], [4], 2, 3, 128, 1)) == lib.ERR_SHAPE
