@@ -635,8 +635,9 @@ int tg_plan_prefill(int batch, int H, int H_q, int d, int N_CTA, const int32_t *
  *   the second product (their sum is of the unrounded ones); bf16 output.
  * Arguments (device): plan_host / plan_dev the same tg_plan_prefill bytes;
  *   q bf16 [rows][H_q][d], rows = the sum of q_len, requests one after the other;
- *   K, V bf16 [batch][H][Nmax][d], Nmax >= every kv_len, rows [0, kv_len) of each request
- *   finite (rows behind them may hold anything); scale > 0; workspace 256-byte
+ *   K, V bf16 [batch][H][Nmax][d], Nmax >= every kv_len, the rows that some token of the
+ *   pass sees finite (rows ahead of its windows and from kv_len on may hold anything: an
+ *   infinite row would reach the earlier tokens of its tile too); scale > 0; workspace 256-byte
  *   aligned, no initial contents (may be NULL if the plan needs none), one per stream;
  *   out bf16 [rows][H_q][d]; lse float32 [rows][H_q] (may be NULL).  q, K, V
  *   16-byte aligned, out 32-byte.  batch * H and Nmax fit TMA coordinates (int32). */
@@ -664,7 +665,8 @@ int tg_plan_prefix(int groups, int H, int H_q, int H_p, int P, int d, int N_CTA,
  *   empty).  Arithmetic as tg_prefill_attn.
  * Arguments (device): q bf16 [batch][H_q][d]; pool, pt_off (int64 [groups*G + 1]) and
  *   pt_ids as tg_decode_attn, list r*G + g being page group g of group r, with a
- *   list's pages covering its ntok (a shorter list counts as pages outside the pool);
+ *   list's pages covering its ntok (a shorter list counts as pages outside the pool; what a
+ *   page holds past a head's ntok does not matter here);
  *   own_out bf16 [batch][H_q][d] and own_lse float32 [batch][H_q], both or neither NULL:
  *   tg_decode_attn's out and lse over the requests' own tokens; out and lse (may be
  *   NULL) the results, which may be the same buffers as own_out and own_lse; workspace

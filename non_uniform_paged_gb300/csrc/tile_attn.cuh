@@ -18,7 +18,7 @@
 // two tiles at d = 128 and one at d = 256.
 //   warps 0-7: softmax and output, a thread per row at d = 128, two at d = 256;
 //   then two warps whose elected lanes issue the MMAs, one that streams Q, K and V by TMA, and
-//   one that clears the V rows behind the end of a context.
+//   one that clears the V rows that no row sees.
 // K and V go through a ring of eight 20 KB stages (80 keys x 128 columns each; d = 256
 // takes two per block).
 //
@@ -459,11 +459,17 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, i
 }
 
 // ------------------------------------------------------------------ MMA lanes
-// rows of the last block behind the context's end have to be cleared (pages hold finite rows)
+// Rows of V that no row of the item sees lie in its first block, ahead of the window, and in its
+// last, behind the run's end: those blocks' rows [from, to) are kept, the others cleared.
 template <bool PAGED>
-__device__ __forceinline__ bool has_tail(const tg_tile_item &it, int j1) {
-  return !PAGED && j1 * kKeys > it.kv_len;
+__device__ __forceinline__ tgi::TileRange kept_rows(const tg_tile_item &it, const ItemRange &rg, int j, const TileArgs &a) {
+  const int first = !PAGED && a.window > 0 ? it.pos0 - a.window + 1 : 0;
+  tgi::TileRange k = {0, kKeys};
+  if (j == rg.b) k.b = max(0, first - j * kKeys);
+  if (j + 1 == rg.e) k.e = min(kKeys, it.kv_len - j * kKeys);
+  return k;
 }
+__device__ __forceinline__ bool cleared(const tgi::TileRange &k) { return k.b > 0 || k.e < kKeys; }
 
 // S = Q K^T over one 128-column piece
 __device__ __forceinline__ void issue_qk(uint32_t s, uint32_t q, uint32_t k, bool accumulate) {
@@ -572,6 +578,8 @@ __device__ __forceinline__ bool pv_items(const TileArgs &a, uint32_t bars, uint3
     const ItemRange rg = item_range<D, PAGED>(it, a);
     if (rg.b >= rg.e) continue;
     ring.skip(NP);  // K(b)
+    const bool clear_first = cleared(kept_rows<PAGED>(it, rg, rg.b, a));
+    const bool clear_last = cleared(kept_rows<PAGED>(it, rg, rg.e - 1, a));
     if (D == 128) {  // the two steps ahead of a tile's first P V
       for (int j = rg.b; j < rg.b + 2; ++j) {
 #pragma unroll
@@ -591,7 +599,7 @@ __device__ __forceinline__ bool pv_items(const TileArgs &a, uint32_t bars, uint3
         ring.next();
         if (!lane_wait(bars, kFull + 8 * vs[c].at, vs[c].phase, a.status)) return false;
       }
-      if (j + 1 == rg.e && has_tail<PAGED>(it, rg.e)) {
+      if ((j == rg.b && clear_first) || (j + 1 == rg.e && clear_last)) {
         bar_arrive(bars + kToClear);
         if (!lane_wait(bars, kCleared, c_phase, a.status)) return false;
         c_phase ^= 1;
@@ -626,11 +634,11 @@ __device__ __forceinline__ bool pv_items(const TileArgs &a, uint32_t bars, uint3
 }
 
 // ------------------------------------------------------------------ clearing warp
-// Zeroes the rows of an item's last V block that lie behind the context: P is 0 there, and must
-// meet 0 whatever memory holds.  It finds the block's stages by counting the ring; the MMA lane
+// Zeroes the rows of an item's first and last V block that none of its rows sees: P is 0 there, and
+// must meet 0 whatever memory holds.  It finds the blocks' stages by counting the ring; the P V lane
 // tells it that they have landed and waits for it.
-template <int D>
-__device__ __forceinline__ void clear_tails(const TileArgs &a, uint32_t bars, uint32_t ring_at) {
+template <int D, bool PAGED>
+__device__ __forceinline__ void clear_rows(const TileArgs &a, uint32_t bars, uint32_t ring_at) {
   constexpr int NP = D / 128;
   const int lane = threadIdx.x & 31;
   uint32_t phase = 0;
@@ -638,27 +646,30 @@ __device__ __forceinline__ void clear_tails(const TileArgs &a, uint32_t bars, ui
   ItemList list;
   list.start(a);
   while (list.advance()) {
-    const ItemRange rg = item_range<D, false>(list.cur, a);
+    const ItemRange rg = item_range<D, PAGED>(list.cur, a);
     if (rg.b >= rg.e) continue;
-    ring.skip((rg.e - rg.b) * 2 * NP - NP);  // the item's last V block ends its stages
-    if (!has_tail<false>(list.cur, rg.e)) {
-      ring.skip(NP);
-      continue;
-    }
-    const int from = list.cur.kv_len - (rg.e - 1) * kKeys;
-    if (!tile_wait(bars, kToClear, phase, a.status)) return;
-    phase ^= 1;
-    for (int c = 0; c < NP; ++c) {
-      for (int i = from * 8 + lane; i < kKeys * 8; i += 32) {
-        const uint32_t at = ring_at + ring.at * kStageBytes + (uint32_t)i * 16;
-        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
-        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + kHalfBytes), "r"(0) : "memory");
+    const int n = rg.e - rg.b;
+    for (int i = 0; i < n; i = max(i + 1, n - 1)) {  // the first and the last block
+      const tgi::TileRange keep = kept_rows<PAGED>(list.cur, rg, rg.b + i, a);
+      if (!cleared(keep)) continue;
+      if (!tile_wait(bars, kToClear, phase, a.status)) return;
+      phase ^= 1;
+      Cycle<kStages> at = ring;
+      at.skip((i + 1 == n ? 2 * n - 1 : 2) * NP);  // ring order: K(b), K(b+1), V(b), ..., V(e-1)
+      for (int c = 0; c < NP; ++c) {
+        for (int k = lane; k < kKeys * 8; k += 32) {
+          if ((k >> 3) >= keep.b && (k >> 3) < keep.e) continue;
+          const uint32_t to = ring_at + at.at * kStageBytes + (uint32_t)k * 16;
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to + kHalfBytes), "r"(0) : "memory");
+        }
+        at.next();
       }
-      ring.next();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) bar_arrive(bars + kCleared);
     }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) bar_arrive(bars + kCleared);
+    ring.skip(2 * n * NP);
   }
 }
 
@@ -834,7 +845,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   } else if (warp == SW + 2) {
     load_items<D, PAGED>(&qm, &km, &vm, a, bars, q_at, ring_at);
   } else {
-    if (!PAGED) clear_tails<D>(a, bars, ring_at);
+    clear_rows<D, PAGED>(a, bars, ring_at);
   }
   tc_fence_before();
   __syncthreads();

@@ -209,3 +209,28 @@ def test_binding_refusals(lib, cuda):
     assert e.value.code == lib.ERR_SHAPE
     with pytest.raises(lib.TGError):
         p.attend(q, K, V, out, scale=0.0)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("window", [1, 50, 79, 80, 81, 300])
+def test_rows_ahead_of_every_window_hold_anything(lib, cuda, d, window):
+    """Rows that no token of the pass sees, ahead of its first window as behind its end."""
+    from non_uniform_paged_gb300.ragged import PrefillPass
+    q_len, kv_len, H, g = [1, 90, 300, 40], [700, 333, 1203, 60], 2, 4
+    for n_cta in (1, 152):
+        q, K, V = _inputs(cuda, q_len, kv_len, H, H * g, d, max(kv_len), seed=window)
+        for b in range(len(q_len)):
+            first = max(0, kv_len[b] - q_len[b] - window + 1)
+            K[b, :, :first] = float("inf")
+            V[b, :, :first] = float("nan")
+        p = PrefillPass(H, H * g, d, q_len, kv_len, window=window, n_cta=n_cta, device=cuda)
+        out, lse = torch.full_like(q, 9.0), torch.full(q.shape[:2], 9.0, device=cuda)
+        p.attend(q, K, V, out, lse)
+        at = 0
+        for b, (nq, nk) in enumerate(zip(q_len, kv_len)):
+            first = max(0, nk - nq - window + 1)
+            seen = seen_keys(nq, nk, window, cuda)[:, first:]
+            for j in range(H * g):
+                ref = attend64(q[at:at + nq, j], K[b, j // g, first:nk], V[b, j // g, first:nk], 1 / math.sqrt(d), seen)
+                check(out[at:at + nq, j], lse[at:at + nq, j], ref, f"request {b} head {j}")
+            at += nq

@@ -256,3 +256,29 @@ def test_projections_to_decode(lib, cuda, d, H_q, H):
             v = torch.cat([V[0, h, idx], Vo[b, h, :own[b]]])
             o, l, t, lt = attend64(q[b:b + 1, j], k, v, scale)
             check(out[b:b + 1, j], lse[b:b + 1, j], (o, l, 2 * t + 2.0 ** -8 * own_out[b, j].double().abs(), 4 * lt + 1e-5), (b, j))
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("P", [16, 48, 128])
+def test_rows_behind_a_count_hold_anything(lib, cuda, d, P):
+    """A head's last page past its count: neither its keys nor its values reach a result."""
+    from non_uniform_paged_gb300.ragged import SharedPrefix
+    ntok, req_off, g, H_p = [[700, 1, 129, 80], [333, 5000, 79, 81]], [0, 9, 60], 4, 2
+    G, H = 2, 4
+    s = _setup(cuda, req_off, ntok, H_p, P, d, g, seed=P)
+    for r in range(2):
+        for h in range(H):
+            n, lst = ntok[r][h], r * G + h // H_p
+            if n % P:
+                page = int(s["ids"][int(s["off"][lst]) + n // P])
+                s["pool"][page, h % H_p, 0, n % P:] = float("inf")
+                s["pool"][page, h % H_p, 1, n % P:] = float("nan")
+    for n_cta in (1, 152):
+        p = SharedPrefix(H * g, H_p, P, d, req_off, s["order"], np.array(ntok, np.int32), n_cta=n_cta, device=cuda)
+        out, lse = torch.full_like(s["q"], 9.0), torch.full(s["q"].shape[:2], 9.0, device=cuda)
+        p.attend(0, s["q"], s["pool"], s["pages"], s["off"], s["ids"], out, lse)
+        for r in range(2):
+            lo, hi = req_off[r], req_off[r + 1]
+            for j in range(H * g):
+                check(out[lo:hi, j], lse[lo:hi, j], attend64(s["q"][lo:hi, j], *s["kv"][r, j // g], 1 / math.sqrt(d)),
+                      f"group {r} head {j}")
