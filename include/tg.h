@@ -571,7 +571,7 @@ int tg_qk_norm_rope(tg_stream_t stream, int batch, int T, int H_q, int H, int d,
  * Tile plan: the work of tg_prefill_attn or tg_prefix_attn, laid out ahead of the
  * calls like the decode plan.  An item is up to 256 (d = 128) or 128 (d = 256) query
  * rows of one KV head -- consecutive tokens (requests) x the head's g query heads --
- * over a range of 128-key blocks.  Items are given to the N_CTA thread blocks longest
+ * over a range of 80-key blocks.  Items are given to the N_CTA thread blocks longest
  * first, each to the least loaded; runs of keys are cut only where that shortens the
  * longest block's work, and the cut pieces leave float32 partials that a second,
  * dependent kernel merges.  One byte buffer:
@@ -648,7 +648,7 @@ int tg_prefill_attn(tg_stream_t stream, const void *plan_host, const void *plan_
 /* tg_plan_prefix -- plan of tg_prefix_attn for one layer.
  * Inputs (host): groups of requests that share a prefix: group r is the requests
  *   [req_off[r], req_off[r+1]) (int32 [groups+1], req_off[0] = 0, ascending), batch =
- *   req_off[groups]; head_order int32 [H] and ntok int32 [groups][H], >= 0, of the layer
+ *   req_off[groups] <= 2^30; head_order int32 [H] and ntok int32 [groups][H], >= 0, of the layer
  *   as tg_build_pages gives them for `groups` requests (ntok 0: the group shares nothing).
  *   Sizes as tg_plan_prefill; H % H_p == 0, P % 16 == 0. */
 int tg_plan_prefix(int groups, int H, int H_q, int H_p, int P, int d, int N_CTA, const int32_t *req_off,

@@ -224,8 +224,12 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, i
     tc_fence_after();
     return ok;
   };
-  // both warps' values of a row, through tensor memory
-  auto exchange = [&](int column, float v) -> float {
+  // Both warps' values of a row, through tensor memory: two pairs of columns in turn, so that a
+  // value is overwritten only behind the barrier after the one ahead of its reading.
+  uint32_t turn = 0;
+  auto exchange = [&](float v) -> float {
+    const uint32_t column = turn;
+    turn ^= 2;
     tmem_st1(swap + column + half, v);
     tmem_wait_st();
     tc_fence_before();
@@ -303,7 +307,7 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, i
 #pragma unroll
           for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], s[c + k]), s[c + 4 + k]);
         const float v = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        return HALVES == 1 ? v : fmaxf(v, exchange(0, v));
+        return HALVES == 1 ? v : fmaxf(v, exchange(v));
       };
       if (__any_sync(0xffffffffu, m == -INFINITY)) {  // the same rows, so the same answer, in both warps
         const float mx = find_max();
@@ -374,7 +378,7 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, i
     const bool mine = tok < n && r < a.tq * a.g;
     const int64_t row = ((int64_t)(it.row0 + first + tok)) * a.H_q + it.h * a.g + head;
     if (HALVES == 2 && some) {
-      l += exchange(2, l);
+      l += exchange(l);
       wait(kPvDone + 8 * slot_of(count - 1), phase_of(count - 1));
     }
     const float mo = m == -INFINITY ? -INFINITY : m * sl2;  // base-2 reference

@@ -3,7 +3,7 @@
 // The same idea as the decode plan ([Tangram] "Tangram: Unlocking Non-Uniform KV Cache
 // Compression for Efficient Multi-turn LLM Serving", paper-review page, 3.3: the split of
 // the work over the thread blocks is fixed ahead of the calls): here the unit is a tile of
-// query rows against a range of 128-key blocks, because many rows share each key.
+// query rows against a range of 80-key blocks, because many rows share each key.
 //
 // Items are sorted by cost and given, longest first, to the block with the least work.  Where
 // that leaves blocks idle -- an item is longer than an even share, or each block gets so few
@@ -268,6 +268,8 @@ int plan_prefix(int groups, int H, int H_q, int H_p, int P, int d, int N_CTA, co
     count += ((int64_t)(req_off[r + 1] - req_off[r]) + step - 1) / step * H;
   }
   if (count > (1 << 24)) return fail(TG_ERR_SHAPE, "%s: %lld work items", fn, (long long)count);
+  if (req_off[groups] > (1 << 30) || (int64_t)groups * (H / H_p) >= INT32_MAX)
+    return fail(TG_ERR_SHAPE, "%s: %d requests, %d groups of %d page lists", fn, req_off[groups], groups, H / H_p);
   std::vector<int32_t> place(H, -1);
   for (int i = 0; i < H; ++i) {
     const int32_t h = head_order[i];

@@ -254,3 +254,13 @@ def test_calls_refuse_on_the_host(lib):
     assert rope(K=None) == lib.ERR_INVALID_ARG
     assert rope(qkv=odd) == lib.ERR_INVALID_ARG
     assert rope(qw=odd) == lib.ERR_INVALID_ARG
+
+
+def test_prefix_sizes_past_32_bits_are_refused(lib):
+    """As many requests as int32 holds, and more page lists: refused, not planned without work."""
+    one = np.zeros(1, np.int32)
+    for batch in (2**31 - 1, 2**30 + 1):
+        with pytest.raises(lib.TGError) as e:
+            lib.tg_plan_prefix([0, batch], one, one[None], 1, 1, 16, 128, 152)
+        assert e.value.code == -2
+    lib.tg_plan_prefix([0, 70000], one, one[None], 1, 1, 16, 128, 152)
