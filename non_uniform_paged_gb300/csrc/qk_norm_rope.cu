@@ -42,7 +42,7 @@ struct RopeArgs {
   int32_t *status;
   int batch, T, H_q, H, Nmax, rot, max_pos;
   int q_batches, kv_batches;  // batches of the query heads, and of the key (and of the value) heads
-  int parts;                  // warps of a token, each with a part of its batches
+  int parts;                  // warps of a token: one, or one for each of its batches
   float eps;
 };
 
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(32, kBlocks) qk_norm_rope_kernel(const RopeArg
   const int lane = threadIdx.x, sub = lane % LANES, side = lane / LANES;
   const int all = a.q_batches + 2 * a.kv_batches;
   const int t = blockIdx.x / a.parts, part = blockIdx.x - t * a.parts;
-  const int first = all * part / a.parts, last = all * (part + 1) / a.parts;
+  const int first = part, last = a.parts == 1 ? all : part + 1;
   // the two groups of this lane
   const bool turned = sub * 8 < a.rot;
   const int ga = !PAIRS && turned ? sub * 4 : sub * 8, gb = !PAIRS && turned ? sub * 4 + a.rot / 2 : sub * 8 + 4;

@@ -189,3 +189,10 @@ def test_binding_refusals(lib, cuda):
     for bad in (dict(qkv=qkv.float()), dict(q=q.half()), dict(start=st.long()), dict(cu_q=cu.cpu())):
         with pytest.raises(TypeError):
             lib.tg_qk_norm_rope(**dict(dict(qkv=qkv, cu_q=cu, start=st, cos_sin=None, q=q, K=K, V=K), **bad))
+
+
+def test_more_heads_than_a_product_of_batches_holds(lib, cuda):
+    """A token's batches squared pass 2^31."""
+    out = _run(lib, cuda, [1], [2], 4, 400_000, 1, 128, 128, seed=5)
+    assert out[6] == 0
+    _verify(out, [1], [2], 400_000, 1, 128, False)
