@@ -24,8 +24,9 @@ import torch
 from . import (tg_build_pages, tg_split_map, tg_query_ncta, tg_plan_decode, tg_decode_attn,
                tg_compact_topk, tg_compact_topk_workspace, tg_build_minmax, tg_page_score_topk, tg_page_score_workspace,
                tg_page_score_topk_rows, tg_rerank_rows, tg_plan_set_flags, PLAN_WAIT_TABLES,
-               SCORE_LET_NEXT_START, TilePlan, tg_plan_prefill, tg_prefill_attn, tg_plan_prefix, tg_prefix_attn, tg_tier_promote, tg_compact_chunk, tg_compact_chunk_workspace,
-               tg_sparse_layer, tg_qk_norm_rope)
+               SCORE_LET_NEXT_START, tg_tier_promote, tg_compact_chunk, tg_compact_chunk_workspace,
+               tg_sparse_layer, TilePlan, tg_qk_norm_rope, tg_plan_prefill, tg_prefill_attn, tg_plan_prefix,
+               tg_prefix_attn)
 
 BYTES_BF16 = 2
 
@@ -413,14 +414,16 @@ class PrefillPass:
         self.kv_len = np.asarray(kv_len, np.int32).reshape(-1)
         self.n_cta = int(n_cta) if n_cta else _sm_count(self.device)
         plan, self.workspace_bytes = tg_plan_prefill(self.q_len, self.kv_len, H, H_q, d, self.n_cta, window)
+        # The uploads come last: each waits for the current stream, so that whatever used this memory
+        # before is done and any stream may run the pass.
+        self.workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=self.device) \
+            if self.workspace_bytes else None
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self.plan = TilePlan(plan, torch.from_numpy(plan).to(self.device))
         cu = np.concatenate([[0], np.cumsum(self.q_len, dtype=np.int64)])
         self.rows = int(cu[-1])
         self.cu_q = torch.from_numpy(cu.astype(np.int32)).to(self.device)
         self.start = torch.from_numpy(self.kv_len - self.q_len).to(self.device)
-        self.workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=self.device) \
-            if self.workspace_bytes else None
-        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self.scale = 1.0 / math.sqrt(d)
 
     def place(self, qkv, cos_sin, q, K, V, q_weight=None, k_weight=None, eps=1e-6, pairs=False, positions=None,
@@ -448,13 +451,12 @@ class SharedPrefix:
         order = np.asarray(order, np.int32)
         order = np.broadcast_to(order, (ntok.shape[0], ntok.shape[2])) if order.ndim == 1 else order
         self.n_cta = int(n_cta) if n_cta else _sm_count(self.device)
-        self.plans, most = [], 0
-        for l in range(ntok.shape[0]):
-            plan, ws = tg_plan_prefix(req_off, order[l], ntok[l], H_q, H_p, P, d, self.n_cta)
-            self.plans.append(TilePlan(plan, torch.from_numpy(plan).to(self.device)))
-            most = max(most, ws)
+        plans = [tg_plan_prefix(req_off, order[l], ntok[l], H_q, H_p, P, d, self.n_cta) for l in range(ntok.shape[0])]
+        most = max((ws for _, ws in plans), default=0)
         self.workspace = torch.empty(most, dtype=torch.uint8, device=self.device) if most else None
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        # last, as in PrefillPass: the uploads wait for the current stream
+        self.plans = [TilePlan(plan, torch.from_numpy(plan).to(self.device)) for plan, _ in plans]
         self.scale = 1.0 / math.sqrt(d)
 
     @classmethod

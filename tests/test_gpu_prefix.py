@@ -282,3 +282,20 @@ def test_rows_behind_a_count_hold_anything(lib, cuda, d, P):
             for j in range(H * g):
                 check(out[lo:hi, j], lse[lo:hi, j], attend64(s["q"][lo:hi, j], *s["kv"][r, j // g], 1 / math.sqrt(d)),
                       f"group {r} head {j}")
+
+
+def test_made_on_one_stream_run_on_another(lib, cuda):
+    """Workspace, status and plan are there when the constructors return, whatever the current stream
+    still had to do: memory it was using a moment ago is not handed out."""
+    from non_uniform_paged_gb300.ragged import PrefillPass, SharedPrefix
+    ntok, d = np.array([[20000, 9000]], np.int32), 128
+    s = _setup(cuda, [0, 7], ntok, 2, 16, d, 4)
+    work = torch.zeros(1 << 28, dtype=torch.uint8, device=cuda)
+    for make in (lambda: SharedPrefix(8, 2, 16, d, [0, 7], s["order"], ntok, device=cuda),
+                 lambda: PrefillPass(2, 8, d, [1, 40], [9000, 4000], device=cuda)):
+        torch.cuda.synchronize()
+        for _ in range(40):
+            work.add_(1)
+        made = make()
+        assert torch.cuda.current_stream().query()
+        assert made.workspace is not None
