@@ -559,7 +559,9 @@ int tg_alloc_query(const void *state, int64_t *n_free, int64_t *n_live);
  *   Host sizes: d in {128, 256}, rot % 16 == 0, 0 <= rot <= d, eps >= 0.
  *   Rows from cu_q[batch] on are left as they are.  A token whose position is outside
  *   [0, max_pos) (with rot > 0) or whose context row is outside [0, Nmax) sets
- *   TG_STATUS_BAD_INPUT and writes nothing.  T = 0 launches nothing. */
+ *   TG_STATUS_BAD_INPUT and writes nothing.  T = 0 launches nothing.
+ * Launch: programmatic dependent launch.  The kernel may be set up while the one before
+ *   it ends, waits for it before it reads or writes anything, and lets no kernel start early. */
 #define TG_ROPE_PAIRS 0x1u
 int tg_qk_norm_rope(tg_stream_t stream, int batch, int T, int H_q, int H, int d, int Nmax, int rot, int max_pos,
                     uint32_t flags, const int32_t *cu_q, const int32_t *start, const uint16_t *qkv,
@@ -640,7 +642,9 @@ int tg_plan_prefill(int batch, int H, int H_q, int d, int N_CTA, const int32_t *
  *   infinite row would reach the earlier tokens of its tile too); scale > 0; workspace 256-byte
  *   aligned, no initial contents (may be NULL if the plan needs none), one per stream;
  *   out bf16 [rows][H_q][d]; lse float32 [rows][H_q] (may be NULL).  q, K, V
- *   16-byte aligned, out 32-byte.  batch * H and Nmax fit TMA coordinates (int32). */
+ *   16-byte aligned, out 32-byte.  batch * H and Nmax fit TMA coordinates (int32).
+ * Launch: as tg_qk_norm_rope; a plan with cut runs launches a second kernel, which joins
+ *   the pieces. */
 int tg_prefill_attn(tg_stream_t stream, const void *plan_host, const void *plan_dev, const uint16_t *q,
                     const uint16_t *K, const uint16_t *V, int Nmax, float scale, void *workspace,
                     int64_t workspace_bytes, uint16_t *out, float *lse, int32_t *dev_status);
@@ -671,7 +675,8 @@ int tg_plan_prefix(int groups, int H, int H_q, int H_p, int P, int d, int N_CTA,
  *   tg_decode_attn's out and lse over the requests' own tokens; out and lse (may be
  *   NULL) the results, which may be the same buffers as own_out and own_lse; workspace
  *   as tg_prefill_attn.  A page id outside [0, pool_pages) sets TG_STATUS_BAD_PAGE and
- *   reads as zeros.  q, pool and own_out 16-byte aligned, out 32-byte. */
+ *   reads as zeros.  q, pool and own_out 16-byte aligned, out 32-byte.
+ * Launch: as tg_prefill_attn. */
 int tg_prefix_attn(tg_stream_t stream, const void *plan_host, const void *plan_dev, const uint16_t *q,
                    const uint16_t *pool, int64_t pool_pages, const int64_t *pt_off, const int32_t *pt_ids,
                    float scale, const uint16_t *own_out, const float *own_lse, void *workspace,
