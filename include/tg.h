@@ -644,7 +644,8 @@ int tg_plan_prefill(int batch, int H, int H_q, int d, int N_CTA, const int32_t *
  *   out bf16 [rows][H_q][d]; lse float32 [rows][H_q] (may be NULL).  q, K, V
  *   16-byte aligned, out 32-byte.  batch * H and Nmax fit TMA coordinates (int32).
  * Launch: as tg_qk_norm_rope; a plan with cut runs launches a second kernel, which joins
- *   the pieces. */
+ *   the pieces.  However long a pass takes, a thread block gives up waiting only when it has
+ *   loaded no key block for 2 s (TG_STATUS_TIMEOUT; out and lse are then invalid). */
 int tg_prefill_attn(tg_stream_t stream, const void *plan_host, const void *plan_dev, const uint16_t *q,
                     const uint16_t *K, const uint16_t *V, int Nmax, float scale, void *workspace,
                     int64_t workspace_bytes, uint16_t *out, float *lse, int32_t *dev_status);

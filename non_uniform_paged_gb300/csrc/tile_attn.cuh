@@ -53,6 +53,7 @@ constexpr uint32_t kTileSmem = kQBytes + kStages * kStageBytes + 1024 + 1024;  /
 constexpr uint32_t kWeights = 160;  // first column of P (S: 0 and 80)
 constexpr uint32_t kSwap = 240;    // columns through which two warps exchange row values
 constexpr uint32_t kOut = 256;     // first column of O
+// a wait gives up when its block has loaded nothing for this long
 constexpr uint64_t kTileWaitNs = 2000000000ull;
 constexpr float kTileLn2 = 0.69314718055994531f;
 constexpr float kTileLog2e = 1.4426950408889634f;
@@ -83,7 +84,8 @@ struct TileArgs {
 //   of them takes part in the next, so none is overtaken.
 constexpr uint32_t kQFull = 0, kQEmpty = 8, kFull = 16, kEmpty = kFull + 8 * kStages, kSFull = kEmpty + 8 * kStages,
                    kPvDone = kSFull + 16, kToClear = kPvDone + 16, kCleared = kToClear + 8, kDrain = kCleared + 8,
-                   kSFree = kDrain + 16, kPReady = kSFree + 16, kTmemSlot = kPReady + 16, kAbort = kTmemSlot + 4;
+                   kSFree = kDrain + 16, kPReady = kSFree + 16, kTmemSlot = kPReady + 16, kAbort = kTmemSlot + 4,
+                   kProgress = kAbort + 4;  // stages filled, by the loader at every block of K
 constexpr uint32_t kMade = kSFull, kTaken = kSFree;  // d = 128
 
 __device__ __forceinline__ void bar_init(uint32_t at, uint32_t count) {
@@ -105,14 +107,26 @@ __device__ __forceinline__ bool bar_try(uint32_t at, uint32_t parity) {
   return done != 0;
 }
 
-// Looked at every 64 polls: whether to give up, because another warp did or the time is over.
-static __device__ __noinline__ bool tile_give_up(uint32_t bars, uint64_t *since, int32_t *status) {
+// Looked at every 64 polls: whether to give up, because another warp did, or because the loader has filled no stage for the time
+// above.  How long one wait lasts says nothing: the clearing warp waits while every item that needs no
+// clearing goes by, and a second tile's warps while items leave theirs empty.  Every other warp feeds on
+// the loader's stages or frees them, so a block in which any of them moves fills the next one soon.
+struct Patience {
+  uint64_t since;
+  uint32_t seen;
+};
+static __device__ __noinline__ bool tile_give_up(uint32_t bars, Patience *p, int32_t *status) {
   int32_t abort;
+  uint32_t progress;
   asm volatile("ld.volatile.shared.s32 %0, [%1];" : "=r"(abort) : "r"(bars + kAbort) : "memory");
   if (abort) return true;
+  asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(progress) : "r"(bars + kProgress) : "memory");
   const uint64_t now = globaltimer_ns();
-  if (*since == 0) *since = now;
-  if (now - *since < kTileWaitNs) return false;
+  if (p->since == 0 || progress != p->seen) {
+    p->since = now, p->seen = progress;
+    return false;
+  }
+  if (now - p->since < kTileWaitNs) return false;
   asm volatile("st.volatile.shared.s32 [%0], %1;" ::"r"(bars + kAbort), "r"(1) : "memory");
   report(status, TG_STATUS_TIMEOUT);
   return true;
@@ -120,9 +134,9 @@ static __device__ __noinline__ bool tile_give_up(uint32_t bars, uint64_t *since,
 // Wait for a phase of the barrier at bars + at; false when this block gave up.
 __device__ __forceinline__ bool lane_wait(uint32_t bars, uint32_t at, uint32_t parity, int32_t *status) {
   if (bar_try(bars + at, parity)) return true;
-  uint64_t since = 0;
+  Patience p = {0, 0};
   for (uint32_t n = 1; !bar_try(bars + at, parity); ++n)
-    if (!(n & 63) && tile_give_up(bars, &since, status)) return false;
+    if (!(n & 63) && tile_give_up(bars, &p, status)) return false;
   return true;
 }
 // the last wait of a block that gave up: at most 0.1 s
@@ -742,6 +756,9 @@ __device__ __forceinline__ void load_items(const CUtensorMap *qm, const CUtensor
       }
       return (id * a.H_p + it.hpos) * 2;
     };
+    auto progress = [&] {
+      asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(bars + kProgress), "r"(filled + 1) : "memory");
+    };
     // one block of K (kv 0) or V (kv 1) into the ring
     auto fill = [&](int j, int kv, int z, int row) -> bool {
 #pragma unroll
@@ -758,6 +775,7 @@ __device__ __forceinline__ void load_items(const CUtensorMap *qm, const CUtensor
             rows[i] = __shfl_sync(0xffffffffu, row, i);
           }
           if (elect_one()) {
+            if (!kv) progress();
             bar_expect(full, kStageBytes);
 #pragma unroll
             for (int i = 0; i < BOXES; ++i) {
@@ -768,6 +786,7 @@ __device__ __forceinline__ void load_items(const CUtensorMap *qm, const CUtensor
         } else if (elect_one()) {
           const CUtensorMap *m = kv ? vm : km;
           const int context = it.src * a.H + it.h;
+          if (!kv) progress();
           bar_expect(full, kStageBytes);
           tma_load_3d(dst, m, full, c * 128, j * kKeys, context);
           tma_load_3d(dst + kHalfBytes, m, full, c * 128 + 64, j * kKeys, context);
@@ -839,6 +858,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (threadIdx.x == 0) {
     for (uint32_t at = 0; at < kTmemSlot; at += 8) bar_init(bars + at, at >= kSFree ? SW * D / 256 : D == 128 && at >= kMade && at < kMade + 16 ? 2 : 1);
     asm volatile("st.volatile.shared.s32 [%0], %1;" ::"r"(bars + kAbort), "r"(0) : "memory");
+    asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(bars + kProgress), "r"(0) : "memory");
     fence_barrier_init();
   }
   // rows behind the last whole group of heads get no query: zeros, once
