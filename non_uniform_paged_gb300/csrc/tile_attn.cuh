@@ -53,8 +53,15 @@ constexpr uint32_t kTileSmem = kQBytes + kStages * kStageBytes + 1024 + 1024;  /
 constexpr uint32_t kWeights = 160;  // first column of P (S: 0 and 80)
 constexpr uint32_t kSwap = 240;    // columns through which two warps exchange row values
 constexpr uint32_t kOut = 256;     // first column of O
-// a wait gives up when its block has loaded nothing for this long
+// A wait gives up when its block has loaded nothing for this long, looked at every so many polls.  (The
+// short form is for the test of giving up: there nearly every wait does.)
+#ifdef TG_TILE_SHORT_WAIT
+constexpr uint64_t kTileWaitNs = 0;
+constexpr uint32_t kTilePolls = 1;
+#else
 constexpr uint64_t kTileWaitNs = 2000000000ull;
+constexpr uint32_t kTilePolls = 64;
+#endif
 constexpr float kTileLn2 = 0.69314718055994531f;
 constexpr float kTileLog2e = 1.4426950408889634f;
 constexpr float kMost = 65536.f;  // the reference moves when a block's weights sum to more
@@ -107,7 +114,7 @@ __device__ __forceinline__ bool bar_try(uint32_t at, uint32_t parity) {
   return done != 0;
 }
 
-// Looked at every 64 polls: whether to give up, because another warp did, or because the loader has filled no stage for the time
+// Whether to give up: because another warp did, or because the loader has filled no stage for the time
 // above.  How long one wait lasts says nothing: the clearing warp waits while every item that needs no
 // clearing goes by, and a second tile's warps while items leave theirs empty.  Every other warp feeds on
 // the loader's stages or frees them, so a block in which any of them moves fills the next one soon.
@@ -136,7 +143,7 @@ __device__ __forceinline__ bool lane_wait(uint32_t bars, uint32_t at, uint32_t p
   if (bar_try(bars + at, parity)) return true;
   Patience p = {0, 0};
   for (uint32_t n = 1; !bar_try(bars + at, parity); ++n)
-    if (!(n & 63) && tile_give_up(bars, &p, status)) return false;
+    if (!(n & (kTilePolls - 1)) && tile_give_up(bars, &p, status)) return false;
   return true;
 }
 // the last wait of a block that gave up: at most 0.1 s
@@ -548,7 +555,7 @@ __device__ __forceinline__ bool next_step(uint32_t bars, int tile, uint32_t n, i
 // about 200 clocks of work; a lane alone left it empty while it waited for the next barrier
 // (2390 clocks a block of both tiles against 1800 with two, 1456 of MMAs).
 template <int D, bool PAGED>
-__device__ __forceinline__ bool qk_items(const TileArgs &a, uint32_t bars, uint32_t q_at, uint32_t ring_at) {
+__device__ __forceinline__ void qk_items(const TileArgs &a, uint32_t bars, uint32_t q_at, uint32_t ring_at) {
   constexpr int NP = D / 128;
   Cycle<kStages> ring;
   uint32_t q_phase = 0, count[2] = {0, 0};
@@ -558,7 +565,7 @@ __device__ __forceinline__ bool qk_items(const TileArgs &a, uint32_t bars, uint3
     const tg_tile_item &it = list.cur;
     const ItemRange rg = item_range<D, PAGED>(it, a);
     if (rg.b >= rg.e) continue;
-    if (!lane_wait(bars, kQFull, q_phase, a.status)) return false;
+    if (!lane_wait(bars, kQFull, q_phase, a.status)) return;
     q_phase ^= 1;
     // ring order: K(b), K(b+1), V(b), K(b+2), V(b+1), ...
     for (int j = rg.b; j < rg.e; ++j) {
@@ -567,13 +574,13 @@ __device__ __forceinline__ bool qk_items(const TileArgs &a, uint32_t bars, uint3
       for (int c = 0; c < NP; ++c) {
         ks[c] = ring;
         ring.next();
-        if (!lane_wait(bars, kFull + 8 * ks[c].at, ks[c].phase, a.status)) return false;
+        if (!lane_wait(bars, kFull + 8 * ks[c].at, ks[c].phase, a.status)) return;
       }
       if (D == 128) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (!in_steps(rg.tile[i], j)) continue;
-          if (!next_step(bars, i, count[i]++, a.status)) return false;
+          if (!next_step(bars, i, count[i]++, a.status)) return;
           if (j < rg.tile[i].e) {
             issue_qk(i * kKeys, q_at + i * kQPiece, ring_at + ks[0].at * kStageBytes, false);
             mma_commit(bars + kMade + 8 * i);
@@ -583,7 +590,7 @@ __device__ __forceinline__ bool qk_items(const TileArgs &a, uint32_t bars, uint3
         }
       } else {
         const uint32_t slot = count[0] & 1, uses = count[0] >> 1;
-        if (uses > 0 && !lane_wait(bars, kSFree + 8 * slot, (uses - 1) & 1, a.status)) return false;
+        if (uses > 0 && !lane_wait(bars, kSFree + 8 * slot, (uses - 1) & 1, a.status)) return;
         tc_fence_after();
         ++count[0];
 #pragma unroll
@@ -601,17 +608,16 @@ __device__ __forceinline__ bool qk_items(const TileArgs &a, uint32_t bars, uint3
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (!in_steps(rg.tile[i], j)) continue;
-          if (!next_step(bars, i, count[i]++, a.status)) return false;
+          if (!next_step(bars, i, count[i]++, a.status)) return;
           bar_arrive(bars + kMade + 8 * i);
         }
       }
     }
   }
-  return true;
 }
 
 template <int D, bool PAGED>
-__device__ __forceinline__ bool pv_items(const TileArgs &a, uint32_t bars, uint32_t ring_at) {
+__device__ __forceinline__ void pv_items(const TileArgs &a, uint32_t bars, uint32_t ring_at) {
   constexpr int NP = D / 128;
   Cycle<kStages> ring;
   uint32_t c_phase = 0, count[2] = {0, 0};
@@ -629,7 +635,7 @@ __device__ __forceinline__ bool pv_items(const TileArgs &a, uint32_t bars, uint3
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (!in_steps(rg.tile[i], j)) continue;
-          if (!next_step(bars, i, count[i]++, a.status)) return false;
+          if (!next_step(bars, i, count[i]++, a.status)) return;
           bar_arrive(bars + kMade + 8 * i);
         }
       }
@@ -641,18 +647,18 @@ __device__ __forceinline__ bool pv_items(const TileArgs &a, uint32_t bars, uint3
       for (int c = 0; c < NP; ++c) {
         vs[c] = ring;
         ring.next();
-        if (!lane_wait(bars, kFull + 8 * vs[c].at, vs[c].phase, a.status)) return false;
+        if (!lane_wait(bars, kFull + 8 * vs[c].at, vs[c].phase, a.status)) return;
       }
       if ((j == rg.b && clear_first) || (j + 1 == rg.e && clear_last)) {
         bar_arrive(bars + kToClear);
-        if (!lane_wait(bars, kCleared, c_phase, a.status)) return false;
+        if (!lane_wait(bars, kCleared, c_phase, a.status)) return;
         c_phase ^= 1;
       }
       if (D == 128) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (!in_steps(rg.tile[i], j + 2)) continue;
-          if (!next_step(bars, i, count[i]++, a.status)) return false;
+          if (!next_step(bars, i, count[i]++, a.status)) return;
           if (j >= rg.tile[i].b) {
             issue_pv(kOut + i * 128, kWeights + i * (kKeys / 2), ring_at + vs[0].at * kStageBytes, j > rg.tile[i].b);
             mma_commit(bars + kMade + 8 * i);
@@ -662,7 +668,7 @@ __device__ __forceinline__ bool pv_items(const TileArgs &a, uint32_t bars, uint3
         }
       } else {
         const uint32_t slot = count[0] & 1, uses = count[0] >> 1;
-        if (!lane_wait(bars, kPReady + 8 * slot, uses & 1, a.status)) return false;
+        if (!lane_wait(bars, kPReady + 8 * slot, uses & 1, a.status)) return;
         tc_fence_after();
         ++count[0];
 #pragma unroll
@@ -674,7 +680,6 @@ __device__ __forceinline__ bool pv_items(const TileArgs &a, uint32_t bars, uint3
       for (int c = 0; c < NP; ++c) mma_commit(bars + kEmpty + 8 * vs[c].at);
     }
   }
-  return true;
 }
 
 // ------------------------------------------------------------------ clearing warp
@@ -884,12 +889,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     softmax_role<D, PAGED>(a, bars, D == 128 ? warp >> 2 : 0, D == 128 ? 0 : warp >> 2);
   } else if (warp <= SW + 1) {
     if (elect_one()) {
-      const bool done = warp == SW ? qk_items<D, PAGED>(a, bars, q_at, ring_at) : pv_items<D, PAGED>(a, bars, ring_at);
-      if (!done) {
-        // gave up: what was issued must finish before tensor memory is freed
-        mma_commit(bars + kDrain + 8 * (warp - SW));
-        bar_wait_ns(bars + kDrain + 8 * (warp - SW), 0);
-      }
+      if (warp == SW) qk_items<D, PAGED>(a, bars, q_at, ring_at);
+      else pv_items<D, PAGED>(a, bars, ring_at);
+      // What was issued must finish before tensor memory is freed and the block's shared memory goes to
+      // another.  The softmax waits for the last P V and the loader for every stage, but neither does
+      // where the block gave up, perhaps after this lane had issued its last.
+      mma_commit(bars + kDrain + 8 * (warp - SW));
+      bar_wait_ns(bars + kDrain + 8 * (warp - SW), 0);
     }
     __syncwarp();
   } else if (warp == SW + 2) {
