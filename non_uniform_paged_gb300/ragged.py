@@ -402,11 +402,32 @@ def _sm_count(dev) -> int:
     return torch.cuda.get_device_properties(dev).multi_processor_count
 
 
-class PrefillPass:
+class _OnStreams:
+    """Buffers that are made on one stream and used on others.  The allocator takes a dropped buffer
+    back in the order of the stream it was made on, so the others are told to it at their first use."""
+
+    def _own(self, *buffers):
+        self._buffers = [t for t in buffers if t is not None]
+        self._index = self._buffers[0].get_device()
+        self._streams = {torch.cuda.current_stream(self._index).cuda_stream}
+
+    def _used_on(self, stream):
+        raw = torch._C._cuda_getCurrentRawStream(self._index) if stream is None else \
+            stream if isinstance(stream, int) else stream.cuda_stream
+        if raw not in self._streams:
+            s = torch.cuda.ExternalStream(raw, self._index) if raw else torch.cuda.default_stream(self._index)
+            for t in self._buffers:
+                t.record_stream(s)
+            self._streams.add(raw)
+
+
+class PrefillPass(_OnStreams):
     """One packed prefill pass over a batch of contexts: request b brings q_len[b] tokens, the last
     of its kv_len[b] context rows (whole prompts, chunks, follow-up turns or single tokens).
     Owns the plan, shared by every layer of the pass, its workspace, and the device arrays that
-    place the tokens (cu_q, start) for tg_qk_norm_rope.  One pass runs on one stream at a time."""
+    place the tokens (cu_q, start) for tg_qk_norm_rope.  One pass runs on one stream at a time, any
+    stream; it may be dropped while its calls are queued, but not while a graph that captured them
+    is still replayed."""
 
     def __init__(self, H, H_q, d, q_len, kv_len, window=0, n_cta=None, device="cuda"):
         self.device = torch.device(device)
@@ -425,24 +446,28 @@ class PrefillPass:
         self.cu_q = torch.from_numpy(cu.astype(np.int32)).to(self.device)
         self.start = torch.from_numpy(self.kv_len - self.q_len).to(self.device)
         self.scale = 1.0 / math.sqrt(d)
+        self._own(self.plan.plan_dev, self.workspace, self.status, self.cu_q, self.start)
 
     def place(self, qkv, cos_sin, q, K, V, q_weight=None, k_weight=None, eps=1e-6, pairs=False, positions=None,
               stream=None):
         """Norm, rotate and place the pass's projections (tg_qk_norm_rope)."""
+        self._used_on(stream)
         tg_qk_norm_rope(qkv, self.cu_q, self.start, cos_sin, q, K, V, q_weight=q_weight, k_weight=k_weight, eps=eps,
                         pairs=pairs, positions=positions, dev_status=self.status, stream=stream)
 
     def attend(self, q, K, V, out, lse=None, scale=None, stream=None):
         """Causal attention of the pass's queries over their contexts, one layer (tg_prefill_attn)."""
+        self._used_on(stream)
         tg_prefill_attn(self.plan, q, K, V, self.scale if scale is None else scale, out, lse=lse,
                         workspace=self.workspace, dev_status=self.status, stream=stream)
 
 
-class SharedPrefix:
+class SharedPrefix(_OnStreams):
     """Retained tokens shared by groups of requests of a decode batch: group r is the requests
     [req_off[r], req_off[r+1]) and its tokens are the page lists of request r of a RaggedCache
     (or tg_build_pages) built for the prefixes.  order int32 [H] or [L][H], ntok int32
-    [groups][H] or [L][groups][H].  One workspace serves all layers, on one stream at a time."""
+    [groups][H] or [L][groups][H].  One workspace serves all layers, on one stream at a time; used and
+    dropped as a PrefillPass."""
 
     def __init__(self, H_q, H_p, P, d, req_off, order, ntok, n_cta=None, device="cuda"):
         self.device = torch.device(device)
@@ -458,6 +483,7 @@ class SharedPrefix:
         # last, as in PrefillPass: the uploads wait for the current stream
         self.plans = [TilePlan(plan, torch.from_numpy(plan).to(self.device)) for plan, _ in plans]
         self.scale = 1.0 / math.sqrt(d)
+        self._own(*(p.plan_dev for p in self.plans), self.workspace, self.status)
 
     @classmethod
     def of_cache(cls, cache, req_off, n_cta=None):
@@ -469,6 +495,7 @@ class SharedPrefix:
                stream=None):
         """One layer's attention over the shared tokens, merged with the requests' own (tg_prefix_attn);
         pt_off: this layer's lists (RaggedCache.list_offsets)."""
+        self._used_on(stream)
         tg_prefix_attn(self.plans[layer], q, pool, pool_pages, pt_off, pt_ids, self.scale if scale is None else scale,
                        out, lse=lse, own_out=own_out, own_lse=own_lse, workspace=self.workspace, dev_status=self.status,
                        stream=stream)
