@@ -110,6 +110,17 @@ void *pointer(PyObject *o) {
 }
 tg_stream_t stream_of(PyObject *o) { return static_cast<tg_stream_t>(pointer(o)); }
 
+// The call itself, without the interpreter's lock, as through ctypes: a launch may wait for room in
+// the stream's queue, which may wait for a host callback that needs the lock.
+template <typename F, typename... A>
+int unlocked(F fn, A... args) {
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = fn(args...);
+  Py_END_ALLOW_THREADS
+  return rc;
+}
+
 // no C++ exception reaches Python's C code
 template <typename F>
 PyObject *guarded(Py_ssize_t given, Py_ssize_t wanted, F f) {
@@ -165,15 +176,16 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     const int yes = PyObject_IsTrue(a[12]);
     if (yes < 0) throw Refused();
-    return rope_fn(stream_of(a[0]), small(batch, "batch"), small(T, "T"), small(H_q, "H_q"), small(H, "H"), small(d, "d"),
-                   small(Nmax, "Nmax"), small(rot, "rot"), small(max_pos, "max_pos"), yes ? TG_ROPE_PAIRS : 0u,
-                   arg<int32_t>(a[3], "cu_q", dev, kI32, {batch + 1}), arg<int32_t>(a[4], "start", dev, kI32, {batch}),
-                   static_cast<uint16_t *>(qkv.data_ptr()), T > 1 ? qkv.stride(0) : heads * d,
-                   opt<float>(a[9], "q_weight", dev, kF32, std::initializer_list<int64_t>{d}),
-                   opt<float>(a[10], "k_weight", dev, kF32, std::initializer_list<int64_t>{d}), (float)real(a[11]),
-                   opt<int32_t>(a[13], "positions", dev, kI32, std::initializer_list<int64_t>{T}), table,
-                   address<uint16_t>(q, "q"), address<uint16_t>(K, "K"),
-                   arg<uint16_t>(a[8], "V", dev, kBf16, {batch, H, Nmax, d}), opt<int32_t>(a[14], "dev_status", dev, kI32));
+    return unlocked(
+        rope_fn, stream_of(a[0]), small(batch, "batch"), small(T, "T"), small(H_q, "H_q"), small(H, "H"), small(d, "d"),
+        small(Nmax, "Nmax"), small(rot, "rot"), small(max_pos, "max_pos"), yes ? TG_ROPE_PAIRS : 0u,
+        arg<int32_t>(a[3], "cu_q", dev, kI32, {batch + 1}), arg<int32_t>(a[4], "start", dev, kI32, {batch}),
+        static_cast<uint16_t *>(qkv.data_ptr()), T > 1 ? qkv.stride(0) : heads * d,
+        opt<float>(a[9], "q_weight", dev, kF32, std::initializer_list<int64_t>{d}),
+        opt<float>(a[10], "k_weight", dev, kF32, std::initializer_list<int64_t>{d}), (float)real(a[11]),
+        opt<int32_t>(a[13], "positions", dev, kI32, std::initializer_list<int64_t>{T}), table, address<uint16_t>(q, "q"),
+        address<uint16_t>(K, "K"), arg<uint16_t>(a[8], "V", dev, kBf16, {batch, H, Nmax, d}),
+        opt<int32_t>(a[14], "dev_status", dev, kI32));
   });
 }
 
@@ -196,13 +208,14 @@ PyObject *prefill_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
     check_dims(K, "K", 4);
     const int64_t Nmax = K.size(2);
     const Workspace ws(a[10], dev);
-    return prefill_fn(stream_of(a[0]), hd, pointer(a[3]), arg<uint16_t>(a[4], "q", dev, kBf16, {hd->rows, hd->H_q, hd->d}),
-                      arg<uint16_t>(a[5], "K", dev, kBf16, {hd->batch, hd->H, Nmax, hd->d}),
-                      arg<uint16_t>(a[6], "V", dev, kBf16, {hd->batch, hd->H, Nmax, hd->d}), small(Nmax, "Nmax"),
-                      (float)real(a[7]), ws.at, ws.bytes,
-                      arg<uint16_t>(a[8], "out", dev, kBf16, {hd->rows, hd->H_q, hd->d}),
-                      opt<float>(a[9], "lse", dev, kF32, std::initializer_list<int64_t>{hd->rows, hd->H_q}),
-                      opt<int32_t>(a[11], "dev_status", dev, kI32));
+    return unlocked(prefill_fn, stream_of(a[0]), hd, pointer(a[3]),
+                    arg<uint16_t>(a[4], "q", dev, kBf16, {hd->rows, hd->H_q, hd->d}),
+                    arg<uint16_t>(a[5], "K", dev, kBf16, {hd->batch, hd->H, Nmax, hd->d}),
+                    arg<uint16_t>(a[6], "V", dev, kBf16, {hd->batch, hd->H, Nmax, hd->d}), small(Nmax, "Nmax"),
+                    (float)real(a[7]), ws.at, ws.bytes,
+                    arg<uint16_t>(a[8], "out", dev, kBf16, {hd->rows, hd->H_q, hd->d}),
+                    opt<float>(a[9], "lse", dev, kF32, std::initializer_list<int64_t>{hd->rows, hd->H_q}),
+                    opt<int32_t>(a[11], "dev_status", dev, kI32));
   });
 }
 
@@ -221,14 +234,15 @@ PyObject *prefix_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     const int64_t lists = (int64_t)hd->groups * (hd->H_p ? hd->H / hd->H_p : 0);
     const Workspace ws(a[14], dev);
-    return prefix_fn(stream_of(a[0]), hd, pointer(a[3]), arg<uint16_t>(a[4], "q", dev, kBf16, {hd->rows, hd->H_q, hd->d}),
-                     address<uint16_t>(pool, "pool"), pages, arg<int64_t>(a[7], "pt_off", dev, at::kLong, {lists + 1}),
-                     arg<int32_t>(a[8], "pt_ids", dev, kI32), (float)real(a[9]),
-                     opt<uint16_t>(a[10], "own_out", dev, kBf16, std::initializer_list<int64_t>{hd->rows, hd->H_q, hd->d}),
-                     opt<float>(a[11], "own_lse", dev, kF32, std::initializer_list<int64_t>{hd->rows, hd->H_q}), ws.at,
-                     ws.bytes, arg<uint16_t>(a[12], "out", dev, kBf16, {hd->rows, hd->H_q, hd->d}),
-                     opt<float>(a[13], "lse", dev, kF32, std::initializer_list<int64_t>{hd->rows, hd->H_q}),
-                     opt<int32_t>(a[15], "dev_status", dev, kI32));
+    return unlocked(
+        prefix_fn, stream_of(a[0]), hd, pointer(a[3]), arg<uint16_t>(a[4], "q", dev, kBf16, {hd->rows, hd->H_q, hd->d}),
+        address<uint16_t>(pool, "pool"), pages, arg<int64_t>(a[7], "pt_off", dev, at::kLong, {lists + 1}),
+        arg<int32_t>(a[8], "pt_ids", dev, kI32), (float)real(a[9]),
+        opt<uint16_t>(a[10], "own_out", dev, kBf16, std::initializer_list<int64_t>{hd->rows, hd->H_q, hd->d}),
+        opt<float>(a[11], "own_lse", dev, kF32, std::initializer_list<int64_t>{hd->rows, hd->H_q}), ws.at, ws.bytes,
+        arg<uint16_t>(a[12], "out", dev, kBf16, {hd->rows, hd->H_q, hd->d}),
+        opt<float>(a[13], "lse", dev, kF32, std::initializer_list<int64_t>{hd->rows, hd->H_q}),
+        opt<int32_t>(a[15], "dev_status", dev, kI32));
   });
 }
 
