@@ -512,12 +512,14 @@ _fast = None
 
 
 def _setup():
-    """(current device, its current stream, _calls), looked up once."""
+    """(current device, its current stream, _calls), looked up once; builds _calls if it is missing or
+    stale."""
     global _fast
     if _fast is None:
         import torch
         torch.cuda.init()
         lib = load()
+        _build.build_calls()
         from . import _calls
         _calls.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
                       for n in ("tg_qk_norm_rope", "tg_prefill_attn", "tg_prefix_attn")))

@@ -3,8 +3,9 @@
 Each translation unit compiles in its own nvcc process, in parallel; objects
 go to ``_build/`` at the repository root and the shared library next to this
 file.  The host code is portable C++17 (it builds the same on x86_64 and
-aarch64); the device code targets sm_103a only.  Beside it g++ builds the Python module _calls
-(binding/calls.cpp), which checks torch tensors for the calls whose host time counts.
+aarch64); the device code targets sm_103a only.  Apart from it, g++ builds the Python module _calls
+(binding/calls.cpp), which checks torch tensors for the calls whose host time counts: libtg needs
+neither torch nor that module.
 """
 from __future__ import annotations
 
@@ -43,18 +44,25 @@ def sources():
 
 def _inputs():
     return sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        glob.glob(os.path.join(INCLUDE, "*.h")) + [CALLS_SRC, os.path.abspath(__file__)]
+        glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
+
+
+def _newer(path, inputs) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in inputs)
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALLS):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
-    return all(os.path.getmtime(p) <= t for p in _inputs())
+    return _newer(LIB, _inputs())
 
 
-def build_calls() -> str:
-    """Compile the Python module _calls against the torch that will import it."""
+def calls_up_to_date() -> bool:
+    return _newer(CALLS, [CALLS_SRC, os.path.join(INCLUDE, "tg.h"), os.path.abspath(__file__)])
+
+
+def build_calls(force: bool = False) -> str:
+    """Compile the Python module _calls against the torch that will import it; returns its path."""
+    if not force and calls_up_to_date():
+        return CALLS
     spec = importlib.util.find_spec("torch")
     if spec is None or not spec.submodule_search_locations:
         raise RuntimeError("torch not found: its headers are required to build _calls")
@@ -72,7 +80,7 @@ def build_calls() -> str:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile and link libtg.so and _calls.so; returns libtg's path.  Raises on any compiler error."""
+    """Compile and link libtg.so; returns its path.  Raises on any compiler error."""
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -89,9 +97,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 2)) as ex:
-        calls = ex.submit(build_calls)
         objs = list(ex.map(compile_one, sources()))
-        calls.result()
     tmp = LIB + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -101,6 +107,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     return LIB
 
 
+def build_all(force: bool = False, verbose: bool = False):
+    """libtg.so and _calls, side by side; returns both paths."""
+    with concurrent.futures.ThreadPoolExecutor(max_workers=1) as ex:
+        calls = ex.submit(build_calls, force)
+        return build(force, verbose), calls.result()
+
+
 if __name__ == "__main__":
     import sys
-    print(build(force="--force" in sys.argv, verbose=True))
+    print(*build_all(force="--force" in sys.argv, verbose=True))
