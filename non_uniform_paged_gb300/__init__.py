@@ -11,6 +11,7 @@ fails loudly.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional
 
@@ -519,8 +520,9 @@ def _setup():
         import torch
         torch.cuda.init()
         lib = load()
-        _build.build_calls()
-        from . import _calls
+        spec = importlib.util.spec_from_file_location(__name__ + "._calls", _build.build_calls())
+        _calls = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_calls)
         _calls.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
                       for n in ("tg_qk_norm_rope", "tg_prefill_attn", "tg_prefix_attn")))
         _fast = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, _calls)

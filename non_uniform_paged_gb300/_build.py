@@ -12,7 +12,9 @@ from __future__ import annotations
 import concurrent.futures
 import glob
 import importlib.util
+import hashlib
 import os
+import re
 import shutil
 import subprocess
 import sysconfig
@@ -24,7 +26,6 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libtg.so")
 CALLS_SRC = os.path.join(PKG, "binding", "calls.cpp")
-CALLS = os.path.join(PKG, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O3", "-I", INCLUDE,
@@ -55,19 +56,33 @@ def up_to_date() -> bool:
     return _newer(LIB, _inputs())
 
 
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("torch not found: its headers are required to build _calls")
+    return spec.submodule_search_locations[0]
+
+
+def calls_path() -> str:
+    """Where _calls is for this Python and this torch: the module holds the layout of the one's tensors
+    and the other's objects, so each pair has a file of its own."""
+    where = _torch_dir()
+    with open(os.path.join(where, "version.py")) as f:
+        version = re.search(r"__version__\s*=\s*['\"]([^'\"]+)", f.read())
+    key = f"{version.group(1) if version else 'unknown'}-{hashlib.sha256(where.encode()).hexdigest()[:8]}"
+    return os.path.join(PKG, f"_calls-{key}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def calls_up_to_date() -> bool:
-    return _newer(CALLS, [CALLS_SRC, os.path.join(INCLUDE, "tg.h"), os.path.abspath(__file__)])
+    return _newer(calls_path(), [CALLS_SRC, os.path.join(INCLUDE, "tg.h"), os.path.abspath(__file__)])
 
 
 def build_calls(force: bool = False) -> str:
     """Compile the Python module _calls against the torch that will import it; returns its path."""
+    torch_dir, path = _torch_dir(), calls_path()
     if not force and calls_up_to_date():
-        return CALLS
-    spec = importlib.util.find_spec("torch")
-    if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("torch not found: its headers are required to build _calls")
-    torch_dir = spec.submodule_search_locations[0]
-    tmp = CALLS + ".tmp"
+        return path
+    tmp = f"{path}.{os.getpid()}.tmp"  # several processes may meet here at their first call
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            "-I", os.path.join(torch_dir, "include"), "-I", sysconfig.get_paths()["include"], CALLS_SRC, "-o", tmp,
            "-L", os.path.join(torch_dir, "lib"), "-Wl,-rpath," + os.path.join(torch_dir, "lib"), "-ltorch_python",
@@ -75,8 +90,8 @@ def build_calls(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on calls.cpp:\n{r.stderr}")
-    os.replace(tmp, CALLS)
-    return CALLS
+    os.replace(tmp, path)
+    return path
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:

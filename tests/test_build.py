@@ -20,8 +20,8 @@ def compilers(monkeypatch, tmp_path):
         return Done
 
     monkeypatch.setattr(_build.subprocess, "run", run)
-    for name in ("LIB", "CALLS"):
-        monkeypatch.setattr(_build, name, str(tmp_path / (name + ".so")))
+    monkeypatch.setattr(_build, "LIB", str(tmp_path / "libtg.so"))
+    monkeypatch.setattr(_build, "PKG", str(tmp_path))
     monkeypatch.setattr(_build, "BUILD_DIR", str(tmp_path))
     return commands
 
@@ -49,3 +49,21 @@ def test_calls_are_built_apart(compilers):
     assert len(compilers) == 1
     _build.build_calls(force=True)
     assert len(compilers) == 2
+
+
+def test_calls_belong_to_one_torch_and_one_python(compilers, monkeypatch, tmp_path):
+    """Another torch, another place of it or another Python: the module is built for it, beside the first."""
+    first = _build.build_calls()
+    for version, place in (("9.9.1", "a"), ("9.9.2", "a"), ("9.9.2", "b")):
+        where = tmp_path / place / "torch"
+        where.mkdir(parents=True, exist_ok=True)
+        (where / "version.py").write_text(f"__all__ = ['__version__']\n__version__ = '{version}'\n")
+        monkeypatch.setattr(_build, "_torch_dir", lambda: str(where))
+        assert not _build.calls_up_to_date()
+        assert _build.build_calls() != first and _build.calls_up_to_date()
+    config = _build.sysconfig.get_config_var
+    monkeypatch.setattr(_build.sysconfig, "get_config_var",
+                        lambda name: ".cpython-399-none.so" if name == "EXT_SUFFIX" else config(name))
+    assert not _build.calls_up_to_date()
+    assert os.path.basename(_build.calls_path()).endswith(".cpython-399-none.so")
+    assert len(compilers) == 4 and os.path.exists(first)
