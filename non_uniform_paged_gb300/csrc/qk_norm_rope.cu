@@ -151,7 +151,11 @@ __global__ void __launch_bounds__(32, kBlocks) qk_norm_rope_kernel(const RopeArg
       }
       float2 zu[2], zv[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) zu[i] = fma2(vs[i], xv[i], mul2(uc[i], xu[i])), zv[i] = fma2(us[i], xu[i], mul2(vc[i], xv[i]));
+      for (int i = 0; i < 2; ++i) zu[i] = mul2(uc[i], xu[i]), zv[i] = mul2(vc[i], xv[i]);
+      if (turned) {  // behind rot a value meets no other: 0 times an infinite one would be NaN
+#pragma unroll
+        for (int i = 0; i < 2; ++i) zu[i] = fma2(vs[i], xv[i], zu[i]), zv[i] = fma2(us[i], xu[i], zv[i]);
+      }
       if (w) {
         float2 sq = mul2(xu[0], xu[0]);
         sq = fma2(xu[1], xu[1], sq), sq = fma2(xv[0], xv[0], sq), sq = fma2(xv[1], xv[1], sq);
