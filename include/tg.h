@@ -537,9 +537,10 @@ int tg_alloc_query(const void *state, int64_t *n_free, int64_t *n_live);
 /* ------------------------------------------------------------------ p1 ---
  * tg_qk_norm_rope -- one layer's packed projections into queries and context rows:
  *   RMS norm of every query and key head (optional), position rotation, and the
- *   placement of the K and V rows, in one pass.  With one token per request it is
- *   the step ahead of tg_decode_attn, with whole prompts or chunks the one ahead of
- *   tg_prefill_attn and tg_compact_topk / tg_compact_chunk.
+ *   placement of the K and V rows in dense contexts, in one pass: the step ahead of
+ *   tg_prefill_attn and tg_compact_topk / tg_compact_chunk.  No call puts a row into a page
+ *   beside those two, so tg_decode_attn, which reads pages alone, does not see a token that is
+ *   only placed; how a new token sees itself and the retained ones is said at tg_prefix_attn.
  *   Request b owns the packed tokens [cu_q[b], cu_q[b+1]); its token cu_q[b] + i is
  *   row start[b] + i of its context.  For a query or key head x of a token:
  *     y = x / sqrt(mean(x^2) + eps) * weight          (weight NULL: y = x)
@@ -676,7 +677,13 @@ int tg_plan_prefix(int groups, int H, int H_q, int H_p, int P, int d, int N_CTA,
  *   tg_decode_attn's out and lse over the requests' own tokens; out and lse (may be
  *   NULL) the results, which may be the same buffers as own_out and own_lse; workspace
  *   as tg_prefill_attn.  A page id outside [0, pool_pages) sets TG_STATUS_BAD_PAGE and
- *   reads as zeros.  q, pool and own_out 16-byte aligned, out 32-byte.
+ *   reads as zeros.  q, pool and own_out 16-byte aligned, out 32-byte.  An own_lse below -2.3e38
+ *   counts as -inf.
+ * New tokens over retained ones (a turn, a chunk, a decode step that sees its own token): keep the
+ *   rows since the last retention in dense contexts (tg_qk_norm_rope with its positions), call
+ *   tg_prefill_attn over those, and then this call with the new tokens in the place of requests,
+ *   each request's a group of its own (req_off = its cu_q, ntok and lists = its retained tokens'):
+ *   every new token sees all of what was retained and the new ones up to itself.
  * Launch: as tg_prefill_attn. */
 int tg_prefix_attn(tg_stream_t stream, const void *plan_host, const void *plan_dev, const uint16_t *q,
                    const uint16_t *pool, int64_t pool_pages, const int64_t *pt_off, const int32_t *pt_ids,

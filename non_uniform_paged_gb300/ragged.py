@@ -465,9 +465,10 @@ class PrefillPass(_OnStreams):
 class SharedPrefix(_OnStreams):
     """Retained tokens shared by groups of requests of a decode batch: group r is the requests
     [req_off[r], req_off[r+1]) and its tokens are the page lists of request r of a RaggedCache
-    (or tg_build_pages) built for the prefixes.  order int32 [H] or [L][H], ntok int32
-    [groups][H] or [L][groups][H].  One workspace serves all layers, on one stream at a time; used and
-    dropped as a PrefillPass."""
+    (or tg_build_pages) built for the prefixes.  New tokens over their request's own retained ones
+    are such groups too (tg.h: tg_prefix_attn): req_off is then the pass's cu_q.  order int32 [H] or
+    [L][H], ntok int32 [groups][H] or [L][groups][H].  One workspace serves all layers, on one stream
+    at a time; used and dropped as a PrefillPass."""
 
     def __init__(self, H_q, H_p, P, d, req_off, order, ntok, n_cta=None, device="cuda"):
         self.device = torch.device(device)
