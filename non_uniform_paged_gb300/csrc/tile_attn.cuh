@@ -214,7 +214,6 @@ __device__ __forceinline__ ItemRange item_range(const tg_tile_item &it, const Ti
   r.e = !has1 ? r.tile[0].e : !has0 ? r.tile[1].e : max(r.tile[0].e, r.tile[1].e);
   return r;
 }
-__device__ __forceinline__ bool needs(const tgi::TileRange &r, int j) { return j >= r.b && j < r.e; }
 
 // ------------------------------------------------------------------ softmax and output warps
 __device__ __forceinline__ void store_v8(uint16_t *to, const uint32_t *w) {

@@ -8,7 +8,9 @@
 namespace tgi {
 
 constexpr int kTileRows = 128;  // rows of one MMA tile: tokens (or requests) x the g heads of a KV head
-constexpr int kTileKeys = 80;   // keys of one block (three S buffers fit beside O in tensor memory)
+// keys of one block: two S of 80 columns, two P of 40 and 4 columns of exchange fit in the 256 of tensor
+// memory beside O
+constexpr int kTileKeys = 80;
 constexpr int kPrefillPlan = 0, kPrefixPlan = 1;
 
 // tiles of one item: two at d = 128, one at d = 256 (their outputs fill tensor memory)
