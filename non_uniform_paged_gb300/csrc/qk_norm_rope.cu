@@ -29,7 +29,7 @@ using namespace tgk;
 constexpr int kSteps = 4;  // loads of a batch: heads at d = 256, pairs of heads at d = 128
 // Blocks of one warp, 24 to an SM: a block's place is free when its token is done.  For 20000 tokens
 // of 32 + 16 heads of 128, blocks of 4 warps took 92 us, of one 88; batches of 4 instead of 8 loads,
-// with 24 instead of 16 warps to an SM, 81.
+// with 24 instead of 16 warps to an SM, 81.  (At 80 registers the d = 128 forms spill 8 and 20 bytes.)
 constexpr int kBlocks = 24;
 
 struct RopeArgs {
@@ -84,7 +84,8 @@ __global__ void __launch_bounds__(32, kBlocks) qk_norm_rope_kernel(const RopeArg
   griddep_wait();  // a programmatic dependent of the kernel before it: set up while that one ends
   Head8 x0[kSteps] = {}, x1[kSteps] = {};
   load(x0, first);  // does not wait for the request's lookup
-  // the request: how many end at or before t
+  // The request: how many end at or before t, 32 at a time.  (4096 requests of one token take 34 us,
+  // 4096 tokens of one request 16.)
   int b = 0;
   for (int i = 0; i < a.batch; i += 32) {
     const int32_t end = i + lane < a.batch ? __ldg(a.cu_q + i + lane + 1) : INT32_MAX;
@@ -224,6 +225,7 @@ extern "C" int tg_qk_norm_rope(tg_stream_t stream, int batch, int T, int H_q, in
   a.batch = batch, a.T = T, a.H_q = H_q, a.H = H, a.Nmax = Nmax, a.rot = rot, a.max_pos = max_pos, a.eps = eps;
   // A warp a token, or, below 2048 tokens, one for each of its batches: 256 tokens of 32 + 16 heads of
   // 128 take 6.6 us one way and 3.2 the other, 2048 tokens 10.3 and 10.0, 4096 tokens 15.0 and 18.7.
+  // (Other head counts were not measured; with more heads a token's warp has more batches in a row.)
   const int per = kSteps * (d == 128 ? 2 : 1);
   a.q_batches = (H_q + per - 1) / per;
   a.kv_batches = (H + per - 1) / per;

@@ -450,7 +450,8 @@ __device__ __forceinline__ void softmax_role(const TileArgs &a, uint32_t bars, i
       if (HALVES == 2 && PAGED && a.own_lse) pair_sync(pair);
       if (mine && half == 0 && a.lse) a.lse[row] = total == 0.f ? -INFINITY : (top + log2f(total)) * kTileLn2;
       // A prompt's rows: two lanes exchange 16 of 32 columns, so that a store touches 16 lines of 128 bytes,
-      // not 32 (16 prompts of 64 to 4096 tokens 178 -> 172 us).  A decode batch's rows go out as they are.
+      // not 32 (16 prompts of 64 to 4096 tokens, the same inputs again at 2070 MHz: 178 -> 172 us).  A
+      // decode batch's rows go out as they are.
       const int odd = threadIdx.x & 1;
       int even_row = -1, odd_row = -1;  // of the two lanes, from the tile's first
       uint16_t *to = nullptr;
@@ -845,7 +846,8 @@ __device__ __forceinline__ void load_items(const CUtensorMap *qm, const CUtensor
 }
 
 // twelve warps, 168 registers each at launch; at d = 128 they move to the eight softmax warps
-// (384 x 168 = 256 x 208 + 128 x 88)
+// (384 x 168 = 256 x 208 + 128 x 88).  What does not fit is spilled: 12 bytes stored and 92 loaded in the
+// prompts' form, 16 and 260 in the pages'; at d = 256 nothing.
 constexpr int kTileThreads = 384;
 
 template <int D, bool PAGED>
