@@ -426,8 +426,8 @@ class PrefillPass(_OnStreams):
     of its kv_len[b] context rows (whole prompts, chunks, follow-up turns or single tokens).
     Owns the plan, shared by every layer of the pass, its workspace, and the device arrays that
     place the tokens (cu_q, start) for tg_qk_norm_rope.  One pass runs on one stream at a time, any
-    stream; it may be dropped while its calls are queued, but not while a graph that captured them
-    is still replayed."""
+    stream (one given as a handle has to outlive the pass); it may be dropped while its calls are
+    queued, but not while a graph that captured them is still replayed."""
 
     def __init__(self, H, H_q, d, q_len, kv_len, window=0, n_cta=None, device="cuda"):
         self.device = torch.device(device)
@@ -451,15 +451,15 @@ class PrefillPass(_OnStreams):
     def place(self, qkv, cos_sin, q, K, V, q_weight=None, k_weight=None, eps=1e-6, pairs=False, positions=None,
               stream=None):
         """Norm, rotate and place the pass's projections (tg_qk_norm_rope)."""
-        self._used_on(stream)
         tg_qk_norm_rope(qkv, self.cu_q, self.start, cos_sin, q, K, V, q_weight=q_weight, k_weight=k_weight, eps=eps,
                         pairs=pairs, positions=positions, dev_status=self.status, stream=stream)
+        self._used_on(stream)
 
     def attend(self, q, K, V, out, lse=None, scale=None, stream=None):
         """Causal attention of the pass's queries over their contexts, one layer (tg_prefill_attn)."""
-        self._used_on(stream)
         tg_prefill_attn(self.plan, q, K, V, self.scale if scale is None else scale, out, lse=lse,
                         workspace=self.workspace, dev_status=self.status, stream=stream)
+        self._used_on(stream)
 
 
 class SharedPrefix(_OnStreams):
@@ -496,10 +496,10 @@ class SharedPrefix(_OnStreams):
                stream=None):
         """One layer's attention over the shared tokens, merged with the requests' own (tg_prefix_attn);
         pt_off: this layer's lists (RaggedCache.list_offsets)."""
-        self._used_on(stream)
         tg_prefix_attn(self.plans[layer], q, pool, pool_pages, pt_off, pt_ids, self.scale if scale is None else scale,
                        out, lse=lse, own_out=own_out, own_lse=own_lse, workspace=self.workspace, dev_status=self.status,
                        stream=stream)
+        self._used_on(stream)
 
 
 class RerankSchedule:

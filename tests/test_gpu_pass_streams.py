@@ -106,3 +106,13 @@ def test_made_while_busy_and_run_on_another_stream(lib, cuda, case):
     side.synchronize()
     assert int(p.status.item()) == 0
     right(out, lse)
+
+
+@pytest.mark.parametrize("case", [_prompt_case, _prefix_case])
+def test_a_refused_call_uses_no_stream(lib, cuda, case):
+    make, attend, _, q = case(cuda)
+    p = make()
+    before = set(p._streams)
+    with pytest.raises(ValueError):
+        attend(p, torch.empty_like(q)[:1], None, stream=torch.cuda.Stream())
+    assert p._streams == before
