@@ -63,7 +63,7 @@ enum {
 };
 
 /* Bits of the device status word. */
-#define TG_STATUS_NONFINITE 0x1 /* a NaN score reached a top-k selection            */
+#define TG_STATUS_NONFINITE 0x1 /* a NaN score reached a top-k selection, a NaN or Inf a 4-bit page */
 #define TG_STATUS_BAD_PAGE 0x2  /* a page id outside [0, pool_pages)                */
 #define TG_STATUS_TIMEOUT 0x4   /* a copy wait gave up (about 2 s); outputs invalid */
 #define TG_STATUS_BAD_INPUT 0x8 /* a device-side size outside its limits            */
@@ -689,6 +689,124 @@ int tg_prefix_attn(tg_stream_t stream, const void *plan_host, const void *plan_d
                    const uint16_t *pool, int64_t pool_pages, const int64_t *pt_off, const int32_t *pt_ids,
                    float scale, const uint16_t *own_out, const float *own_lse, void *workspace,
                    int64_t workspace_bytes, uint16_t *out, float *lse, int32_t *dev_status);
+
+/* ------------------------------------------------------------- g1 .. g4 ---
+ * Pages that grow, and pages held in 4 bits.
+ *
+ * A cache with a reserve: every head of a request holds its ntok[b][h] retained tokens and, behind
+ * them, up to `reserve` appended ones, the same number added[b] for every head and layer.  Its page
+ * lists come from tg_reserve_pages, its decode plan from tg_plan_decode with ntok + reserve in the
+ * place of ntok.  A decode step is, per layer, tg_append_rope and then tg_decode_grown with plus = 1;
+ * after the last layer the caller adds the step's tokens to added (device int32 [batch]).
+ *
+ * Page formats.  TG_PAGES_BF16: [pages][H_p][2][P][d] bf16, as everywhere above.
+ * TG_PAGES_E2M1: [pages][H_p][P/16][d/128] tiles of 16 tokens x 128 values, 2304 bytes each.  Blocks of
+ *   16 consecutive values x of a row share a scale:
+ *     s = the e4m3 number nearest to max|x| / (6 unit), at least 2^-9 and at most 448,
+ *     code = the e2m1 number nearest to x / (unit s), at most 6 in magnitude,
+ *   both with ties to the even code; a code stands for code * s * unit, which bf16 holds exactly.
+ *   unit is a power of two in [2^-60, 2^60], one for K and one for V, the same in every call on a
+ *   pool (1 unless values leave [2^-8, 2^11]).  An infinite value is held as the largest; a NaN as
+ *   +6 s unit.  Both set TG_STATUS_NONFINITE.
+ *   In a tile, with token t, value i, block j = i / 16, and two codes to a byte, the lower i in the lower bits:
+ *     K codes   byte 64 t + i / 2              K scales  byte 2048 + 8 t + j
+ *     V codes   byte 1024 + 512 (t / 8) + 64 j + 8 (t % 8) + (i % 16) / 2
+ *     V scales  byte 2176 + 16 j + t */
+#define TG_PAGES_BF16 0
+#define TG_PAGES_E2M1 1
+#define TG_TILE4_BYTES 2304
+
+/* tg_page_bytes -- bytes of one page (host). */
+int tg_page_bytes(int format, int H_p, int P, int d, int64_t *bytes);
+
+/* tg_reserve_pages -- page lists for ntok + reserve tokens a head.  [Tangram] 3.1: a request's
+ *   footprint is fixed when it is scheduled; the tokens it may generate are part of it.
+ * Inputs (host): head_order int32 [L][H] and ntok int32 [L][batch][H] of tg_build_pages; reserve >= 0;
+ *   ntok + reserve <= 2^31 - 1 - P.
+ * Outputs (host, each may be NULL): pt_off int64 [L*batch*G + 1]; pt_ids int32 [pt_cap], numbered from 0
+ *   in (request, layer, group, page) order (TG_ERR_CAPACITY if pt_cap < *n_pages); *n_pages. */
+int tg_reserve_pages(int L, int batch, int H, int H_p, int P, const int32_t *head_order, const int32_t *ntok,
+                     int reserve, int64_t *pt_off, int32_t *pt_ids, int64_t pt_cap, int64_t *n_pages);
+
+/* tg_append_rope -- one layer's packed projections into queries and page rows: norm and rotation as
+ *   tg_qk_norm_rope, and the new tokens' K and V rows behind the tokens that their heads hold.
+ *   Token i of request b (packed token cu_q[b] + i) becomes token ntok[b][h] + added[b] + i of head h.
+ * Positions: with axes = 1, token i of request b stands at positions[cu_q[b] + i], or with positions NULL
+ *   at origin[b] + added[b] + i.  With axes 2 to 4 (time, height, width of images and video) positions
+ *   holds [T][axes] and rotation pair i turns by its axis' position, cos_sin[positions[t][axis_of[i]]][i].
+ * Arguments (device unless stated): qkv, qkv_stride, q_weight, k_weight, eps, cos_sin, max_pos, rot, flags, q
+ *   and cu_q as tg_qk_norm_rope; positions int32 [T][axes] (may be NULL with axes = 1); axis_of
+ *   (host) uint8 [rot/2], each < axes (axes > 1 only); origin int32 [batch] (positions NULL only);
+ *   head_order int32 [H], ntok int32 [batch][H], pt_off int64 [batch*G + 1] of this layer, pt_ids; added
+ *   int32 [batch] (NULL: zeros); reserve the tokens a head may hold behind its ntok;
+ *   pool: the pages, written; k_unit, v_unit: of TG_PAGES_E2M1 (any for bf16);
+ *   K, V bf16 [batch][H][Nmax][d] (both or neither NULL): if given, row start[b] + i of each head also
+ *   gets what the pages hold of the token, for tg_prefill_attn over the pass's own tokens: bf16 pages their
+ *   row, 4-bit pages the values they stand for; start int32 [batch].
+ *   qkv, q, pool, K, V, cos_sin and the weights 16-byte aligned (pt_off 8, the int32 arrays 4); q, K and V
+ *   may not overlap qkv.
+ *   Host sizes: d in {128, 256}, rot % 16 == 0, P % 16 == 0, H % H_p == 0.
+ *   4-bit pages: a K value is rounded to 4 bits from what float32 arithmetic gives, or, where that is too
+ *   close to the border of two codes or scales to tell, from float64 arithmetic: the codes are those of the formulas.
+ *   A token with added[b] < 0, added[b] + i >= reserve, a position outside [0, max_pos) (rot > 0) or a dense
+ *   row outside [0, Nmax) sets TG_STATUS_BAD_INPUT and writes nothing.  A head whose list is too short
+ *   or names a page outside [0, pool_pages) sets TG_STATUS_BAD_PAGE and none of its rows is written.
+ *   Rows from cu_q[batch] on are left as they are.  Two tokens never share a row unless lists share pages.
+ * Launch: as tg_qk_norm_rope. */
+int tg_append_rope(tg_stream_t stream, int batch, int T, int H_q, int H, int H_p, int P, int d, int rot, int max_pos,
+                   uint32_t flags, const int32_t *cu_q, const uint16_t *qkv, int64_t qkv_stride,
+                   const float *q_weight, const float *k_weight, float eps, int axes, const int32_t *positions,
+                   const uint8_t *axis_of, const int32_t *origin, const float *cos_sin, const int32_t *head_order,
+                   const int32_t *ntok, const int32_t *added, int reserve, const int64_t *pt_off,
+                   const int32_t *pt_ids, int format, float k_unit, float v_unit, void *pool, int64_t pool_pages,
+                   uint16_t *q, uint16_t *K, uint16_t *V, int Nmax, const int32_t *start, int32_t *dev_status);
+
+/* tg_quant_pages -- the retained tokens of one layer from bf16 pages (tg_compact_topk's or
+ *   tg_compact_chunk's output, for instance in pages that the next layer uses again) into 4-bit pages.
+ *   Token t < ntok[b][h] of list b*G + g in the source lists becomes the same token of that list in the
+ *   destination lists.  Rows behind the last token in its tile of 16 are written as zeros.
+ * Arguments (device): head_order int32 [H], ntok int32 [batch][H]; src bf16 pages with src_off int64
+ *   [batch*G + 1] and src_ids; dst 4-bit pages with dst_off and dst_ids; both pools 16-byte aligned and apart.
+ *   A list too short for its tokens or a page id outside its pool sets TG_STATUS_BAD_PAGE and its tile of
+ *   16 tokens is skipped.  Host sizes as tg_append_rope.
+ * Launch: as tg_qk_norm_rope. */
+int tg_quant_pages(tg_stream_t stream, int batch, int H, int H_p, int P, int d, const int32_t *head_order,
+                   const int32_t *ntok, const int64_t *src_off, const int32_t *src_ids, const uint16_t *src,
+                   int64_t src_pages, const int64_t *dst_off, const int32_t *dst_ids, void *dst, int64_t dst_pages,
+                   float k_unit, float v_unit, int32_t *dev_status);
+
+/* tg_dequant_pages -- the tokens of one layer's 4-bit pages into bf16 pages, for the calls that read those
+ *   (tg_prefix_attn over a 4-bit cache, for instance).  A head has ntok[b][h] + added[b] + plus tokens
+ *   (added NULL: zeros; added[b] + plus outside [0, reserve] sets TG_STATUS_BAD_INPUT and counts as
+ *   the nearer end).  Rows behind the last token in its page are written as zeros.  Everything else as
+ *   tg_quant_pages. */
+int tg_dequant_pages(tg_stream_t stream, int batch, int H, int H_p, int P, int d, const int32_t *head_order,
+                     const int32_t *ntok, const int32_t *added, int plus, int reserve, const int64_t *src_off,
+                     const int32_t *src_ids, const void *src, int64_t src_pages, const int64_t *dst_off,
+                     const int32_t *dst_ids, uint16_t *dst, int64_t dst_pages, float k_unit, float v_unit,
+                     int32_t *dev_status);
+
+/* tg_decode_grown -- tg_decode_attn over pages of either format and over appended tokens: a head has
+ *   ntok[b][h] + added[b] + plus tokens, read on the device, so that one plan and one captured graph
+ *   serve every step.
+ * The plan is tg_plan_decode's for ntok + reserve tokens a head.  A piece [t0, t1) of a run takes the same share of
+ *   the tokens that are there: with n tokens of c = ntok + reserve, [t0 n / c, t1 n / c) in float32, a
+ *   partition of [0, n) into pieces as even as the plan's.
+ * Arguments: plan, q, pt_off, pt_ids, scale, workspace, out, lse, dev_status, cta_time as tg_decode_attn; format
+ *   and pool (16-byte aligned); ntok int32 [batch][H] of this layer; added int32 [batch] (NULL: zeros);
+ *   plus >= 0; k_unit, v_unit as tg_append_rope.  added[b] + plus outside [0, reserve] sets
+ *   TG_STATUS_BAD_INPUT and counts as the nearer end.  Rows behind the last token may hold anything.
+ *   A list too short for its tokens, or a page id outside the pool, sets TG_STATUS_BAD_PAGE (out is then
+ *   unspecified).  out = 0 and lse = -inf for a head without tokens.
+ *   bf16 pages: arithmetic as tg_decode_attn, but that the sum of the weights is of the unrounded ones.  4-bit pages: products of f16 (codes times scales are exact
+ *   in it, q is scaled by a power of two into its range, weights are rounded to it) with float32 sums.
+ * Launch: programmatic dependent launch; waits for the kernel before it before it reads anything but the
+ *   plan, and lets the next kernel start after that. */
+int tg_decode_grown(tg_stream_t stream, const void *plan_host, const void *plan_dev, int layer, int format,
+                    const uint16_t *q, const void *pool, int64_t pool_pages, const int64_t *pt_off,
+                    const int32_t *pt_ids, const int32_t *ntok, const int32_t *added, int plus, int reserve,
+                    float scale, float k_unit, float v_unit, void *workspace, int64_t workspace_bytes,
+                    uint16_t *out, float *lse, int32_t *dev_status, int64_t *cta_time);
 
 /* tg_check_status -- synchronously read a device status word (waits for the
  *   device).  Returns TG_OK when it is 0, TG_ERR_TIMEOUT when TG_STATUS_TIMEOUT

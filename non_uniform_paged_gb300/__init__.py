@@ -26,6 +26,8 @@ __all__ = ["TGError", "load", "tg_build_pages", "tg_split_map", "tg_query_ncta",
            "tg_sparse_layer", "tg_compact_chunk", "tg_compact_chunk_workspace", "tg_tier_promote", "tg_tier_promote_background", "tg_alloc_state_bytes", "tg_alloc_init", "tg_alloc_admit", "tg_alloc_release", "tg_alloc_query",
            "tg_qk_norm_rope", "tg_plan_prefill", "tg_prefill_attn", "tg_plan_prefix", "tg_prefix_attn", "tile_header",
            "tile_items", "TilePlan", "TILE_ITEM_DTYPE", "ROPE_PAIRS",
+           "tg_page_bytes", "tg_reserve_pages", "tg_append_rope", "tg_quant_pages", "tg_dequant_pages",
+           "tg_decode_grown", "DecodePlan", "PAGES_BF16", "PAGES_E2M1", "TILE4_BYTES",
            "tg_check_status", "tg_version", "plan_header", "plan_items", "plan_lead", "WORK_ITEM_DTYPE",
            "STATUS_NONFINITE", "STATUS_BAD_PAGE", "STATUS_TIMEOUT", "STATUS_BAD_INPUT", "ERR_INVALID_ARG",
            "ERR_SHAPE", "ERR_NONFINITE", "ERR_CAPACITY", "ERR_CUDA", "ERR_TIMEOUT", "ERR_DEVICE"]
@@ -36,6 +38,8 @@ ERR_INVALID_ARG, ERR_SHAPE, ERR_NONFINITE, ERR_CAPACITY, ERR_CUDA, ERR_TIMEOUT, 
 PLAN_WAIT_TABLES = 0x1       # tg.h TG_PLAN_WAIT_TABLES
 SCORE_LET_NEXT_START = 0x1   # tg.h TG_SCORE_LET_NEXT_START
 ROPE_PAIRS = 0x1             # tg.h TG_ROPE_PAIRS
+PAGES_BF16, PAGES_E2M1 = 0, 1  # tg.h TG_PAGES_*
+TILE4_BYTES = 2304           # tg.h TG_TILE4_BYTES
 PLAN_MAGIC = 0x31504754
 TILE_MAGIC = 0x31544754
 
@@ -83,6 +87,13 @@ _SIGS = {
     "tg_prefill_attn": (_I, [_P, _P, _P, _P, _P, _P, _I, _F, _P, _L, _P, _P, _P]),
     "tg_plan_prefix": (_I, [_I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _L, _P, _P]),
     "tg_prefix_attn": (_I, [_P, _P, _P, _P, _P, _L, _P, _P, _F, _P, _P, _P, _L, _P, _P, _P]),
+    "tg_page_bytes": (_I, [_I, _I, _I, _I, _P]),
+    "tg_reserve_pages": (_I, [_I, _I, _I, _I, _I, _P, _P, _I, _P, _P, _L, _P]),
+    "tg_append_rope": (_I, [_P, _I, _I, _I, _I, _I, _I, _I, _I, _I, ctypes.c_uint32, _P, _P, _L, _P, _P, _F, _I, _P, _P, _P,
+                            _P, _P, _P, _P, _I, _P, _P, _I, _F, _F, _P, _L, _P, _P, _P, _I, _P, _P]),
+    "tg_quant_pages": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _L, _P, _P, _P, _L, _F, _F, _P]),
+    "tg_dequant_pages": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P, _I, _I, _P, _P, _P, _L, _P, _P, _P, _L, _F, _F, _P]),
+    "tg_decode_grown": (_I, [_P, _P, _P, _I, _I, _P, _P, _L, _P, _P, _P, _P, _I, _I, _F, _F, _F, _P, _L, _P, _P, _P, _P]),
     "tg_check_status": (_I, [_P, _P]),
 }
 
@@ -525,6 +536,8 @@ def _setup():
         spec.loader.exec_module(_calls)
         _calls.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
                       for n in ("tg_qk_norm_rope", "tg_prefill_attn", "tg_prefix_attn")))
+        _calls.bind_pages(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
+                            for n in ("tg_append_rope", "tg_decode_grown")))
         _fast = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, _calls)
     return _fast
 
@@ -653,6 +666,156 @@ def tg_prefix_attn(plan: TilePlan, q, pool, pool_pages: int, pt_off, pt_ids, sca
                            pool, pool_pages, pt_off, pt_ids, scale, own_out, own_lse, out, lse, workspace, dev_status)
     if rc:
         _check(rc)
+
+
+# ------------------------------------------------------------------ pages that grow, 4-bit pages
+
+def tg_page_bytes(fmt: int, H_p: int, P: int, d: int) -> int:
+    """Bytes of one page (tg.h: tg_page_bytes)."""
+    v = ctypes.c_int64(0)
+    _check(load().tg_page_bytes(int(fmt), int(H_p), int(P), int(d), ctypes.addressof(v)))
+    return v.value
+
+
+def tg_reserve_pages(head_order, ntok, H_p: int, P: int, reserve: int):
+    """Page lists for ntok + reserve tokens a head (tg.h: tg_reserve_pages): head_order int32 [L][H], ntok int32
+    [L][batch][H] -> (pt_off int64, pt_ids int32, pages)."""
+    lib = load()
+    head_order, po = _np(head_order, np.int32)
+    ntok, pn = _np(ntok, np.int32)
+    if ntok.ndim != 3 or head_order.shape != (ntok.shape[0], ntok.shape[2]):
+        raise ValueError("ntok must be [L][batch][H] and head_order [L][H]")
+    L, batch, H = ntok.shape
+    n = ctypes.c_int64(0)
+    _check(lib.tg_reserve_pages(L, batch, H, H_p, P, po, pn, reserve, None, None, 0, ctypes.addressof(n)))
+    off, ids = np.zeros(L * batch * (H // H_p) + 1, np.int64), np.zeros(max(n.value, 1), np.int32)
+    _check(lib.tg_reserve_pages(L, batch, H, H_p, P, po, pn, reserve, off.ctypes.data, ids.ctypes.data, ids.size, None))
+    return off, ids[:n.value], n.value
+
+
+class DecodePlan:
+    """A decode plan's host and device bytes with what tg_decode_grown's call checks of it, read once."""
+
+    def __init__(self, plan: np.ndarray, plan_dev):
+        if not (isinstance(plan, np.ndarray) and plan.dtype == np.uint8 and plan.flags.c_contiguous):
+            raise TypeError("plan must be the contiguous uint8 array tg_plan_decode returned")
+        if plan.size < _HEADER_DTYPE.itemsize:
+            raise ValueError("not a tg plan")
+        hd = plan_header(plan)
+        if hd["plan_bytes"] != plan.size:
+            raise ValueError(f"plan has {plan.size} bytes, its header says {hd['plan_bytes']}")
+        import torch
+        self.dev_ptr = _dev(plan_dev, torch.uint8, "plan_dev")
+        if plan_dev is None or plan_dev.numel() != plan.size:
+            raise ValueError(f"plan_dev must hold the plan's {plan.size} bytes")
+        self._host, self.plan_dev, self.device = plan, plan_dev, plan_dev.get_device()
+        self.host_ptr = plan.ctypes.data
+        self.header = hd
+
+
+def tg_append_rope(qkv, cu_q, cos_sin, q, pool, pool_pages: int, head_order, ntok, added, reserve: int, pt_off, pt_ids,
+                   H_p: int, P: int, fmt: int = PAGES_BF16, k_unit: float = 1.0, v_unit: float = 1.0, q_weight=None,
+                   k_weight=None, eps=1e-6, pairs=False, positions=None, axis_of=None, origin=None, K=None, V=None,
+                   start=None, dev_status=None, stream=None):
+    """Norm, rotation and the new tokens' rows behind the retained ones in the pages (tg.h: tg_append_rope).
+    qkv [T][H_q + 2H][d] (rows may be strided), q [T][H_q][d], cos_sin [max_pos][rot/2][2] (None: no rotation),
+    positions [T] or [T][axes], axis_of the axis of each pair (host), ntok [batch][H], K, V [batch][H][Nmax][d]."""
+    device, current, calls = _fast or _setup()
+    dev = device()
+    if axis_of is not None and not isinstance(axis_of, bytes):
+        axis_of = bytes(axis_of)
+    rc = calls.append_rope(current(dev) if stream is None else _raw_stream(stream), dev, qkv, cu_q, cos_sin, q, pool,
+                           pool_pages, head_order, ntok, added, reserve, pt_off, pt_ids, H_p, P, fmt, k_unit, v_unit,
+                           q_weight, k_weight, eps, pairs, positions, axis_of, origin, K, V, start, dev_status)
+    if rc:
+        _check(rc)
+
+
+def tg_decode_grown(plan: DecodePlan, layer: int, fmt: int, q, pool, pool_pages: int, pt_off, pt_ids, ntok, added, plus: int,
+                    reserve: int, scale: float, out, lse=None, k_unit: float = 1.0, v_unit: float = 1.0, workspace=None,
+                    dev_status=None, cta_time=None, stream=None):
+    """Decode attention over retained and appended tokens (tg.h: tg_decode_grown); asynchronous.
+    q, out [batch][H_q][d], ntok [batch][H], lse [batch][H_q]."""
+    device, current, calls = _fast or _setup()
+    dev = device()
+    if plan.device != dev:
+        raise _plan_elsewhere(plan, dev)
+    rc = calls.decode_grown(current(dev) if stream is None else _raw_stream(stream), dev, plan.host_ptr, plan.dev_ptr, layer,
+                            fmt, q, pool, pool_pages, pt_off, pt_ids, ntok, added, plus, reserve, scale, k_unit, v_unit,
+                            out, lse, workspace, dev_status, cta_time)
+    if rc:
+        _check(rc)
+
+
+def _here(*tensors):
+    """The tensors' device is the current one: their pointers are of it."""
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+
+
+def _pool_pages(t, name, page_bytes, pages):
+    if t.numel() * t.element_size() < pages * page_bytes:
+        raise ValueError(f"{name} holds {t.numel() * t.element_size() // page_bytes} pages, not {pages}")
+
+
+def _lists(t, name, n):
+    if t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} entries, not {n}")
+
+
+def _convert_args(head_order, ntok, src_off, src_ids, src, src_pages, dst_off, dst_ids, dst, dst_pages, H_p, P, d, dev_status,
+                  to4):
+    """What both conversions check of their tensors -> (batch, H)."""
+    import torch
+    for t, n in ((head_order, "head_order"), (ntok, "ntok"), (src_off, "src_off"), (src_ids, "src_ids"), (src, "src"),
+                 (dst_off, "dst_off"), (dst_ids, "dst_ids"), (dst, "dst")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{n} must be a CUDA torch.Tensor")
+    if ntok.dim() != 2:
+        raise ValueError("ntok must be [batch][H]")
+    batch, H = ntok.shape
+    _here(head_order, ntok, src_off, src_ids, src, dst_off, dst_ids, dst, dev_status)
+    _lists(head_order, "head_order", H)
+    if H_p > 0:
+        for t, n in ((src_off, "src_off"), (dst_off, "dst_off")):
+            _lists(t, n, batch * (H // H_p) + 1)
+    _pool_pages(src, "src", tg_page_bytes(PAGES_BF16 if to4 else PAGES_E2M1, H_p, P, d), src_pages)
+    _pool_pages(dst, "dst", tg_page_bytes(PAGES_E2M1 if to4 else PAGES_BF16, H_p, P, d), dst_pages)
+    return batch, H
+
+
+def tg_quant_pages(head_order, ntok, H_p, P, d, src_off, src_ids, src, src_pages, dst_off, dst_ids, dst, dst_pages,
+                   k_unit=1.0, v_unit=1.0, dev_status=None, stream=None):
+    """Retained tokens of one layer from bf16 pages into 4-bit pages (tg.h: tg_quant_pages): src bf16, dst uint8."""
+    import torch
+    batch, H = _convert_args(head_order, ntok, src_off, src_ids, src, src_pages, dst_off, dst_ids, dst, dst_pages, H_p, P, d,
+                             dev_status, True)
+    _check(load().tg_quant_pages(_stream(stream), batch, H, H_p, P, d, _dev(head_order, torch.int32, "head_order"),
+                                 _dev(ntok, torch.int32, "ntok"), _dev(src_off, torch.int64, "src_off"),
+                                 _dev(src_ids, torch.int32, "src_ids"), _dev(src, torch.bfloat16, "src"), int(src_pages),
+                                 _dev(dst_off, torch.int64, "dst_off"), _dev(dst_ids, torch.int32, "dst_ids"),
+                                 _dev(dst, torch.uint8, "dst"), int(dst_pages), float(k_unit), float(v_unit),
+                                 _dev(dev_status, torch.int32, "dev_status")))
+
+
+def tg_dequant_pages(head_order, ntok, H_p, P, d, src_off, src_ids, src, src_pages, dst_off, dst_ids, dst, dst_pages,
+                     added=None, plus=0, reserve=0, k_unit=1.0, v_unit=1.0, dev_status=None, stream=None):
+    """Tokens of one layer from 4-bit pages into bf16 pages (tg.h: tg_dequant_pages): src uint8, dst bf16."""
+    import torch
+    batch, H = _convert_args(head_order, ntok, src_off, src_ids, src, src_pages, dst_off, dst_ids, dst, dst_pages, H_p, P, d,
+                             dev_status, False)
+    if added is not None:
+        _here(added)
+        _lists(added, "added", batch)
+    _check(load().tg_dequant_pages(_stream(stream), batch, H, H_p, P, d, _dev(head_order, torch.int32, "head_order"),
+                                   _dev(ntok, torch.int32, "ntok"), _dev(added, torch.int32, "added"), int(plus),
+                                   int(reserve), _dev(src_off, torch.int64, "src_off"), _dev(src_ids, torch.int32, "src_ids"),
+                                   _dev(src, torch.uint8, "src"), int(src_pages), _dev(dst_off, torch.int64, "dst_off"),
+                                   _dev(dst_ids, torch.int32, "dst_ids"), _dev(dst, torch.bfloat16, "dst"), int(dst_pages),
+                                   float(k_unit), float(v_unit), _dev(dev_status, torch.int32, "dev_status")))
 
 
 def tg_check_status(dev_status) -> int:

@@ -1,10 +1,11 @@
 // Calls of a decode step's latency path without ctypes: checks of the tensors and the call into
-// libtg, for tg_qk_norm_rope, tg_prefill_attn and tg_prefix_attn.  Marshalling only, like the
+// libtg, for tg_qk_norm_rope, tg_prefill_attn and tg_prefix_attn, and for tg_append_rope and
+// tg_decode_grown.  Marshalling only, like the
 // ctypes binding beside it; a dozen tensors checked from Python and passed through ctypes took
 // 9 us a call, more than the kernels of a small step.
 //
 // Built as the Python module _calls.  The addresses of the libtg functions come from the ctypes
-// handle (bind), so that there is one libtg and one way of loading it.
+// handle (bind, bind_pages), so that there is one libtg and one way of loading it.
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "../../include/tg.h"
@@ -19,6 +20,10 @@ using Prefix = decltype(&tg_prefix_attn);
 Rope rope_fn = nullptr;
 Prefill prefill_fn = nullptr;
 Prefix prefix_fn = nullptr;
+using Append = decltype(&tg_append_rope);
+using Grown = decltype(&tg_decode_grown);
+Append append_fn = nullptr;
+Grown grown_fn = nullptr;
 
 struct Refused {};  // a Python exception is set
 
@@ -246,12 +251,134 @@ PyObject *prefix_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// bind_pages(append, grown): addresses of the libtg functions
+PyObject *bind_pages(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 2, [&] {
+    append_fn = reinterpret_cast<Append>(pointer(a[0]));
+    grown_fn = reinterpret_cast<Grown>(pointer(a[1]));
+    return 0;
+  });
+}
+
+// A pool of `pages` pages of the format: bf16, or bytes for 4-bit pages.
+void *pool_arg(PyObject *o, int64_t dev, int format, int64_t pages, int64_t H_p, int64_t P, int64_t d) {
+  const at::Tensor &pool = tensor(o, "pool", dev);
+  const bool bf16 = format == TG_PAGES_BF16;
+  check_type(pool, "pool", bf16 ? kBf16 : at::kByte);
+  const int64_t page = bf16 ? H_p * 2 * P * d : H_p * (P / 16) * (d / 128) * TG_TILE4_BYTES;
+  const int64_t held = page > 0 ? pool.numel() / page : 0;
+  if (pages > held) {
+    PyErr_Format(PyExc_ValueError, "pool holds %lld pages, not %lld", (long long)held, (long long)pages);
+    throw Refused();
+  }
+  return address<void>(pool, "pool");
+}
+
+// (stream, device, qkv, cu_q, cos_sin, q, pool, pool_pages, head_order, ntok, added, reserve, pt_off, pt_ids, H_p, P,
+//  format, k_unit, v_unit, q_weight, k_weight, eps, pairs, positions, axis_of (bytes), origin, K, V, start, dev_status)
+PyObject *append_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 30, [&] {
+    const int64_t dev = integer(a[1]);
+    const at::Tensor &qkv = tensor(a[2], "qkv", dev), &q = tensor(a[5], "q", dev), &ntok = tensor(a[9], "ntok", dev);
+    check_dims(q, "q", 3), check_dims(ntok, "ntok", 2);
+    const int64_t T = q.size(0), H_q = q.size(1), d = q.size(2), batch = ntok.size(0), H = ntok.size(1);
+    const int64_t heads = H_q + 2 * H, pages = integer(a[7]);
+    const int H_p = small(integer(a[14]), "H_p"), P = small(integer(a[15]), "P"), format = small(integer(a[16]), "format");
+    const int64_t lists = H_p > 0 ? batch * (H / H_p) : 0;
+    check_type(qkv, "qkv", kBf16), check_type(q, "q", kBf16);
+    check_shape(qkv, "qkv", {T, heads, d});
+    if (T && (qkv.stride(2) != 1 || qkv.stride(1) != d)) {
+      PyErr_SetString(PyExc_ValueError, "qkv must have contiguous token rows");
+      throw Refused();
+    }
+    int64_t max_pos = 0, rot = 0, axes = 1;
+    const float *table = nullptr;
+    if (a[4] != Py_None) {
+      const at::Tensor &t = tensor(a[4], "cos_sin", dev);
+      check_dims(t, "cos_sin", 3);
+      max_pos = t.size(0), rot = 2 * t.size(1);
+      table = arg<float>(a[4], "cos_sin", dev, kF32, {max_pos, t.size(1), 2});
+    }
+    const int32_t *positions = nullptr;
+    if (a[23] != Py_None) {
+      const at::Tensor &t = tensor(a[23], "positions", dev);
+      if (t.dim() == 2) axes = t.size(1);
+      positions = t.dim() == 2 ? arg<int32_t>(a[23], "positions", dev, kI32, {T, axes})
+                               : arg<int32_t>(a[23], "positions", dev, kI32, {T});
+    }
+    const uint8_t *axis_of = nullptr;
+    if (a[24] != Py_None) {
+      if (!PyBytes_Check(a[24]) || PyBytes_GET_SIZE(a[24]) != rot / 2) {
+        PyErr_Format(PyExc_ValueError, "axis_of must have an axis for each of the %lld pairs", (long long)(rot / 2));
+        throw Refused();
+      }
+      axis_of = reinterpret_cast<const uint8_t *>(PyBytes_AS_STRING(a[24]));
+    }
+    int64_t Nmax = 0;
+    uint16_t *K = nullptr, *V = nullptr;
+    if (a[26] != Py_None) {
+      const at::Tensor &t = tensor(a[26], "K", dev);
+      check_dims(t, "K", 4);
+      Nmax = t.size(2);
+      K = arg<uint16_t>(a[26], "K", dev, kBf16, {batch, H, Nmax, d});
+    }
+    if (a[27] != Py_None) V = arg<uint16_t>(a[27], "V", dev, kBf16, {batch, H, Nmax, d});
+    const int yes = PyObject_IsTrue(a[22]);
+    if (yes < 0) throw Refused();
+    return unlocked(
+        append_fn, stream_of(a[0]), small(batch, "batch"), small(T, "T"), small(H_q, "H_q"), small(H, "H"), H_p, P,
+        small(d, "d"), small(rot, "rot"), small(max_pos, "max_pos"), yes ? TG_ROPE_PAIRS : 0u,
+        arg<int32_t>(a[3], "cu_q", dev, kI32, {batch + 1}), static_cast<const uint16_t *>(qkv.data_ptr()),
+        T > 1 ? qkv.stride(0) : heads * d, opt<float>(a[19], "q_weight", dev, kF32, std::initializer_list<int64_t>{d}),
+        opt<float>(a[20], "k_weight", dev, kF32, std::initializer_list<int64_t>{d}), (float)real(a[21]),
+        small(axes, "axes"), positions, axis_of,
+        opt<int32_t>(a[25], "origin", dev, kI32, std::initializer_list<int64_t>{batch}), table,
+        arg<int32_t>(a[8], "head_order", dev, kI32, {H}), arg<int32_t>(a[9], "ntok", dev, kI32),
+        opt<int32_t>(a[10], "added", dev, kI32, std::initializer_list<int64_t>{batch}), small(integer(a[11]), "reserve"),
+        arg<int64_t>(a[12], "pt_off", dev, at::kLong, {lists + 1}), arg<int32_t>(a[13], "pt_ids", dev, kI32), format,
+        (float)real(a[17]), (float)real(a[18]), pool_arg(a[6], dev, format, pages, H_p, P, d), pages,
+        address<uint16_t>(q, "q"), K, V, small(Nmax, "Nmax"),
+        opt<int32_t>(a[28], "start", dev, kI32, std::initializer_list<int64_t>{batch}),
+        opt<int32_t>(a[29], "dev_status", dev, kI32));
+  });
+}
+
+// (stream, device, plan host, plan device, layer, format, q, pool, pool_pages, pt_off, pt_ids, ntok, added, plus, reserve,
+//  scale, k_unit, v_unit, out, lse, workspace, dev_status, cta_time)
+PyObject *decode_grown(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 23, [&] {
+    const int64_t dev = integer(a[1]), pages = integer(a[8]);
+    const tg_plan_header *hd = static_cast<const tg_plan_header *>(pointer(a[2]));
+    const int format = small(integer(a[5]), "format");
+    const int64_t lists = (int64_t)hd->batch * hd->G;
+    const Workspace ws(a[20], dev);
+    return unlocked(
+        grown_fn, stream_of(a[0]), hd, pointer(a[3]), small(integer(a[4]), "layer"), format,
+        arg<uint16_t>(a[6], "q", dev, kBf16, {hd->batch, hd->H_q, hd->d}),
+        pool_arg(a[7], dev, format, pages, hd->H_p, hd->P, hd->d), pages,
+        arg<int64_t>(a[9], "pt_off", dev, at::kLong, {lists + 1}), arg<int32_t>(a[10], "pt_ids", dev, kI32),
+        arg<int32_t>(a[11], "ntok", dev, kI32, {hd->batch, hd->H}),
+        opt<int32_t>(a[12], "added", dev, kI32, std::initializer_list<int64_t>{hd->batch}), small(integer(a[13]), "plus"),
+        small(integer(a[14]), "reserve"), (float)real(a[15]), (float)real(a[16]), (float)real(a[17]), ws.at, ws.bytes,
+        arg<uint16_t>(a[18], "out", dev, kBf16, {hd->batch, hd->H_q, hd->d}),
+        opt<float>(a[19], "lse", dev, kF32, std::initializer_list<int64_t>{hd->batch, hd->H_q}),
+        opt<int32_t>(a[21], "dev_status", dev, kI32),
+        opt<int64_t>(a[22], "cta_time", dev, at::kLong, std::initializer_list<int64_t>{2 * (int64_t)hd->N_CTA}));
+  });
+}
+
 PyMethodDef methods[] = {{"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind)), METH_FASTCALL, nullptr},
                          {"qk_norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(qk_norm_rope)),
                           METH_FASTCALL, nullptr},
                          {"prefill_attn", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(prefill_attn)),
                           METH_FASTCALL, nullptr},
                          {"prefix_attn", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(prefix_attn)),
+                          METH_FASTCALL, nullptr},
+                         {"bind_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind_pages)),
+                          METH_FASTCALL, nullptr},
+                         {"append_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append_rope)),
+                          METH_FASTCALL, nullptr},
+                         {"decode_grown", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(decode_grown)),
                           METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

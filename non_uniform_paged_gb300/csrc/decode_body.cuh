@@ -41,7 +41,26 @@ struct DecodeArgs {
   const uint8_t *row_due;    // [batch*H]: only rows marked 1 are waited for (NULL: every row)
   uint64_t wait_ns;          // limit of each row-ready wait
   int epoch;
+  // grown runs (GROWN): tokens of a head, those appended behind them and how many may be (else unused)
+  const int32_t *ntok, *added;
+  int plus, reserve;
 };
+
+// Item `it` of a plan made for ntok + reserve tokens a head, over the tokens that are there: [t0, t1) becomes
+// the same share of them.  The product with one factor a head is monotone in t, so that pieces next to each
+// other stay so, whatever float32 rounds.
+__device__ __forceinline__ tg_work_item grown_item(const DecodeArgs &a, tg_work_item it) {
+  const int n0 = max(__ldcg(a.ntok + it.b * a.H + it.h), 0);
+  const int64_t asked = (int64_t)(a.added ? __ldcg(a.added + it.b) : 0) + a.plus;
+  const int extra = (int)min(max(asked, (int64_t)0), (int64_t)a.reserve);
+  if (extra != asked) report(a.status, TG_STATUS_BAD_INPUT);
+  const int64_t cap = (int64_t)n0 + a.reserve;
+  const int n = n0 + extra;
+  const float f = cap > 0 ? (float)n / (float)cap : 0.f;
+  it.t0 = it.t0 >= cap ? n : min(n, (int)((float)it.t0 * f));
+  it.t1 = it.t1 >= cap ? n : min(n, (int)((float)it.t1 * f));
+  return it;
+}
 
 // wait (bounded) until *flag == epoch; false after the time limit
 __device__ __forceinline__ bool wait_flag(const int32_t *flag, int epoch, uint64_t limit_ns) {
@@ -115,6 +134,181 @@ __device__ __forceinline__ void epilogue_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
 }
 
+// The epilogue warps of a CTA (see decode_body).  A piece of a grown run may hold no token: it leaves a
+// partial of no weight.
+template <int D, int NW, int NE, bool GROWN, typename GetItem>
+__device__ __forceinline__ void decode_epilogue(const DecodeArgs &a, GetItem get_item, int n_items, const float *comb_m,
+                                                const float *comb_l, const float *comb_o, int cfl, int ostride,
+                                                float *fac, float *s_mm, float *s_ll, int *flag, volatile int *s_dead,
+                                                uint64_t *full, uint64_t *empty, const uint64_t *s_t0) {
+  constexpr int NS = NW * 32, NET = NE * 32;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x;
+  // 2^(m - M), the weight of a part with maximum m; without tokens anywhere M is -inf
+  auto weight = [](float m, float M) -> float { return GROWN && M == -INFINITY ? 0.f : ex2(m - M); };
+  auto mean = [](float O, float L) -> float { return GROWN && L == 0.f ? 0.f : O / L; };
+  const int etid = tid - NS, ew = warp - NW;
+  // the workspace (merge counters, partials) and the outputs may still be in use by the
+  // previous decode launch in the stream: wait for it before the first write
+  griddep_wait();
+  for (int k = 0; k < n_items; ++k) {
+    const tg_work_item it = get_item(k);
+    const int hb = k & 1, use = k >> 1;
+    if (!*s_dead && !mbar_wait_sleep(&full[hb], (uint32_t)(use & 1), kWaitLimitNs)) {
+      if (etid == 0) report(a.status, TG_STATUS_TIMEOUT);
+      *s_dead = 1;
+    }
+    const float *cm = comb_m + hb * NW * 8, *cl = comb_l + hb * NW * 8, *co = comb_o + hb * cfl;
+    const size_t out_row0 = (size_t)it.b * a.H_q + (size_t)it.h * a.g;
+    if (it.t1 <= it.t0 && (!GROWN || it.nparts == 1)) {  // a head with no token
+      for (int e = etid; e < a.g * D; e += NET) {
+        a.out[(out_row0 + e / D) * D + e % D] = 0;
+        if (e % D == 0 && a.lse) a.lse[out_row0 + e / D] = -INFINITY;
+      }
+    } else {
+      const int slot = it.slot0 + it.part;
+      for (int e = etid; e < a.g * D; e += NET) {
+        const int hd = e / D, dd = e % D;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, cm[w * 8 + hd]);
+        float Ls = 0.f, O = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          const float f = weight(cm[w * 8 + hd], M);
+          Ls += cl[w * 8 + hd] * f;
+          O += co[(w * a.g + hd) * ostride + dd] * f;
+        }
+        if (it.nparts == 1) {
+          __nv_bfloat16 v = __float2bfloat16_rn(mean(O, Ls));
+          a.out[(out_row0 + hd) * D + dd] = *reinterpret_cast<uint16_t *>(&v);
+          if (dd == 0 && a.lse) a.lse[out_row0 + hd] = (M + log2f(Ls)) * kLn2;
+        } else {
+          a.ws_o[((size_t)slot * a.g + hd) * D + dd] = O;
+          if (dd == 0) {
+            a.ws_ml[((size_t)slot * a.g + hd) * 2] = M;
+            a.ws_ml[((size_t)slot * a.g + hd) * 2 + 1] = Ls;
+          }
+        }
+      }
+    }
+    mbar_arrive(&empty[hb]);  // (release: this thread's reads of the buffer come first)
+    if ((GROWN || it.t1 > it.t0) && it.nparts > 1) {
+      __threadfence();
+      epilogue_sync<NET>();
+      if (etid == 0) {
+        const int prev = atomicAdd(&a.counters[it.b * a.H + it.h], 1);
+        *flag = prev == it.nparts - 1;
+      }
+      epilogue_sync<NET>();
+      if (*flag) {  // the last CTA of this run merges every partial
+        __threadfence();
+        const int np = it.nparts, g = a.g;
+        const float *pml = a.ws_ml + (size_t)it.slot0 * g * 2;  // [nparts][g][2]
+        const float *po = a.ws_o + (size_t)it.slot0 * g * D;     // [nparts][g][D]
+        if (np * g <= kFacMax) {
+          // factors 2^(m_p - M) of every part go to shared memory; per head, one warp gathers
+          // M and L with its lanes striding over the parts (independent loads).  Up to 64 parts,
+          // each lane reads its (m, l) pairs once and keeps them in registers
+          for (int hh = ew; hh < g; hh += NE) {
+            float M = -INFINITY, Ls = 0.f;
+            if (np <= 64) {
+              float2 ml[2];
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const int p = lane + 32 * j;
+                ml[j] = p < np ? __ldcg(reinterpret_cast<const float2 *>(pml + ((size_t)p * g + hh) * 2))
+                               : make_float2(-INFINITY, 0.f);
+                M = fmaxf(M, ml[j].x);
+              }
+#pragma unroll
+              for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const int p = lane + 32 * j;
+                if (p < np) {
+                  const float f = weight(ml[j].x, M);
+                  fac[p * g + hh] = f;
+                  Ls += ml[j].y * f;
+                }
+              }
+            } else {
+              for (int p = lane; p < np; p += 32) M = fmaxf(M, __ldcg(pml + ((size_t)p * g + hh) * 2));
+#pragma unroll
+              for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+              for (int p = lane; p < np; p += 32) {
+                const float f = weight(__ldcg(pml + ((size_t)p * g + hh) * 2), M);
+                fac[p * g + hh] = f;
+                Ls += __ldcg(pml + ((size_t)p * g + hh) * 2 + 1) * f;
+              }
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, off);
+            if (lane == 0) {
+              s_mm[hh] = M;
+              s_ll[hh] = Ls;
+            }
+          }
+          epilogue_sync<NET>();
+          // O = sum_p o_p 2^(m_p - M), parts in order.  A thread takes four consecutive outputs
+          // of one head (16-byte loads; partial rows are 16-byte aligned), sixteen parts per
+          // batch in flight
+          for (int e = 4 * etid; e < g * D; e += 4 * NET) {
+            const int hd = e / D, dd = e % D;
+            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int p = 0; p < np; p += 16) {
+              float4 v[16];
+#pragma unroll
+              for (int u = 0; u < 16; ++u)
+                v[u] = p + u < np ? __ldcg(reinterpret_cast<const float4 *>(po + (size_t)(p + u) * g * D + e))
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+              for (int u = 0; u < 16; ++u)
+                if (p + u < np) {
+                  const float f = fac[(p + u) * g + hd];
+                  O.x += v[u].x * f;
+                  O.y += v[u].y * f;
+                  O.z += v[u].z * f;
+                  O.w += v[u].w * f;
+                }
+            }
+            const float Ls = s_ll[hd];
+            uint16_t *orow = a.out + (out_row0 + hd) * D + dd;
+            const float ov[4] = {O.x, O.y, O.z, O.w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              __nv_bfloat16 v = __float2bfloat16_rn(mean(ov[c], Ls));
+              orow[c] = *reinterpret_cast<uint16_t *>(&v);
+            }
+            if (dd == 0 && a.lse) a.lse[out_row0 + hd] = (s_mm[hd] + log2f(s_ll[hd])) * kLn2;
+          }
+        } else {  // more parts than the factor buffer holds: straight loops
+          for (int e = etid; e < g * D; e += NET) {
+            const int hd = e / D, dd = e % D;
+            float M = -INFINITY;
+            for (int p = 0; p < np; ++p) M = fmaxf(M, __ldcg(pml + ((size_t)p * g + hd) * 2));
+            float Ls = 0.f, O = 0.f;
+            for (int p = 0; p < np; ++p) {
+              const float f = weight(__ldcg(pml + ((size_t)p * g + hd) * 2), M);
+              Ls += __ldcg(pml + ((size_t)p * g + hd) * 2 + 1) * f;
+              O += __ldcg(po + (size_t)p * g * D + e) * f;
+            }
+            __nv_bfloat16 v = __float2bfloat16_rn(mean(O, Ls));
+            a.out[(out_row0 + hd) * D + dd] = *reinterpret_cast<uint16_t *>(&v);
+            if (dd == 0 && a.lse) a.lse[out_row0 + hd] = (M + log2f(Ls)) * kLn2;
+          }
+        }
+        if (etid == 0) atomicExch(&a.counters[it.b * a.H + it.h], 0);
+      }
+      epilogue_sync<NET>();  // the flag, the factors and (M, L) are reused by the next item
+    }
+  }
+  if (etid == 0 && a.cta_time) {
+    a.cta_time[2 * cta] = (int64_t)*s_t0;
+    a.cta_time[2 * cta + 1] = (int64_t)globaltimer_ns();
+  }
+}
+
 // The decode of one CTA (blockIdx.x = its place in the plan); smem_raw: Layout<D>::smem_bytes
 // of dynamic shared memory, 16-byte aligned; Layout<D>::THREADS threads.  The kernel below and
 // the fused sparse-layer kernel both run it.
@@ -130,7 +324,7 @@ __device__ __forceinline__ void epilogue_sync() {
 // their merges overlap the streaming of the runs this CTA owns and the CTA ends on a cheap
 // epilogue.  Which warp reads a tile, and every summation order, is as in one-role decoding:
 // the results do not depend on the processing order.
-template <int D>
+template <int D, bool GROWN = false>
 __device__ __forceinline__ void decode_body(const CUtensorMap *pool_map_p, const DecodeArgs &a, uint8_t *smem_raw) {
   const CUtensorMap &pool_map = *pool_map_p;
   using LY = Layout<D>;
@@ -198,7 +392,10 @@ __device__ __forceinline__ void decode_body(const CUtensorMap *pool_map_p, const
         report(a.status, TG_STATUS_TIMEOUT);
     }
   if (items_in_smem)
-    for (int i = tid; i < n_items; i += NT) s_base[i] = __ldcg(a.pt_off + s_items[i].b * a.G + s_items[i].g);
+    for (int i = tid; i < n_items; i += NT) {
+      if (GROWN) s_items[i] = grown_item(a, s_items[i]);
+      s_base[i] = __ldcg(a.pt_off + s_items[i].b * a.G + s_items[i].g);
+    }
   if (warp < NW && lane == 0)
     for (int s = 0; s < R; ++s) mbar_init(&bars[warp * R + s], 1);
   if (tid == 0) {
@@ -220,7 +417,10 @@ __device__ __forceinline__ void decode_body(const CUtensorMap *pool_map_p, const
   }
   __syncthreads();
   // item and page-table base at processing position k (plan order when the items are in global)
-  auto get_item = [&](int k) -> tg_work_item { return items_in_smem ? s_items[s_order[k]] : a.items[i_begin + k]; };
+  auto get_item = [&](int k) -> tg_work_item {
+    if (items_in_smem) return s_items[s_order[k]];
+    return GROWN ? grown_item(a, a.items[i_begin + k]) : a.items[i_begin + k];
+  };
   auto get_base = [&](int k, const tg_work_item &it) -> int64_t {
     return items_in_smem ? s_base[s_order[k]] : __ldcg(a.pt_off + it.b * a.G + it.g);
   };
@@ -252,7 +452,9 @@ __device__ __forceinline__ void decode_body(const CUtensorMap *pool_map_p, const
         const int cnt = warp_tiles(it, lo);
         if (rem < cnt) {
           const int tok = 16 * (lo + warp + NW * rem);
-          page = __ldcg(a.pt_ids + get_base(k, it) + tok / a.P);
+          const int64_t base = get_base(k, it);
+          if (GROWN && base + tok / a.P >= __ldcg(a.pt_off + it.b * a.G + it.g + 1)) return;  // a list too short
+          page = __ldcg(a.pt_ids + base + tok / a.P);
           row_in_page = it.hpos * 2 * a.P + tok % a.P;  // first K row of the tile inside its page
           return;
         }
@@ -369,12 +571,17 @@ __device__ __forceinline__ void decode_body(const CUtensorMap *pool_map_p, const
           // the weights go to the P.V product rounded to bf16; the row sums add the same
           // rounded weights, so the output is a weighted mean of V under one set of weights
           const uint32_t pk01 = pack_bf16x2(p0, p1), pk23 = pack_bf16x2(p2, p3);
-          l0 = l0 * c0 + __uint_as_float(pk01 << 16) + __uint_as_float(pk23 << 16);
-          l1 = l1 * c1 + __uint_as_float(pk01 & 0xffff0000u) + __uint_as_float(pk23 & 0xffff0000u);
+          // (a grown run adds the unrounded ones: of few tokens their roundings do not average out of the lse)
+          l0 = l0 * c0 + (GROWN ? p0 + p2 : __uint_as_float(pk01 << 16) + __uint_as_float(pk23 << 16));
+          l1 = l1 * c1 + (GROWN ? p1 + p3 : __uint_as_float(pk01 & 0xffff0000u) + __uint_as_float(pk23 & 0xffff0000u));
           m0 = mn0;
           m1 = mn1;
           const uint32_t b0 = movmatrix_t(pk01);
           const uint32_t b1 = movmatrix_t(pk23);
+          // rows behind a grown run may hold anything, and 0 times that is not 0: cleared in V
+          const bool part = GROWN && (r0 > 0 || r1 < 16);
+          auto kept = [&](int t) { return (t >= r0 && t < r1 ? 0xffffu : 0u) | (t + 1 >= r0 && t + 1 < r1 ? 0xffff0000u : 0u); };
+          const uint32_t keep0 = kept(2 * tig), keep1 = kept(2 * tig + 8);  // tokens 2 tig, 2 tig + 1 and 8 behind them
           // O^T += V^T . P^T
 #pragma unroll
           for (int mb = 0; mb < KS; ++mb) {
@@ -384,6 +591,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap *pool_map_p, const
             o[mb][3] *= c1;
             uint32_t a0, a1, a2, a3;
             ldsm_x4_t(vbase + swz((lane & 7) + (lane >> 4) * 8, mb * 16 + ((lane >> 3) & 1) * 8), a0, a1, a2, a3);
+            if (GROWN && part) a0 &= keep0, a1 &= keep0, a2 &= keep1, a3 &= keep1;
             mma_16816(o[mb], a0, a1, a2, a3, b0, b1);
           }
           ++consumed;
@@ -444,167 +652,8 @@ __device__ __forceinline__ void decode_body(const CUtensorMap *pool_map_p, const
     return;
   }
 
-  // ================================================================== epilogue warps
-  const int etid = tid - NS, ew = warp - NW;
-  // the workspace (merge counters, partials) and the outputs may still be in use by the
-  // previous decode launch in the stream: wait for it before the first write
-  griddep_wait();
-  for (int k = 0; k < n_items; ++k) {
-    const tg_work_item it = get_item(k);
-    const int hb = k & 1, use = k >> 1;
-    if (!*s_dead && !mbar_wait_sleep(&full[hb], (uint32_t)(use & 1), kWaitLimitNs)) {
-      if (etid == 0) report(a.status, TG_STATUS_TIMEOUT);
-      *s_dead = 1;
-    }
-    const float *cm = comb_m + hb * NW * 8, *cl = comb_l + hb * NW * 8, *co = comb_o + hb * cfl;
-    const size_t out_row0 = (size_t)it.b * a.H_q + (size_t)it.h * a.g;
-    if (it.t1 <= it.t0) {  // a head with no retained token
-      for (int e = etid; e < a.g * D; e += NET) {
-        a.out[(out_row0 + e / D) * D + e % D] = 0;
-        if (e % D == 0 && a.lse) a.lse[out_row0 + e / D] = -INFINITY;
-      }
-    } else {
-      const int slot = it.slot0 + it.part;
-      for (int e = etid; e < a.g * D; e += NET) {
-        const int hd = e / D, dd = e % D;
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) M = fmaxf(M, cm[w * 8 + hd]);
-        float Ls = 0.f, O = 0.f;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          const float f = ex2(cm[w * 8 + hd] - M);
-          Ls += cl[w * 8 + hd] * f;
-          O += co[(w * a.g + hd) * ostride + dd] * f;
-        }
-        if (it.nparts == 1) {
-          __nv_bfloat16 v = __float2bfloat16_rn(O / Ls);
-          a.out[(out_row0 + hd) * D + dd] = *reinterpret_cast<uint16_t *>(&v);
-          if (dd == 0 && a.lse) a.lse[out_row0 + hd] = (M + log2f(Ls)) * kLn2;
-        } else {
-          a.ws_o[((size_t)slot * a.g + hd) * D + dd] = O;
-          if (dd == 0) {
-            a.ws_ml[((size_t)slot * a.g + hd) * 2] = M;
-            a.ws_ml[((size_t)slot * a.g + hd) * 2 + 1] = Ls;
-          }
-        }
-      }
-    }
-    mbar_arrive(&empty[hb]);  // (release: this thread's reads of the buffer come first)
-    if (it.t1 > it.t0 && it.nparts > 1) {
-      __threadfence();
-      epilogue_sync<NET>();
-      if (etid == 0) {
-        const int prev = atomicAdd(&a.counters[it.b * a.H + it.h], 1);
-        *flag = prev == it.nparts - 1;
-      }
-      epilogue_sync<NET>();
-      if (*flag) {  // the last CTA of this run merges every partial
-        __threadfence();
-        const int np = it.nparts, g = a.g;
-        const float *pml = a.ws_ml + (size_t)it.slot0 * g * 2;  // [nparts][g][2]
-        const float *po = a.ws_o + (size_t)it.slot0 * g * D;     // [nparts][g][D]
-        if (np * g <= kFacMax) {
-          // factors 2^(m_p - M) of every part go to shared memory; per head, one warp gathers
-          // M and L with its lanes striding over the parts (independent loads).  Up to 64 parts,
-          // each lane reads its (m, l) pairs once and keeps them in registers
-          for (int hh = ew; hh < g; hh += NE) {
-            float M = -INFINITY, Ls = 0.f;
-            if (np <= 64) {
-              float2 ml[2];
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const int p = lane + 32 * j;
-                ml[j] = p < np ? __ldcg(reinterpret_cast<const float2 *>(pml + ((size_t)p * g + hh) * 2))
-                               : make_float2(-INFINITY, 0.f);
-                M = fmaxf(M, ml[j].x);
-              }
-#pragma unroll
-              for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const int p = lane + 32 * j;
-                if (p < np) {
-                  const float f = ex2(ml[j].x - M);
-                  fac[p * g + hh] = f;
-                  Ls += ml[j].y * f;
-                }
-              }
-            } else {
-              for (int p = lane; p < np; p += 32) M = fmaxf(M, __ldcg(pml + ((size_t)p * g + hh) * 2));
-#pragma unroll
-              for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-              for (int p = lane; p < np; p += 32) {
-                const float f = ex2(__ldcg(pml + ((size_t)p * g + hh) * 2) - M);
-                fac[p * g + hh] = f;
-                Ls += __ldcg(pml + ((size_t)p * g + hh) * 2 + 1) * f;
-              }
-            }
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, off);
-            if (lane == 0) {
-              s_mm[hh] = M;
-              s_ll[hh] = Ls;
-            }
-          }
-          epilogue_sync<NET>();
-          // O = sum_p o_p 2^(m_p - M), parts in order.  A thread takes four consecutive outputs
-          // of one head (16-byte loads; partial rows are 16-byte aligned), sixteen parts per
-          // batch in flight
-          for (int e = 4 * etid; e < g * D; e += 4 * NET) {
-            const int hd = e / D, dd = e % D;
-            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int p = 0; p < np; p += 16) {
-              float4 v[16];
-#pragma unroll
-              for (int u = 0; u < 16; ++u)
-                v[u] = p + u < np ? __ldcg(reinterpret_cast<const float4 *>(po + (size_t)(p + u) * g * D + e))
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-              for (int u = 0; u < 16; ++u)
-                if (p + u < np) {
-                  const float f = fac[(p + u) * g + hd];
-                  O.x += v[u].x * f;
-                  O.y += v[u].y * f;
-                  O.z += v[u].z * f;
-                  O.w += v[u].w * f;
-                }
-            }
-            const float Ls = s_ll[hd];
-            uint16_t *orow = a.out + (out_row0 + hd) * D + dd;
-            const float ov[4] = {O.x, O.y, O.z, O.w};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              __nv_bfloat16 v = __float2bfloat16_rn(ov[c] / Ls);
-              orow[c] = *reinterpret_cast<uint16_t *>(&v);
-            }
-            if (dd == 0 && a.lse) a.lse[out_row0 + hd] = (s_mm[hd] + log2f(s_ll[hd])) * kLn2;
-          }
-        } else {  // more parts than the factor buffer holds: straight loops
-          for (int e = etid; e < g * D; e += NET) {
-            const int hd = e / D, dd = e % D;
-            float M = -INFINITY;
-            for (int p = 0; p < np; ++p) M = fmaxf(M, __ldcg(pml + ((size_t)p * g + hd) * 2));
-            float Ls = 0.f, O = 0.f;
-            for (int p = 0; p < np; ++p) {
-              const float f = ex2(__ldcg(pml + ((size_t)p * g + hd) * 2) - M);
-              Ls += __ldcg(pml + ((size_t)p * g + hd) * 2 + 1) * f;
-              O += __ldcg(po + (size_t)p * g * D + e) * f;
-            }
-            __nv_bfloat16 v = __float2bfloat16_rn(O / Ls);
-            a.out[(out_row0 + hd) * D + dd] = *reinterpret_cast<uint16_t *>(&v);
-            if (dd == 0 && a.lse) a.lse[out_row0 + hd] = (M + log2f(Ls)) * kLn2;
-          }
-        }
-        if (etid == 0) atomicExch(&a.counters[it.b * a.H + it.h], 0);
-      }
-      epilogue_sync<NET>();  // the flag, the factors and (M, L) are reused by the next item
-    }
-  }
-  if (etid == 0 && a.cta_time) {
-    a.cta_time[2 * cta] = (int64_t)*s_t0;
-    a.cta_time[2 * cta + 1] = (int64_t)globaltimer_ns();
-  }
+  decode_epilogue<D, NW, NE, GROWN>(a, get_item, n_items, comb_m, comb_l, comb_o, cfl, ostride, fac, s_mm, s_ll, flag,
+                                    s_dead, full, empty, s_t0);
 }
 
 
@@ -698,6 +747,8 @@ inline DecodeArgs decode_args(const tg_plan_header *hd, const tg_plan_layer *lt,
   args.row_due = nullptr;
   args.wait_ns = kWaitLimitNs;
   args.epoch = 0;
+  args.ntok = args.added = nullptr;
+  args.plus = args.reserve = 0;
   return args;
 }
 

@@ -157,6 +157,76 @@ extern "C" int tg_build_pages(int L, int batch, int H, int H_p, int P, float alp
   return tgi::ok();
 }
 
+// Page lists with a reserve (section 3.1: a request's footprint is fixed when it is scheduled, and the tokens it
+// may generate are part of it): as tg_build_pages, each list as long as its longest head and the reserve.
+extern "C" int tg_reserve_pages(int L, int batch, int H, int H_p, int P, const int32_t *head_order, const int32_t *ntok,
+                                int reserve, int64_t *pt_off, int32_t *pt_ids, int64_t pt_cap, int64_t *n_pages) {
+  const char *fn = "tg_reserve_pages";
+  if (L <= 0 || batch <= 0 || H <= 0 || H_p <= 0 || P <= 0 || reserve < 0)
+    return fail(TG_ERR_INVALID_ARG, "%s: L=%d, batch=%d, H=%d, H_p=%d, P=%d, reserve=%d", fn, L, batch, H, H_p, P, reserve);
+  if (!head_order || !ntok) return fail(TG_ERR_INVALID_ARG, "%s: NULL head_order/ntok", fn);
+  if (H % H_p || P % 16) return fail(TG_ERR_SHAPE, "%s: H=%d of H_p=%d, P=%d (a multiple of 16)", fn, H, H_p, P);
+  const int G = H / H_p;
+  // pages of a list, -1 for a head or a count outside its limits
+  auto pages_of = [&](int l, int b, int g) -> int64_t {
+    int64_t most = 0;
+    for (int j = 0; j < H_p; ++j) {
+      const int32_t h = head_order[(size_t)l * H + g * H_p + j];
+      if (h < 0 || h >= H) return -1;
+      const int64_t n = (int64_t)ntok[((size_t)l * batch + b) * H + h] + reserve;
+      if (n < reserve || n > INT32_MAX - P) return -1;
+      most = std::max(most, n);
+    }
+    return (most + P - 1) / P;
+  };
+  int64_t total = 0;
+  for (int l = 0; l < L; ++l)
+    for (int b = 0; b < batch; ++b)
+      for (int g = 0; g < G; ++g) {
+        const int64_t n = pages_of(l, b, g);
+        if (n < 0)
+          return fail(TG_ERR_INVALID_ARG, "%s: layer %d, request %d, group %d: a head outside [0, %d) or tokens outside "
+                      "[0, 2^31 - 1 - P - reserve]", fn, l, b, g, H);
+        total += n;
+      }
+  if (total > INT32_MAX) return fail(TG_ERR_CAPACITY, "%s: %lld pages exceed int32 ids", fn, (long long)total);
+  if (n_pages) *n_pages = total;
+  if (pt_ids && pt_cap < total)
+    return fail(TG_ERR_CAPACITY, "%s: pt_cap=%lld < %lld pages", fn, (long long)pt_cap, (long long)total);
+  int64_t at = 0;
+  for (int l = 0; l < L; ++l) {
+    int64_t before = 0;  // pages of the earlier requests and, in this one, of the earlier layers
+    for (int b = 0; b < batch; ++b) {
+      if (pt_ids) {
+        for (int i = 0; i < l; ++i)
+          for (int g = 0; g < G; ++g) before += pages_of(i, b, g);
+      }
+      for (int g = 0; g < G; ++g) {
+        const int64_t n = pages_of(l, b, g);
+        if (pt_off) pt_off[((int64_t)l * batch + b) * G + g] = at;
+        if (pt_ids)
+          for (int64_t p = 0; p < n; ++p) pt_ids[at + p] = (int32_t)(before + p);
+        at += n;
+        before += n;
+      }
+      if (pt_ids) {
+        for (int i = l + 1; i < L; ++i)
+          for (int g = 0; g < G; ++g) before += pages_of(i, b, g);
+      }
+    }
+  }
+  if (pt_off) pt_off[(int64_t)L * batch * G] = at;
+  return tgi::ok();
+}
+
+extern "C" int tg_page_bytes(int format, int H_p, int P, int d, int64_t *bytes) {
+  if (!bytes || H_p <= 0 || P <= 0 || P % 16) return fail(TG_ERR_INVALID_ARG, "tg_page_bytes: H_p=%d, P=%d or NULL", H_p, P);
+  if (d != 128 && d != 256) return fail(TG_ERR_SHAPE, "tg_page_bytes: d=%d (128 or 256)", d);
+  if (format != TG_PAGES_BF16 && format != TG_PAGES_E2M1) return fail(TG_ERR_INVALID_ARG, "tg_page_bytes: format=%d", format);
+  *bytes = format == TG_PAGES_BF16 ? (int64_t)H_p * 2 * P * d * 2 : (int64_t)H_p * (P / 16) * (d / 128) * TG_TILE4_BYTES;
+  return tgi::ok();
+}
+
 namespace {
 // One row of the split map (section 3.3, Algorithm 1): one CTA per group, then
 // the rest by largest remainder, ties to the lower group.

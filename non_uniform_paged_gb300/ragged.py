@@ -26,7 +26,8 @@ from . import (tg_build_pages, tg_split_map, tg_query_ncta, tg_plan_decode, tg_d
                tg_page_score_topk_rows, tg_rerank_rows, tg_plan_set_flags, PLAN_WAIT_TABLES,
                SCORE_LET_NEXT_START, tg_tier_promote, tg_compact_chunk, tg_compact_chunk_workspace,
                tg_sparse_layer, TilePlan, tg_qk_norm_rope, tg_plan_prefill, tg_prefill_attn, tg_plan_prefix,
-               tg_prefix_attn)
+               tg_prefix_attn, tg_reserve_pages, tg_append_rope, tg_quant_pages, tg_dequant_pages, tg_decode_grown,
+               tg_page_bytes, DecodePlan, PAGES_BF16, PAGES_E2M1)
 
 BYTES_BF16 = 2
 
@@ -39,7 +40,7 @@ class RaggedCache:
         self.g = H_q // H
         self.device = torch.device(device)
         self.N = np.asarray(N, np.int32)
-        self.pages = tg_build_pages(L, batch, H, H_p, P, alpha, Bhat, self.N, cluster)
+        self.pages = self._build_pages(tg_build_pages(L, batch, H, H_p, P, alpha, Bhat, self.N, cluster))
         self.n_pages = self.pages["n_pages"]
         self.request_pages = None
         if allocator is not None:
@@ -63,6 +64,10 @@ class RaggedCache:
         if alloc_pool:
             self.pool = torch.empty(max(self.n_pages, 1) * H_p * 2 * P * d, dtype=torch.bfloat16, device=dev)
         self.scale = 1.0 / math.sqrt(d)
+
+    def _build_pages(self, pages):
+        """The page tables to use of tg_build_pages' (a cache with a reserve has longer lists)."""
+        return pages
 
     def _take_pages(self, allocator):
         """Budget reservation: each request's page lists, over all layers and groups, come from
@@ -105,7 +110,15 @@ class RaggedCache:
         return total
 
     # ---- prefill: top-n retention into the pages
+    def _retention_pages(self, layer):
+        """(pool, pages, list offsets, page ids) that a retention of the layer writes."""
+        return self.pool, self.n_pages, self.list_offsets(layer), self.pt_ids_dev
+
+    def _retained(self, layer, stream):
+        """A retention of the layer is enqueued."""
+
     def compact_layer(self, layer, scores, K, V, kept_idx=None, stream=None):
+        pool, pages, off, ids = self._retention_pages(layer)
         Nmax = scores.shape[-1]
         ws = self._compact_ws.get(Nmax)
         if ws is None:
@@ -113,8 +126,9 @@ class RaggedCache:
                              device=self.device)
             self._compact_ws = {Nmax: ws}  # one size at a time: the last Nmax used
         tg_compact_topk(self.batch, self.H, self.H_p, self.P, self.d, Nmax, self.N_dev, scores, K, V,
-                        self.order_dev[layer], self.ntok_dev[layer], self.list_offsets(layer), self.pt_ids_dev,
-                        self.n_pages, self.pool, ws, kept_idx=kept_idx, dev_status=self.status, stream=stream)
+                        self.order_dev[layer], self.ntok_dev[layer], off, ids, pages, pool, ws, kept_idx=kept_idx,
+                        dev_status=self.status, stream=stream)
+        self._retained(layer, stream)
 
     def compact_layer_chunked(self, layer, scores, K, V, C, stream=None, chunks=None):
         """Retention fused into chunked prefill (tg_compact_chunk): the prompt's scores and K/V
@@ -122,6 +136,7 @@ class RaggedCache:
         Returns the slot tokens [batch][H][nmax] (slot k of head (b, h) holds token [b, h, k]).
         `chunks` (optional) yields the (scores, K, V) tensors of each chunk [batch][H][C](...);
         by default they are cut from the full tensors."""
+        pool, pages, off, ids = self._retention_pages(layer)
         ntok = self.pages["ntok"][layer]
         nmax = max(1, int(ntok.max()))
         slot_tok = torch.full((self.batch, self.H, nmax), -1, dtype=torch.int32, device=self.device)
@@ -140,9 +155,9 @@ class RaggedCache:
                 kc[:, :, :end - start] = K[:, :, start:end]
                 vc[:, :, :end - start] = V[:, :, start:end]
             tg_compact_chunk(self.batch, self.H, self.H_p, self.P, self.d, start, C, self.N_dev, sc, kc, vc,
-                             self.order_dev[layer], self.ntok_dev[layer], self.list_offsets(layer),
-                             self.pt_ids_dev, self.n_pages, self.pool, slot_tok, slot_key, ws,
+                             self.order_dev[layer], self.ntok_dev[layer], off, ids, pages, pool, slot_tok, slot_key, ws,
                              dev_status=self.status, stream=stream)
+        self._retained(layer, stream)
         return slot_tok
 
     # ---- decode: one layer's attention
@@ -500,6 +515,160 @@ class SharedPrefix(_OnStreams):
                        out, lse=lse, own_out=own_out, own_lse=own_lse, workspace=self.workspace, dev_status=self.status,
                        stream=stream)
         self._used_on(stream)
+
+
+PAGE_FORMATS = {"bf16": PAGES_BF16, "e2m1": PAGES_E2M1}
+
+
+class GrowingLists(_OnStreams):
+    """Page lists that grow behind their retained tokens: the plan, counts and workspace of tg_append_rope
+    and tg_decode_grown, over pages of either format ("bf16", or "e2m1": 4 bits).  order int32 [H] or [L][H] and
+    ntok int32 [batch][H] or [L][batch][H] as tg_build_pages gives them; reserve: the tokens that a head may
+    get behind them.  k_unit, v_unit: of 4-bit pages (tg.h).
+
+    A decode step is append and attend of each layer, then advance(); added (int32 [batch], on the device)
+    counts the tokens appended in earlier steps, so that a captured step may be replayed.  One stream at a time;
+    used and dropped as a PrefillPass."""
+
+    def __init__(self, H_q, H_p, P, d, order, ntok, reserve, pages="bf16", k_unit=1.0, v_unit=1.0, n_cta=None, device="cuda"):
+        if pages not in PAGE_FORMATS:
+            raise ValueError(f"pages={pages!r} (one of {sorted(PAGE_FORMATS)})")
+        self.device = torch.device(device)
+        self.format, self.k_unit, self.v_unit = PAGE_FORMATS[pages], float(k_unit), float(v_unit)
+        ntok = np.asarray(ntok, np.int32)
+        ntok = ntok[None] if ntok.ndim == 2 else ntok
+        order = np.asarray(order, np.int32)
+        order = np.array(np.broadcast_to(order, (ntok.shape[0], ntok.shape[2])) if order.ndim == 1 else order, np.int32)
+        L, self.batch, H = ntok.shape
+        self.H_p, self.P, self.d, self.reserve = H_p, P, d, int(reserve)
+        self.n_cta = int(n_cta) if n_cta else tg_query_ncta(d, H_q // H)
+        most = ntok.astype(np.int64) + self.reserve  # the plan's tokens; the split goes by them too
+        if most.size and most.max() > 2 ** 31 - 1 - P:
+            raise ValueError(f"{most.max()} tokens of a head")
+        Phi = np.stack([most[l][:, order[l]].sum(0).reshape(-1, H_p).sum(1) for l in range(L)])
+        plan, workspace = tg_plan_decode(tg_split_map(Phi, self.n_cta), order, most.astype(np.int32), H_q, H_p, P, d)
+        self.workspace = torch.zeros(workspace, dtype=torch.uint8, device=self.device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self.added = torch.zeros(self.batch, dtype=torch.int32, device=self.device)
+        # last, as in PrefillPass: the uploads wait for the current stream
+        self.plan = DecodePlan(plan, torch.from_numpy(plan).to(self.device))
+        self.order = [torch.from_numpy(o).to(self.device) for o in order]
+        self.ntok = [torch.from_numpy(n).to(self.device) for n in ntok]
+        self.one_each = torch.from_numpy(np.arange(self.batch + 1, dtype=np.int32)).to(self.device)
+        self.scale = 1.0 / math.sqrt(d)
+        self._own(self.plan.plan_dev, self.workspace, self.status, self.added, self.one_each, *self.order, *self.ntok)
+
+    def append(self, layer, qkv, cos_sin, q, pool, pool_pages, pt_off, pt_ids, cu_q=None, origin=None, positions=None,
+               axis_of=None, q_weight=None, k_weight=None, eps=1e-6, pairs=False, K=None, V=None, start=None, stream=None):
+        """One layer's new tokens (tg_append_rope): one for each request, or those of cu_q."""
+        tg_append_rope(qkv, self.one_each if cu_q is None else cu_q, cos_sin, q, pool, pool_pages, self.order[layer],
+                       self.ntok[layer], self.added, self.reserve, pt_off, pt_ids, self.H_p, self.P, fmt=self.format,
+                       k_unit=self.k_unit, v_unit=self.v_unit, q_weight=q_weight, k_weight=k_weight, eps=eps, pairs=pairs,
+                       positions=positions, axis_of=axis_of, origin=origin, K=K, V=V, start=start, dev_status=self.status,
+                       stream=stream)
+        self._used_on(stream)
+
+    def attend(self, layer, q, pool, pool_pages, pt_off, pt_ids, out, lse=None, plus=1, scale=None, cta_time=None,
+               stream=None):
+        """One layer's decode attention over retained and appended tokens (tg_decode_grown); plus: the tokens
+        appended in this step, which added does not count yet."""
+        tg_decode_grown(self.plan, layer, self.format, q, pool, pool_pages, pt_off, pt_ids, self.ntok[layer], self.added,
+                        plus, self.reserve, self.scale if scale is None else scale, out, lse=lse, k_unit=self.k_unit,
+                        v_unit=self.v_unit, workspace=self.workspace, dev_status=self.status, cta_time=cta_time,
+                        stream=stream)
+        self._used_on(stream)
+
+    def advance(self, n=1):
+        """Count a step's tokens, after its last layer, on the current stream: n for each request, or int32 [batch]."""
+        self.added.add_(n)
+        self._used_on(None)
+
+    def quantize(self, layer, src, src_pages, src_off, src_ids, dst, dst_pages, dst_off, dst_ids, stream=None):
+        """One layer's retained tokens from bf16 pages into 4-bit pages (tg_quant_pages)."""
+        tg_quant_pages(self.order[layer], self.ntok[layer], self.H_p, self.P, self.d, src_off, src_ids, src, src_pages,
+                       dst_off, dst_ids, dst, dst_pages, k_unit=self.k_unit, v_unit=self.v_unit, dev_status=self.status,
+                       stream=stream)
+        self._used_on(stream)
+
+    def dequantize(self, layer, src, src_pages, src_off, src_ids, dst, dst_pages, dst_off, dst_ids, plus=0, stream=None):
+        """One layer's retained and appended tokens from 4-bit pages into bf16 pages (tg_dequant_pages)."""
+        tg_dequant_pages(self.order[layer], self.ntok[layer], self.H_p, self.P, self.d, src_off, src_ids, src, src_pages,
+                         dst_off, dst_ids, dst, dst_pages, added=self.added, plus=plus, reserve=self.reserve,
+                         k_unit=self.k_unit, v_unit=self.v_unit, dev_status=self.status, stream=stream)
+        self._used_on(stream)
+
+
+class GrowingCache(RaggedCache):
+    """A RaggedCache whose heads get up to `reserve` tokens behind their retained ones, in pages of either
+    format.  compact_layer and compact_layer_chunked retain into it; a decode step is append_layer and
+    decode_layer of each layer, then advance().  With pages="e2m1" retention goes through bf16 pages of
+    one layer, which the next one uses again; dequantize_layer gives a layer's tokens as bf16 pages, for
+    SharedPrefix and the like.  The base class' own decode plan (`plan`) covers the retained tokens alone."""
+
+    def __init__(self, L, batch, H, H_q, d, P, H_p, alpha, Bhat, N, reserve, pages="bf16", k_unit=1.0, v_unit=1.0,
+                 cluster=False, n_cta=None, device="cuda", allocator=None):
+        self.reserve = int(reserve)
+        super().__init__(L, batch, H, H_q, d, P, H_p, alpha, Bhat, N, cluster=cluster, n_cta=n_cta, device=device,
+                         alloc_pool=False, allocator=allocator)
+        self.lists = GrowingLists(H_q, H_p, P, d, self.pages["order"], self.pages["ntok"], reserve, pages=pages,
+                                  k_unit=k_unit, v_unit=v_unit, n_cta=self.n_cta, device=device)
+        self.status = self.lists.status  # one word for all calls
+        self.four = self.lists.format == PAGES_E2M1
+        page = tg_page_bytes(self.lists.format, H_p, P, d)
+        kind = torch.uint8 if self.four else torch.bfloat16
+        self.pool = torch.empty(max(self.n_pages, 1) * page // kind.itemsize, dtype=kind, device=self.device)
+        self._layer_pages = None
+
+    def _build_pages(self, pages):
+        """The same heads' lists with the reserve."""
+        off, ids, n = tg_reserve_pages(pages["order"], pages["ntok"], self.H_p, self.P, self.reserve)
+        return dict(pages, pt_off=off, pt_ids=ids, n_pages=n)
+
+    def _bf16_layer(self):
+        """bf16 pages of one layer, with a table that numbers any layer's pages from 0."""
+        if self._layer_pages is None:
+            n = self.batch * self.G
+            off = self.pages["pt_off"]
+            tables = [torch.from_numpy(off[l * n:(l + 1) * n + 1] - off[l * n]).to(self.device) for l in range(self.L)]
+            most = max(int(off[(l + 1) * n] - off[l * n]) for l in range(self.L))
+            ids = torch.arange(max(most, 1), dtype=torch.int32, device=self.device)
+            pool = torch.empty(max(most, 1) * self.H_p * 2 * self.P * self.d, dtype=torch.bfloat16, device=self.device)
+            self._layer_pages = (pool, max(most, 1), tables, ids)
+        return self._layer_pages
+
+    def _retention_pages(self, layer):
+        if not self.four:
+            return super()._retention_pages(layer)
+        pool, pages, tables, ids = self._bf16_layer()
+        return pool, pages, tables[layer], ids
+
+    def _retained(self, layer, stream):
+        if self.four:
+            pool, pages, off, ids = self._retention_pages(layer)
+            self.lists.quantize(layer, pool, pages, off, ids, self.pool, self.n_pages, self.list_offsets(layer),
+                                self.pt_ids_dev, stream=stream)
+
+    def append_layer(self, layer, qkv, cos_sin, q, stream=None, **how):
+        """GrowingLists.append into this cache's pages."""
+        self.lists.append(layer, qkv, cos_sin, q, self.pool, self.n_pages, self.list_offsets(layer), self.pt_ids_dev,
+                          stream=stream, **how)
+
+    def decode_layer(self, layer, q, out, lse=None, cta_time=None, stream=None, pool=None, plus=1):
+        """GrowingLists.attend over this cache's pages."""
+        self.lists.attend(layer, q, self.pool if pool is None else pool, self.n_pages, self.list_offsets(layer),
+                          self.pt_ids_dev, out, lse=lse, plus=plus, cta_time=cta_time, stream=stream)
+
+    def advance(self, n=1):
+        self.lists.advance(n)
+
+    def dequantize_layer(self, layer, plus=0, stream=None):
+        """One layer's tokens in bf16 pages -> (pool, pages, pt_off, pt_ids); the next call uses the same pool."""
+        if not self.four:
+            return self.pool, self.n_pages, self.list_offsets(layer), self.pt_ids_dev
+        pool, pages, off, ids = self._retention_pages(layer)
+        self.lists.dequantize(layer, self.pool, self.n_pages, self.list_offsets(layer), self.pt_ids_dev, pool, pages, off, ids,
+                              plus=plus, stream=stream)
+        return pool, pages, off, ids
 
 
 class RerankSchedule:
