@@ -134,10 +134,10 @@ __device__ __forceinline__ void epilogue_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
 }
 
-// The epilogue warps of a CTA (see decode_body).  A piece of a grown run may hold no token: it leaves a
+// The epilogue warps of a CTA (see decode_body), with one or two hand-off buffers.  A piece of a grown run may hold no token: it leaves a
 // partial of no weight.
 template <int D, int NW, int NE, bool GROWN, typename GetItem>
-__device__ __forceinline__ void decode_epilogue(const DecodeArgs &a, GetItem get_item, int n_items, const float *comb_m,
+__device__ __forceinline__ void decode_epilogue(const DecodeArgs &a, GetItem get_item, int n_items, int buffers, const float *comb_m,
                                                 const float *comb_l, const float *comb_o, int cfl, int ostride,
                                                 float *fac, float *s_mm, float *s_ll, int *flag, volatile int *s_dead,
                                                 uint64_t *full, uint64_t *empty, const uint64_t *s_t0) {
@@ -153,7 +153,7 @@ __device__ __forceinline__ void decode_epilogue(const DecodeArgs &a, GetItem get
   griddep_wait();
   for (int k = 0; k < n_items; ++k) {
     const tg_work_item it = get_item(k);
-    const int hb = k & 1, use = k >> 1;
+    const int hb = buffers == 2 ? k & 1 : 0, use = buffers == 2 ? k >> 1 : k;
     if (!*s_dead && !mbar_wait_sleep(&full[hb], (uint32_t)(use & 1), kWaitLimitNs)) {
       if (etid == 0) report(a.status, TG_STATUS_TIMEOUT);
       *s_dead = 1;
@@ -652,7 +652,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap *pool_map_p, const
     return;
   }
 
-  decode_epilogue<D, NW, NE, GROWN>(a, get_item, n_items, comb_m, comb_l, comb_o, cfl, ostride, fac, s_mm, s_ll, flag,
+  decode_epilogue<D, NW, NE, GROWN>(a, get_item, n_items, 2, comb_m, comb_l, comb_o, cfl, ostride, fac, s_mm, s_ll, flag,
                                     s_dead, full, empty, s_t0);
 }
 

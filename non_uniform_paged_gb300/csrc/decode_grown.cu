@@ -35,33 +35,39 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1)
   decode_body<D, true>(&pool_map, a, smem_raw);
 }
 
-// NW streaming warps, each with an R-stage ring of tiles, and NE epilogue warps
+// NW streaming warps, each with an R-stage ring of steps of 32 tokens, and NE epilogue warps
 template <int D>
 struct Cfg4;
 template <>
 struct Cfg4<128> {
-  static constexpr int NW = 12, R = 4, NE = 4;
+  static constexpr int NW = 12, R = 2, NE = 4;
 };
 template <>
 struct Cfg4<256> {
-  static constexpr int NW = 6, R = 4, NE = 4;
+  static constexpr int NW = 8, R = 2, NE = 4;
 };
 
 template <int D>
 struct Layout4 {
   static constexpr int NW = Cfg4<D>::NW, R = Cfg4<D>::R, NE = Cfg4<D>::NE;
   static constexpr int THREADS = (NW + NE) * 32;
-  static constexpr int STAGE = D / 128 * kTile4;  // 16 tokens
+  static constexpr int TILE = D / 128 * kTile4;  // 16 tokens
+  static constexpr int STAGE = 2 * TILE;
   static constexpr int RING = NW * R * STAGE;
   // as Layout: barriers, start time, items and their page-table bases and order, hand-off (m, l), merged (M, L), flags
   static constexpr int SMALL = NW * R * 8 + 4 * 8 + 8 + kMaxItems * (8 + (int)sizeof(tg_work_item)) +
                                kMaxItems * 4 + 2 * NW * 8 * 4 * 2 + 8 * 4 * 2 + 16;
+  static constexpr int MOST = 227 * 1024;
   __host__ __device__ static int ostride(int g) { return g <= 4 ? D + 4 : D; }
   __host__ __device__ static int comb_floats(int g) { return NW * g * ostride(g); }
-  static int smem_bytes(int g) { return SMALL + 128 + RING + 2 * comb_floats(g) * 4 + kFacMax * 4; }
+  // two hand-off buffers, or one where two do not fit (d = 256 with more than five query heads)
+  static int buffers(int g) { return bytes(g, 2) <= MOST ? 2 : 1; }
+  static int bytes(int g, int nb) { return SMALL + 128 + RING + nb * comb_floats(g) * 4 + kFacMax * 4; }
 };
 
-constexpr float kWeightLog2 = 15.f;  // weights are 2^15 times the softmax's
+// A weight is 2^(x - m + 8), with m a reference that moves only when a score passes it by more than 7: at most
+// 2^15, in reach of f16, and a step that moves nothing neither reduces a maximum over lanes nor rescales O.
+constexpr float kWeightLog2 = 8.f, kWeightMost = 15.f;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -91,6 +97,7 @@ struct Pool4 {
   const uint8_t *base;
   int64_t head_bytes;  // of a head in a page
   float v_unit;
+  int buffers;  // hand-off buffers
 };
 
 template <int D>
@@ -115,7 +122,7 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
   uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + LY::SMALL + 127) & ~uintptr_t(127));
   const int ostride = LY::ostride(a.g), cfl = LY::comb_floats(a.g);
   float *comb_o = reinterpret_cast<float *>(ring + LY::RING);              // [2][NW][g][ostride]
-  float *fac = comb_o + 2 * cfl;                                           // [kFacMax]
+  float *fac = comb_o + pool.buffers * cfl;                                // [kFacMax]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gid = lane >> 2, tig = lane & 3;
   if (tid == 0) *s_t0 = globaltimer_ns();
@@ -164,61 +171,66 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
 
   if (warp < NW) {
     // ================================================================ streaming warps
-    auto warp_tiles = [&](const tg_work_item &it, int &lo) -> int {
-      int hi;
-      item_tiles(it, lo, hi);
-      return hi - lo > warp ? (hi - lo - warp + NW - 1) / NW : 0;
+    // steps of 32 tokens of item `it` that this warp takes: lo + warp, lo + warp + NW, ...
+    auto warp_steps = [&](const tg_work_item &it, int &lo) -> int {
+      lo = it.t0 >> 5;
+      const int n = it.t1 > it.t0 ? ((it.t1 + 31) >> 5) - lo : 0;
+      return n > warp ? (n - warp + NW - 1) / NW : 0;
     };
-    int total_tiles = 0;
+    int total = 0;
     for (int k = 0; k < n_items; ++k) {
       int lo;
-      total_tiles += warp_tiles(get_item(k), lo);
+      total += warp_steps(get_item(k), lo);
     }
-    // where a tile of this warp lies: 32 of them looked up at a time, one by each lane, a batch ahead
+    // where the two tiles of a step of this warp lie: sixteen steps looked up at a time, a tile by each lane, a batch
+    // ahead; kNone: no token of the item in it
+    constexpr int64_t kBad = -1, kNone = -2;
     auto tile_at = [&](int n) -> int64_t {
-      if (n >= total_tiles) return -1;
-      int rem = n;
+      if (n >= 2 * total) return kNone;
+      int rem = n >> 1;
       for (int k = 0; k < n_items; ++k) {
         const tg_work_item it = get_item(k);
         int lo;
-        const int cnt = warp_tiles(it, lo);
+        const int cnt = warp_steps(it, lo);
         if (rem < cnt) {
-          const int tok = 16 * (lo + warp + NW * rem);
+          const int tok = 32 * (lo + warp + NW * rem) + 16 * (n & 1);
+          if (tok + 16 <= it.t0 || tok >= it.t1) return kNone;
           const int64_t at = get_base(k, it) + tok / a.P;
-          if (at >= __ldcg(a.pt_off + it.b * a.G + it.g + 1)) return -1;  // a list too short
+          if (at >= __ldcg(a.pt_off + it.b * a.G + it.g + 1)) return kBad;  // a list too short
           const int32_t page = __ldcg(a.pt_ids + at);
-          if (page < 0 || page >= a.pool_pages) return -1;
-          return ((int64_t)page * a.H_p + it.hpos) * pool.head_bytes + (tok % a.P / 16) * LY::STAGE;
+          if (page < 0 || page >= a.pool_pages) return kBad;
+          return ((int64_t)page * a.H_p + it.hpos) * pool.head_bytes + (tok % a.P / 16) * LY::TILE;
         }
         rem -= cnt;
       }
-      return -1;
+      return kNone;
     };
     int64_t at_cur = tile_at(lane), at_nxt = tile_at(32 + lane);
     int issued = 0, consumed = 0;
-    auto issue = [&]() {  // whole warp: tile number `issued` of this warp into stage issued % R
-      const int64_t at = __shfl_sync(0xffffffffu, at_cur, issued & 31);
+    auto issue = [&]() {  // whole warp: step number `issued` of this warp into stage issued % R
+      const int from = 2 * (issued & 15);
+      const int64_t at0 = __shfl_sync(0xffffffffu, at_cur, from), at1 = __shfl_sync(0xffffffffu, at_cur, from + 1);
       if (lane == 0) {
         const int s = issued % R;
         uint64_t *bar = &bars[warp * R + s];
-        if (at < 0) {
-          report(a.status, TG_STATUS_BAD_PAGE);
-          mbar_arrive(bar);  // complete the phase without data
-        } else {
-          mbar_arrive_expect_tx(bar, LY::STAGE);
-          bulk_load(ring + (warp * R + s) * LY::STAGE, pool.base + at, LY::STAGE, bar);
-        }
+        uint8_t *to = ring + (warp * R + s) * LY::STAGE;
+        if (at0 == kBad || at1 == kBad) report(a.status, TG_STATUS_BAD_PAGE);
+        // (a phase without data completes at once)
+        mbar_arrive_expect_tx(bar, (at0 >= 0 ? LY::TILE : 0) + (at1 >= 0 ? LY::TILE : 0));
+        if (at0 >= 0) bulk_load(to, pool.base + at0, LY::TILE, bar);
+        if (at1 >= 0) bulk_load(to + LY::TILE, pool.base + at1, LY::TILE, bar);
       }
       ++issued;
-      if ((issued & 31) == 0) {
+      if ((issued & 15) == 0) {
         at_cur = at_nxt;
-        at_nxt = tile_at(issued + 32 + lane);
+        at_nxt = tile_at(2 * issued + 32 + lane);
       }
     };
-    for (int s = 0; s < R && issued < total_tiles; ++s) issue();
+    for (int s = 0; s < R && issued < total; ++s) issue();
 
     bool dead = false;  // a copy wait timed out: skip all further tiles, keep handing off
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    // the reference of each head's weights, 8 less it, and their sum
+    float m0 = -INFINITY, m1 = -INFINITY, d0 = INFINITY, d1 = INFINITY, l0 = 0.f, l1 = 0.f;
     float o[C][8][4];
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -227,9 +239,9 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
 
     for (int k = 0; k < n_items; ++k) {
       const tg_work_item it = get_item(k);
-      int k_lo, k_hi;
-      item_tiles(it, k_lo, k_hi);
-      if (k_hi - k_lo > warp && !dead) {
+      int lo;
+      const int steps = warp_steps(it, lo);
+      if (steps > 0 && !dead) {
         // Query fragments, B of S^T = K Q^T: head gid, values 32 tig .. 32 tig + 31 of each 128, as f16 times
         // 2^-e, e the exponent of the head's largest; z0, z1: what that and the softmax scale give the scores of
         // the heads 2 tig and 2 tig + 1 that this lane holds
@@ -265,7 +277,8 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
           z0 = __shfl_sync(0xffffffffu, up, 8 * tig);
           z1 = __shfl_sync(0xffffffffu, up, 8 * tig + 4);
         }
-        for (int kk = k_lo + warp; kk < k_hi; kk += NW) {
+        for (int i = 0; i < steps; ++i) {
+          const int kk = lo + warp + i * NW;
           const int s = consumed % R;
           bool ok = mbar_wait(&bars[warp * R + s], (uint32_t)((consumed / R) & 1), kWaitLimitNs);
           ok = __all_sync(0xffffffffu, ok);
@@ -274,96 +287,137 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
             dead = true;
             break;
           }
-          const uint32_t tile = smem_addr(ring + (warp * R + s) * LY::STAGE);
-          const int r0 = it.t0 - kk * 16, r1 = it.t1 - kk * 16;  // valid rows [r0, r1) of the tile
+          const uint32_t stage = smem_addr(ring + (warp * R + s) * LY::STAGE);
+          const int r0 = it.t0 - kk * 32, r1 = it.t1 - kk * 32;  // valid rows [r0, r1) of the step
+          const bool part = r0 > 0 || r1 < 32;
 
-          // S^T = K Q^T (rows: tokens gid and gid + 8, columns: heads 2 tig and 2 tig + 1)
-          float sc[4] = {0.f, 0.f, 0.f, 0.f};
+          // S^T = K Q^T (rows: tokens gid and gid + 8 of each half, columns: heads 2 tig and 2 tig + 1)
+          float sc[2][4];
 #pragma unroll
-          for (int c = 0; c < C; ++c) {
-            const uint32_t kt = tile + c * kTile4;
-            const uint4 x = lds128(kt + 64 * gid + 16 * tig), y = lds128(kt + 64 * (gid + 8) + 16 * tig);
-            const uint32_t sx = e4m3x2_to_f16x2(lds16(kt + kKScales4 + 8 * gid + 2 * tig));
-            const uint32_t sy = e4m3x2_to_f16x2(lds16(kt + kKScales4 + 8 * (gid + 8) + 2 * tig));
-            const uint32_t wx[4] = {x.x, x.y, x.z, x.w}, wy[4] = {y.x, y.y, y.z, y.w};
+          for (int hf = 0; hf < 2; ++hf) {
+            sc[hf][0] = sc[hf][1] = sc[hf][2] = sc[hf][3] = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {  // eight values of each row; the first 16 have one scale, the others the next
-              const uint32_t fx = __byte_perm(sx, 0, i < 2 ? 0x1010 : 0x3232), fy = __byte_perm(sy, 0, i < 2 ? 0x1010 : 0x3232);
-              uint32_t hx[4], hy[4];
-              e2m1x8_to_f16x2(wx[i], hx);
-              e2m1x8_to_f16x2(wy[i], hy);
+            for (int c = 0; c < C; ++c) {
+              const uint32_t kt = stage + hf * LY::TILE + c * kTile4;
+              const uint4 x = lds128(kt + 64 * gid + 16 * tig), y = lds128(kt + 64 * (gid + 8) + 16 * tig);
+              const uint32_t sx = e4m3x2_to_f16x2(lds16(kt + kKScales4 + 8 * gid + 2 * tig));
+              const uint32_t sy = e4m3x2_to_f16x2(lds16(kt + kKScales4 + 8 * (gid + 8) + 2 * tig));
+              const uint32_t wx[4] = {x.x, x.y, x.z, x.w}, wy[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-              for (int j = 0; j < 2; ++j)
-                mma_f16(sc, mul_f16x2(hx[2 * j], fx), mul_f16x2(hy[2 * j], fy), mul_f16x2(hx[2 * j + 1], fx),
-                        mul_f16x2(hy[2 * j + 1], fy), qf[c][2 * i + j][0], qf[c][2 * i + j][1]);
-            }
-          }
-          // online softmax, base 2
-          const bool v0 = gid >= r0 && gid < r1, v1 = gid + 8 >= r0 && gid + 8 < r1;
-          const float x0 = v0 ? sc[0] * z0 : -INFINITY, x1 = v0 ? sc[1] * z1 : -INFINITY;
-          const float x2 = v1 ? sc[2] * z0 : -INFINITY, x3 = v1 ? sc[3] * z1 : -INFINITY;
-          float mx0 = fmaxf(x0, x2), mx1 = fmaxf(x1, x3);
+              for (int w = 0; w < 4; ++w) {  // eight values of each row; the first 16 have one scale, the others the next
+                const uint32_t fx = __byte_perm(sx, 0, w < 2 ? 0x1010 : 0x3232), fy = __byte_perm(sy, 0, w < 2 ? 0x1010 : 0x3232);
+                uint32_t hx[4], hy[4];
+                e2m1x8_to_f16x2(wx[w], hx);
+                e2m1x8_to_f16x2(wy[w], hy);
 #pragma unroll
-          for (int off = 4; off < 32; off <<= 1) {
-            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
-            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
-          }
-          const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
-          const float c0 = ex2(m0 - mn0), c1 = ex2(m1 - mn1);
-          // (15 comes last: added to a maximum of 2^28 it would be rounded to 16 or 32)
-          const float p0 = ex2(x0 - mn0 + kWeightLog2), p1 = ex2(x1 - mn1 + kWeightLog2);
-          const float p2 = ex2(x2 - mn0 + kWeightLog2), p3 = ex2(x3 - mn1 + kWeightLog2);
-          l0 = l0 * c0 + p0 + p2;
-          l1 = l1 * c1 + p1 + p3;
-          m0 = mn0;
-          m1 = mn1;
-          const uint32_t w0 = movmatrix_t(pack_f16x2(p0, p1)), w1 = movmatrix_t(pack_f16x2(p2, p3));
-          // O^T += V^T P^T (rows: values 16 gid + 2 i and one on, columns: heads); this lane's tokens: 2 tig, 2 tig + 1
-          // and the two 8 behind them
-#pragma unroll
-          for (int c = 0; c < C; ++c) {
-            const uint32_t vt = tile + c * kTile4 + kVCodes4;
-            const uint4 x = lds128(vt + 64 * gid + 16 * tig), y = lds128(vt + 512 + 64 * gid + 16 * tig);
-            uint32_t sx = e4m3x2_to_f16x2(lds16(tile + c * kTile4 + kVScales4 + 16 * gid + 2 * tig));
-            uint32_t sy = e4m3x2_to_f16x2(lds16(tile + c * kTile4 + kVScales4 + 16 * gid + 2 * tig + 8));
-            if (r0 > 0 || r1 < 16) {  // rows that are no token of this piece may hold anything: 0 times a code is 0
-              auto kept = [&](int t) {
-                return (t >= r0 && t < r1 ? 0xffffu : 0u) | (t + 1 >= r0 && t + 1 < r1 ? 0xffff0000u : 0u);
-              };
-              sx &= kept(2 * tig);
-              sy &= kept(2 * tig + 8);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {  // values 8 i .. 8 i + 7 of the block
-              const uint32_t xa = i ? x.y : x.x, xb = i ? x.w : x.z, ya = i ? y.y : y.x, yb = i ? y.w : y.z;
-              // even and odd values, the first token in the lower half of each byte
-              uint32_t ex[4], ox[4], ey[4], oy[4];
-              e2m1x8_to_f16x2((xa & 0x0f0f0f0fu) | (xb << 4 & 0xf0f0f0f0u), ex);
-              e2m1x8_to_f16x2((xa >> 4 & 0x0f0f0f0fu) | (xb & 0xf0f0f0f0u), ox);
-              e2m1x8_to_f16x2((ya & 0x0f0f0f0fu) | (yb << 4 & 0xf0f0f0f0u), ey);
-              e2m1x8_to_f16x2((ya >> 4 & 0x0f0f0f0fu) | (yb & 0xf0f0f0f0u), oy);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                float(&oo)[4] = o[c][4 * i + j];
-                oo[0] *= c0;
-                oo[1] *= c1;
-                oo[2] *= c0;
-                oo[3] *= c1;
-                mma_f16(oo, mul_f16x2(ex[j], sx), mul_f16x2(ox[j], sx), mul_f16x2(ey[j], sy), mul_f16x2(oy[j], sy), w0, w1);
+                for (int j = 0; j < 2; ++j)
+                  mma_f16(sc[hf], mul_f16x2(hx[2 * j], fx), mul_f16x2(hy[2 * j], fy), mul_f16x2(hx[2 * j + 1], fx),
+                          mul_f16x2(hy[2 * j + 1], fy), qf[c][2 * w + j][0], qf[c][2 * w + j][1]);
               }
             }
           }
+          // online softmax, base 2; y = x - m + 8
+          auto logits = [&](float(&y)[2][4]) {
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                y[hf][j] = fmaf(sc[hf][j], j & 1 ? z1 : z0, j & 1 ? d1 : d0);
+                if (part) {
+                  const int t = 16 * hf + gid + (j & 2 ? 8 : 0);
+                  if (t < r0 || t >= r1) y[hf][j] = -INFINITY;
+                }
+              }
+          };
+          float y[2][4];
+          logits(y);
+          const float top0 = fmaxf(fmaxf(y[0][0], y[0][2]), fmaxf(y[1][0], y[1][2]));
+          const float top1 = fmaxf(fmaxf(y[0][1], y[0][3]), fmaxf(y[1][1], y[1][3]));
+          if (__any_sync(0xffffffffu, fmaxf(top0, top1) > kWeightMost)) {
+            // the reference moves to the maximum so far
+            float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+              for (int j = 0; j < 4; j += 2) {
+                const int t = 16 * hf + gid + 4 * j;
+                if (t < r0 || t >= r1) continue;
+                x0 = fmaxf(x0, sc[hf][j] * z0);
+                x1 = fmaxf(x1, sc[hf][j + 1] * z1);
+              }
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) {
+              x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
+              x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
+            }
+            const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+            const float c0 = n0 == m0 ? 1.f : ex2(m0 - n0), c1 = n1 == m1 ? 1.f : ex2(m1 - n1);
+            m0 = n0, m1 = n1;
+            d0 = kWeightLog2 - m0, d1 = kWeightLog2 - m1;
+            l0 *= c0, l1 *= c1;
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) o[c][j][0] *= c0, o[c][j][1] *= c1, o[c][j][2] *= c0, o[c][j][3] *= c1;
+            logits(y);
+            // (where m is past 2^20 the sums round: no weight passes the largest for that)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) y[hf][j] = y[hf][j] > kWeightMost ? kWeightMost : y[hf][j];
+          }
+          uint32_t wt[2][2];
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const float p0 = ex2(y[hf][0]), p1 = ex2(y[hf][1]), p2 = ex2(y[hf][2]), p3 = ex2(y[hf][3]);
+            l0 += p0 + p2;
+            l1 += p1 + p3;
+            wt[hf][0] = movmatrix_t(pack_f16x2(p0, p1));
+            wt[hf][1] = movmatrix_t(pack_f16x2(p2, p3));
+          }
+          // O^T += V^T P^T (rows: values 16 gid + 2 i and one on, columns: heads); this lane's tokens: 2 tig, 2 tig + 1
+          // and the two 8 behind them, of each half
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const uint32_t tile = stage + hf * LY::TILE + c * kTile4, vt = tile + kVCodes4;
+              const uint4 x = lds128(vt + 64 * gid + 16 * tig), yv = lds128(vt + 512 + 64 * gid + 16 * tig);
+              uint32_t sx = e4m3x2_to_f16x2(lds16(tile + kVScales4 + 16 * gid + 2 * tig));
+              uint32_t sy = e4m3x2_to_f16x2(lds16(tile + kVScales4 + 16 * gid + 2 * tig + 8));
+              if (part) {  // rows that are no token of this piece may hold anything: 0 times a code is 0
+                auto kept = [&](int t) {
+                  return (t >= r0 && t < r1 ? 0xffffu : 0u) | (t + 1 >= r0 && t + 1 < r1 ? 0xffff0000u : 0u);
+                };
+                sx &= kept(16 * hf + 2 * tig);
+                sy &= kept(16 * hf + 2 * tig + 8);
+              }
+#pragma unroll
+              for (int w = 0; w < 2; ++w) {  // values 8 w .. 8 w + 7 of the block
+                const uint32_t xa = w ? x.y : x.x, xb = w ? x.w : x.z, ya = w ? yv.y : yv.x, yb = w ? yv.w : yv.z;
+                // even and odd values, the first token in the lower half of each byte
+                uint32_t ex[4], ox[4], ey[4], oy[4];
+                e2m1x8_to_f16x2((xa & 0x0f0f0f0fu) | (xb << 4 & 0xf0f0f0f0u), ex);
+                e2m1x8_to_f16x2((xa >> 4 & 0x0f0f0f0fu) | (xb & 0xf0f0f0f0u), ox);
+                e2m1x8_to_f16x2((ya & 0x0f0f0f0fu) | (yb << 4 & 0xf0f0f0f0u), ey);
+                e2m1x8_to_f16x2((ya >> 4 & 0x0f0f0f0fu) | (yb & 0xf0f0f0f0u), oy);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  mma_f16(o[c][4 * w + j], mul_f16x2(ex[j], sx), mul_f16x2(ox[j], sx), mul_f16x2(ey[j], sy),
+                          mul_f16x2(oy[j], sy), wt[hf][0], wt[hf][1]);
+              }
+            }
           ++consumed;
           __syncwarp();
-          if (issued < total_tiles) {
+          if (issued < total) {
             if (lane == 0) fence_proxy_async_smem();  // our reads of this stage come before the refill
             issue();
           }
         }
       }
 
-      // ---- hand this warp's state of item k to the epilogue (buffer k & 1, its use k >> 1)
-      const int hb = k & 1, use = k >> 1;
+      // ---- hand this warp's state of item k to the epilogue (of two buffers: k & 1, its use k >> 1)
+      const int hb = pool.buffers == 2 ? k & 1 : 0, use = pool.buffers == 2 ? k >> 1 : k;
       if (use > 0 && !*s_dead && !mbar_wait(&empty[hb], (uint32_t)((use - 1) & 1), kWaitLimitNs)) {
         if (lane == 0) report(a.status, TG_STATUS_TIMEOUT);
         *s_dead = 1;
@@ -373,8 +427,8 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
         l0 += __shfl_xor_sync(0xffffffffu, l0, off);
         l1 += __shfl_xor_sync(0xffffffffu, l1, off);
       }
-      // the epilogue knows weights that are 1 at the maximum, and V without its unit
-      constexpr float kBack = 1.f / 32768.f;
+      // the epilogue knows weights that are 1 at the reference, and V with its unit
+      constexpr float kBack = 1.f / 256.f;
       const float back = kBack * pool.v_unit;
       float *cm = comb_m + (hb * NW + warp) * 8, *cl = comb_l + (hb * NW + warp) * 8;
       if (gid == 0) {
@@ -396,6 +450,7 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
           oo[0] = oo[1] = oo[2] = oo[3] = 0.f;
         }
       m0 = m1 = -INFINITY;
+      d0 = d1 = INFINITY;
       l0 = l1 = 0.f;
       mbar_arrive(&full[hb]);  // (release: this thread's hand-off writes come first)
     }
@@ -407,13 +462,15 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
     __syncwarp();
     return;
   }
-  decode_epilogue<D, NW, NE, true>(a, get_item, n_items, comb_m, comb_l, comb_o, cfl, ostride, fac, s_mm, s_ll, flag,
+  decode_epilogue<D, NW, NE, true>(a, get_item, n_items, pool.buffers, comb_m, comb_l, comb_o, cfl, ostride, fac, s_mm, s_ll, flag,
                                    s_dead, full, empty, s_t0);
 }
 
 template <int D>
 int launch(cudaStream_t stream, int format, const void *map, const DecodeArgs &args, const Pool4 &pool, int N_CTA) {
   const char *name = "tg_decode_grown";
+  Pool4 p = pool;
+  p.buffers = Layout4<D>::buffers(args.g);
   void *fn;
   int threads, smem;
   if (format == TG_PAGES_BF16) {
@@ -421,12 +478,12 @@ int launch(cudaStream_t stream, int format, const void *map, const DecodeArgs &a
     threads = Layout<D>::THREADS, smem = Layout<D>::smem_bytes(args.g);
   } else {
     fn = reinterpret_cast<void *>(&decode4_kernel<D>);
-    threads = Layout4<D>::THREADS, smem = Layout4<D>::smem_bytes(args.g);
+    threads = Layout4<D>::THREADS, smem = Layout4<D>::bytes(args.g, p.buffers);
   }
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return tgi::fail(TG_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", name, cudaGetErrorString(e));
   void *bf16[] = {const_cast<void *>(map), const_cast<DecodeArgs *>(&args)};
-  void *e2m1[] = {const_cast<DecodeArgs *>(&args), const_cast<Pool4 *>(&pool)};
+  void *e2m1[] = {const_cast<DecodeArgs *>(&args), &p};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(N_CTA);
   cfg.blockDim = dim3(threads);
@@ -471,7 +528,7 @@ extern "C" int tg_decode_grown(tg_stream_t stream, const void *plan_host, const 
   args.ntok = ntok, args.added = added, args.plus = plus, args.reserve = reserve;
   args.wait_tables = 1;  // the kernel before it may have written pages, queries and added
   CUtensorMap map;
-  Pool4 p4 = {static_cast<const uint8_t *>(pool), (int64_t)(hd->P / 16) * (hd->d / 128) * kTile4, v_unit};
+  Pool4 p4 = {static_cast<const uint8_t *>(pool), (int64_t)(hd->P / 16) * (hd->d / 128) * kTile4, v_unit, 2};
   if (format == TG_PAGES_BF16) {
     rc = make_pool_map(&map, static_cast<const uint16_t *>(pool), pool_pages, hd, fn);
     if (rc) return rc;
