@@ -134,178 +134,159 @@ __device__ __forceinline__ void epilogue_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
 }
 
-// The epilogue warps of a CTA (see decode_body), with one or two hand-off buffers.  A piece of a grown run may hold no token: it leaves a
-// partial of no weight.
-template <int D, int NW, int NE, bool GROWN, typename GetItem>
-__device__ __forceinline__ void decode_epilogue(const DecodeArgs &a, GetItem get_item, int n_items, int buffers, const float *comb_m,
-                                                const float *comb_l, const float *comb_o, int cfl, int ostride,
-                                                float *fac, float *s_mm, float *s_ll, int *flag, volatile int *s_dead,
-                                                uint64_t *full, uint64_t *empty, const uint64_t *s_t0) {
+// The epilogue warps of a CTA over grown runs: as decode_body's, with one or two hand-off buffers, and with what the
+// short launches of a decode step wait for kept short.  Four outputs to a thread; the first partials of a
+// merge are on their way while its factors are made; and where the next item is already handed over, it is counted
+// before this one's run is merged: a CTA that ends one run and begins the next would else keep the second run's
+// other CTAs' merge waiting for the first's (one request of 18000 tokens: 17 -> 11 us).
+// A piece of a grown run may hold no token: it leaves a partial of no weight.
+template <int D, int NW, int NE, typename GetItem>
+__device__ __forceinline__ void grown_epilogue(const DecodeArgs &a, GetItem get_item, int n_items, int buffers,
+                                               const float *comb_m, const float *comb_l, const float *comb_o, int cfl,
+                                               int ostride, float *fac, float *s_mm, float *s_ll, volatile int *flag,
+                                               volatile int *s_dead, uint64_t *full, uint64_t *empty, const uint64_t *s_t0) {
   constexpr int NS = NW * 32, NET = NE * 32;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int cta = blockIdx.x;
-  // 2^(m - M), the weight of a part with maximum m; without tokens anywhere M is -inf
-  auto weight = [](float m, float M) -> float { return GROWN && M == -INFINITY ? 0.f : ex2(m - M); };
-  auto mean = [](float O, float L) -> float { return GROWN && L == 0.f ? 0.f : O / L; };
-  const int etid = tid - NS, ew = warp - NW;
-  // the workspace (merge counters, partials) and the outputs may still be in use by the
-  // previous decode launch in the stream: wait for it before the first write
-  griddep_wait();
-  for (int k = 0; k < n_items; ++k) {
-    const tg_work_item it = get_item(k);
-    const int hb = buffers == 2 ? k & 1 : 0, use = buffers == 2 ? k >> 1 : k;
-    if (!*s_dead && !mbar_wait_sleep(&full[hb], (uint32_t)(use & 1), kWaitLimitNs)) {
-      if (etid == 0) report(a.status, TG_STATUS_TIMEOUT);
-      *s_dead = 1;
-    }
-    const float *cm = comb_m + hb * NW * 8, *cl = comb_l + hb * NW * 8, *co = comb_o + hb * cfl;
-    const size_t out_row0 = (size_t)it.b * a.H_q + (size_t)it.h * a.g;
-    if (it.t1 <= it.t0 && (!GROWN || it.nparts == 1)) {  // a head with no token
-      for (int e = etid; e < a.g * D; e += NET) {
-        a.out[(out_row0 + e / D) * D + e % D] = 0;
-        if (e % D == 0 && a.lse) a.lse[out_row0 + e / D] = -INFINITY;
+  const int tid = threadIdx.x, lane = tid & 31, etid = tid - NS, ew = (tid >> 5) - NW;
+  const int g = a.g;
+  // 2^(m - M), the weight of a part with reference m; without tokens anywhere M is -inf
+  auto weight = [](float m, float M) { return M == -INFINITY ? 0.f : ex2(m - M); };
+  auto store4 = [&](size_t row, int dd, const float4 &O, float M, float L) {
+    const float r = L == 0.f ? 0.f : 1.f;  // (no token: 0, and not 0 / 0)
+    const float den = L == 0.f ? 1.f : L;
+    uint2 v;
+    v.x = pack_bf16x2(r * O.x / den, r * O.y / den);
+    v.y = pack_bf16x2(r * O.z / den, r * O.w / den);
+    *reinterpret_cast<uint2 *>(a.out + row * D + dd) = v;
+    if (dd == 0 && a.lse) a.lse[row] = (M + log2f(L)) * kLn2;
+  };
+  auto merge = [&](const tg_work_item &it) {
+    const size_t row0 = (size_t)it.b * a.H_q + (size_t)it.h * g;
+    const int np = it.nparts;
+    const float *pml = a.ws_ml + (size_t)it.slot0 * g * 2;  // [nparts][g][2]
+    const float *po = a.ws_o + (size_t)it.slot0 * g * D;     // [nparts][g][D]
+    constexpr int U = 16;
+    auto load = [&](float4(&v)[U], int e, int p) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (p + u < np) v[u] = __ldcg(reinterpret_cast<const float4 *>(po + (size_t)(p + u) * g * D + e));
+    };
+    if (np * g > kFacMax) {  // more parts than the factor buffer holds: straight loops
+      for (int e = 4 * etid; e < g * D; e += 4 * NET) {
+        const int hd = e / D, dd = e % D;
+        float M = -INFINITY, L = 0.f;
+        for (int p = 0; p < np; ++p) M = fmaxf(M, __ldcg(pml + ((size_t)p * g + hd) * 2));
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = 0; p < np; ++p) {
+          const float f = weight(__ldcg(pml + ((size_t)p * g + hd) * 2), M);
+          const float4 v = __ldcg(reinterpret_cast<const float4 *>(po + (size_t)p * g * D + e));
+          L += __ldcg(pml + ((size_t)p * g + hd) * 2 + 1) * f;
+          O.x += v.x * f, O.y += v.y * f, O.z += v.z * f, O.w += v.w * f;
+        }
+        store4(row0 + hd, dd, O, M, L);
       }
     } else {
+      float4 v[U];
+      load(v, min(4 * etid, g * D - 4), 0);
+      for (int hh = ew; hh < g; hh += NE) {
+        float M = -INFINITY, L = 0.f;
+        float2 ml[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int p = lane + 32 * j;
+          ml[j] = p < np ? __ldcg(reinterpret_cast<const float2 *>(pml + ((size_t)p * g + hh) * 2)) : make_float2(-INFINITY, 0.f);
+          M = fmaxf(M, ml[j].x);
+        }
+        for (int p = lane + 64; p < np; p += 32) M = fmaxf(M, __ldcg(pml + ((size_t)p * g + hh) * 2));
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        for (int p = lane; p < np; p += 32) {
+          const float2 w = p < 64 ? (p < 32 ? ml[0] : ml[1])
+                                  : __ldcg(reinterpret_cast<const float2 *>(pml + ((size_t)p * g + hh) * 2));
+          const float f = weight(w.x, M);
+          fac[p * g + hh] = f;
+          L += w.y * f;
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+        if (lane == 0) s_mm[hh] = M, s_ll[hh] = L;
+      }
+      epilogue_sync<NET>();
+      for (int e = 4 * etid; e < g * D; e += 4 * NET) {  // O = sum_p o_p 2^(m_p - M), parts in order
+        const int hd = e / D, dd = e % D;
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = 0; p < np; p += U) {
+          if (p > 0 || e != 4 * etid) load(v, e, p);
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (p + u < np) {
+              const float f = fac[(p + u) * g + hd];
+              O.x += v[u].x * f, O.y += v[u].y * f, O.z += v[u].z * f, O.w += v[u].w * f;
+            }
+        }
+        store4(row0 + hd, dd, O, s_mm[hd], s_ll[hd]);
+      }
+    }
+    if (etid == 0) a.counters[it.b * a.H + it.h] = 0;
+    epilogue_sync<NET>();  // the factors and (M, L) are used again
+  };
+  int waiting = -1;  // an item whose run this CTA has yet to merge
+  for (int k = 0; k <= n_items; ++k) {
+    int now = -1, later = -1;  // item k, if its run is to be merged now, or after the next item
+    if (k < n_items) {
+      const tg_work_item it = get_item(k);
+      const int hb = buffers == 2 ? k & 1 : 0, use = buffers == 2 ? k >> 1 : k;
+      if (!*s_dead && !mbar_wait_suspended(&full[hb], (uint32_t)(use & 1), kWaitLimitNs)) {
+        if (etid == 0) report(a.status, TG_STATUS_TIMEOUT);
+        *s_dead = 1;
+      }
+      const float *cm = comb_m + hb * NW * 8, *cl = comb_l + hb * NW * 8, *co = comb_o + hb * cfl;
+      const size_t row0 = (size_t)it.b * a.H_q + (size_t)it.h * g;
       const int slot = it.slot0 + it.part;
-      for (int e = etid; e < a.g * D; e += NET) {
+      for (int e = 4 * etid; e < g * D; e += 4 * NET) {
         const int hd = e / D, dd = e % D;
         float M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < NW; ++w) M = fmaxf(M, cm[w * 8 + hd]);
-        float Ls = 0.f, O = 0.f;
+        float L = 0.f;
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
           const float f = weight(cm[w * 8 + hd], M);
-          Ls += cl[w * 8 + hd] * f;
-          O += co[(w * a.g + hd) * ostride + dd] * f;
+          const float4 v = *reinterpret_cast<const float4 *>(co + (w * g + hd) * ostride + dd);
+          L += cl[w * 8 + hd] * f;
+          O.x += v.x * f, O.y += v.y * f, O.z += v.z * f, O.w += v.w * f;
         }
         if (it.nparts == 1) {
-          __nv_bfloat16 v = __float2bfloat16_rn(mean(O, Ls));
-          a.out[(out_row0 + hd) * D + dd] = *reinterpret_cast<uint16_t *>(&v);
-          if (dd == 0 && a.lse) a.lse[out_row0 + hd] = (M + log2f(Ls)) * kLn2;
+          store4(row0 + hd, dd, O, M, L);
         } else {
-          a.ws_o[((size_t)slot * a.g + hd) * D + dd] = O;
-          if (dd == 0) {
-            a.ws_ml[((size_t)slot * a.g + hd) * 2] = M;
-            a.ws_ml[((size_t)slot * a.g + hd) * 2 + 1] = Ls;
-          }
+          *reinterpret_cast<float4 *>(a.ws_o + ((size_t)slot * g + hd) * D + dd) = O;
+          if (dd == 0) *reinterpret_cast<float2 *>(a.ws_ml + ((size_t)slot * g + hd) * 2) = make_float2(M, L);
         }
       }
-    }
-    mbar_arrive(&empty[hb]);  // (release: this thread's reads of the buffer come first)
-    if ((GROWN || it.t1 > it.t0) && it.nparts > 1) {
-      __threadfence();
-      epilogue_sync<NET>();
-      if (etid == 0) {
-        const int prev = atomicAdd(&a.counters[it.b * a.H + it.h], 1);
-        *flag = prev == it.nparts - 1;
-      }
-      epilogue_sync<NET>();
-      if (*flag) {  // the last CTA of this run merges every partial
-        __threadfence();
-        const int np = it.nparts, g = a.g;
-        const float *pml = a.ws_ml + (size_t)it.slot0 * g * 2;  // [nparts][g][2]
-        const float *po = a.ws_o + (size_t)it.slot0 * g * D;     // [nparts][g][D]
-        if (np * g <= kFacMax) {
-          // factors 2^(m_p - M) of every part go to shared memory; per head, one warp gathers
-          // M and L with its lanes striding over the parts (independent loads).  Up to 64 parts,
-          // each lane reads its (m, l) pairs once and keeps them in registers
-          for (int hh = ew; hh < g; hh += NE) {
-            float M = -INFINITY, Ls = 0.f;
-            if (np <= 64) {
-              float2 ml[2];
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const int p = lane + 32 * j;
-                ml[j] = p < np ? __ldcg(reinterpret_cast<const float2 *>(pml + ((size_t)p * g + hh) * 2))
-                               : make_float2(-INFINITY, 0.f);
-                M = fmaxf(M, ml[j].x);
-              }
-#pragma unroll
-              for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const int p = lane + 32 * j;
-                if (p < np) {
-                  const float f = weight(ml[j].x, M);
-                  fac[p * g + hh] = f;
-                  Ls += ml[j].y * f;
-                }
-              }
-            } else {
-              for (int p = lane; p < np; p += 32) M = fmaxf(M, __ldcg(pml + ((size_t)p * g + hh) * 2));
-#pragma unroll
-              for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-              for (int p = lane; p < np; p += 32) {
-                const float f = weight(__ldcg(pml + ((size_t)p * g + hh) * 2), M);
-                fac[p * g + hh] = f;
-                Ls += __ldcg(pml + ((size_t)p * g + hh) * 2 + 1) * f;
-              }
-            }
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, off);
-            if (lane == 0) {
-              s_mm[hh] = M;
-              s_ll[hh] = Ls;
-            }
-          }
-          epilogue_sync<NET>();
-          // O = sum_p o_p 2^(m_p - M), parts in order.  A thread takes four consecutive outputs
-          // of one head (16-byte loads; partial rows are 16-byte aligned), sixteen parts per
-          // batch in flight
-          for (int e = 4 * etid; e < g * D; e += 4 * NET) {
-            const int hd = e / D, dd = e % D;
-            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int p = 0; p < np; p += 16) {
-              float4 v[16];
-#pragma unroll
-              for (int u = 0; u < 16; ++u)
-                v[u] = p + u < np ? __ldcg(reinterpret_cast<const float4 *>(po + (size_t)(p + u) * g * D + e))
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-              for (int u = 0; u < 16; ++u)
-                if (p + u < np) {
-                  const float f = fac[(p + u) * g + hd];
-                  O.x += v[u].x * f;
-                  O.y += v[u].y * f;
-                  O.z += v[u].z * f;
-                  O.w += v[u].w * f;
-                }
-            }
-            const float Ls = s_ll[hd];
-            uint16_t *orow = a.out + (out_row0 + hd) * D + dd;
-            const float ov[4] = {O.x, O.y, O.z, O.w};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              __nv_bfloat16 v = __float2bfloat16_rn(mean(ov[c], Ls));
-              orow[c] = *reinterpret_cast<uint16_t *>(&v);
-            }
-            if (dd == 0 && a.lse) a.lse[out_row0 + hd] = (s_mm[hd] + log2f(s_ll[hd])) * kLn2;
-          }
-        } else {  // more parts than the factor buffer holds: straight loops
-          for (int e = etid; e < g * D; e += NET) {
-            const int hd = e / D, dd = e % D;
-            float M = -INFINITY;
-            for (int p = 0; p < np; ++p) M = fmaxf(M, __ldcg(pml + ((size_t)p * g + hd) * 2));
-            float Ls = 0.f, O = 0.f;
-            for (int p = 0; p < np; ++p) {
-              const float f = weight(__ldcg(pml + ((size_t)p * g + hd) * 2), M);
-              Ls += __ldcg(pml + ((size_t)p * g + hd) * 2 + 1) * f;
-              O += __ldcg(po + (size_t)p * g * D + e) * f;
-            }
-            __nv_bfloat16 v = __float2bfloat16_rn(mean(O, Ls));
-            a.out[(out_row0 + hd) * D + dd] = *reinterpret_cast<uint16_t *>(&v);
-            if (dd == 0 && a.lse) a.lse[out_row0 + hd] = (M + log2f(Ls)) * kLn2;
-          }
+      mbar_arrive(&empty[hb]);  // (release: this thread's reads of the buffer come first)
+      if (it.nparts > 1) {
+        epilogue_sync<NET>();
+        if (etid == 0) {
+          __threadfence();  // the partial, which the barrier has seen written, before the count
+          flag[0] = atomicAdd(&a.counters[it.b * a.H + it.h], 1) == it.nparts - 1;
+          __threadfence();  // the count before the other partials are read
+          const int nb = buffers == 2 ? (k + 1) & 1 : 0, nu = buffers == 2 ? (k + 1) >> 1 : k + 1;
+          flag[2] = k + 1 < n_items && mbar_try_wait(&full[nb], (uint32_t)(nu & 1));
         }
-        if (etid == 0) atomicExch(&a.counters[it.b * a.H + it.h], 0);
+        epilogue_sync<NET>();
+        if (flag[0]) (flag[2] ? later : now) = k;
       }
-      epilogue_sync<NET>();  // the flag, the factors and (M, L) are reused by the next item
     }
+#pragma unroll 1
+    for (int j = 0; j < 2; ++j) {
+      const int m = j ? now : waiting;
+      if (m >= 0) merge(get_item(m));
+    }
+    waiting = later;
   }
   if (etid == 0 && a.cta_time) {
-    a.cta_time[2 * cta] = (int64_t)*s_t0;
-    a.cta_time[2 * cta + 1] = (int64_t)globaltimer_ns();
+    a.cta_time[2 * blockIdx.x] = (int64_t)*s_t0;
+    a.cta_time[2 * blockIdx.x + 1] = (int64_t)globaltimer_ns();
   }
 }
 
@@ -652,8 +633,172 @@ __device__ __forceinline__ void decode_body(const CUtensorMap *pool_map_p, const
     return;
   }
 
-  decode_epilogue<D, NW, NE, GROWN>(a, get_item, n_items, 2, comb_m, comb_l, comb_o, cfl, ostride, fac, s_mm, s_ll, flag,
-                                    s_dead, full, empty, s_t0);
+  if (GROWN) {
+    grown_epilogue<D, NW, NE>(a, get_item, n_items, 2, comb_m, comb_l, comb_o, cfl, ostride, fac, s_mm, s_ll, flag, s_dead,
+                              full, empty, s_t0);
+    return;
+  }
+  // ================================================================== epilogue warps
+  const int etid = tid - NS, ew = warp - NW;
+  // the workspace (merge counters, partials) and the outputs may still be in use by the
+  // previous decode launch in the stream: wait for it before the first write
+  griddep_wait();
+  for (int k = 0; k < n_items; ++k) {
+    const tg_work_item it = get_item(k);
+    const int hb = k & 1, use = k >> 1;
+    if (!*s_dead && !mbar_wait_sleep(&full[hb], (uint32_t)(use & 1), kWaitLimitNs)) {
+      if (etid == 0) report(a.status, TG_STATUS_TIMEOUT);
+      *s_dead = 1;
+    }
+    const float *cm = comb_m + hb * NW * 8, *cl = comb_l + hb * NW * 8, *co = comb_o + hb * cfl;
+    const size_t out_row0 = (size_t)it.b * a.H_q + (size_t)it.h * a.g;
+    if (it.t1 <= it.t0) {  // a head with no retained token
+      for (int e = etid; e < a.g * D; e += NET) {
+        a.out[(out_row0 + e / D) * D + e % D] = 0;
+        if (e % D == 0 && a.lse) a.lse[out_row0 + e / D] = -INFINITY;
+      }
+    } else {
+      const int slot = it.slot0 + it.part;
+      for (int e = etid; e < a.g * D; e += NET) {
+        const int hd = e / D, dd = e % D;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, cm[w * 8 + hd]);
+        float Ls = 0.f, O = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          const float f = ex2(cm[w * 8 + hd] - M);
+          Ls += cl[w * 8 + hd] * f;
+          O += co[(w * a.g + hd) * ostride + dd] * f;
+        }
+        if (it.nparts == 1) {
+          __nv_bfloat16 v = __float2bfloat16_rn(O / Ls);
+          a.out[(out_row0 + hd) * D + dd] = *reinterpret_cast<uint16_t *>(&v);
+          if (dd == 0 && a.lse) a.lse[out_row0 + hd] = (M + log2f(Ls)) * kLn2;
+        } else {
+          a.ws_o[((size_t)slot * a.g + hd) * D + dd] = O;
+          if (dd == 0) {
+            a.ws_ml[((size_t)slot * a.g + hd) * 2] = M;
+            a.ws_ml[((size_t)slot * a.g + hd) * 2 + 1] = Ls;
+          }
+        }
+      }
+    }
+    mbar_arrive(&empty[hb]);  // (release: this thread's reads of the buffer come first)
+    if (it.t1 > it.t0 && it.nparts > 1) {
+      __threadfence();
+      epilogue_sync<NET>();
+      if (etid == 0) {
+        const int prev = atomicAdd(&a.counters[it.b * a.H + it.h], 1);
+        *flag = prev == it.nparts - 1;
+      }
+      epilogue_sync<NET>();
+      if (*flag) {  // the last CTA of this run merges every partial
+        __threadfence();
+        const int np = it.nparts, g = a.g;
+        const float *pml = a.ws_ml + (size_t)it.slot0 * g * 2;  // [nparts][g][2]
+        const float *po = a.ws_o + (size_t)it.slot0 * g * D;     // [nparts][g][D]
+        if (np * g <= kFacMax) {
+          // factors 2^(m_p - M) of every part go to shared memory; per head, one warp gathers
+          // M and L with its lanes striding over the parts (independent loads).  Up to 64 parts,
+          // each lane reads its (m, l) pairs once and keeps them in registers
+          for (int hh = ew; hh < g; hh += NE) {
+            float M = -INFINITY, Ls = 0.f;
+            if (np <= 64) {
+              float2 ml[2];
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const int p = lane + 32 * j;
+                ml[j] = p < np ? __ldcg(reinterpret_cast<const float2 *>(pml + ((size_t)p * g + hh) * 2))
+                               : make_float2(-INFINITY, 0.f);
+                M = fmaxf(M, ml[j].x);
+              }
+#pragma unroll
+              for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const int p = lane + 32 * j;
+                if (p < np) {
+                  const float f = ex2(ml[j].x - M);
+                  fac[p * g + hh] = f;
+                  Ls += ml[j].y * f;
+                }
+              }
+            } else {
+              for (int p = lane; p < np; p += 32) M = fmaxf(M, __ldcg(pml + ((size_t)p * g + hh) * 2));
+#pragma unroll
+              for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+              for (int p = lane; p < np; p += 32) {
+                const float f = ex2(__ldcg(pml + ((size_t)p * g + hh) * 2) - M);
+                fac[p * g + hh] = f;
+                Ls += __ldcg(pml + ((size_t)p * g + hh) * 2 + 1) * f;
+              }
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, off);
+            if (lane == 0) {
+              s_mm[hh] = M;
+              s_ll[hh] = Ls;
+            }
+          }
+          epilogue_sync<NET>();
+          // O = sum_p o_p 2^(m_p - M), parts in order.  A thread takes four consecutive outputs
+          // of one head (16-byte loads; partial rows are 16-byte aligned), sixteen parts per
+          // batch in flight
+          for (int e = 4 * etid; e < g * D; e += 4 * NET) {
+            const int hd = e / D, dd = e % D;
+            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int p = 0; p < np; p += 16) {
+              float4 v[16];
+#pragma unroll
+              for (int u = 0; u < 16; ++u)
+                v[u] = p + u < np ? __ldcg(reinterpret_cast<const float4 *>(po + (size_t)(p + u) * g * D + e))
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+              for (int u = 0; u < 16; ++u)
+                if (p + u < np) {
+                  const float f = fac[(p + u) * g + hd];
+                  O.x += v[u].x * f;
+                  O.y += v[u].y * f;
+                  O.z += v[u].z * f;
+                  O.w += v[u].w * f;
+                }
+            }
+            const float Ls = s_ll[hd];
+            uint16_t *orow = a.out + (out_row0 + hd) * D + dd;
+            const float ov[4] = {O.x, O.y, O.z, O.w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              __nv_bfloat16 v = __float2bfloat16_rn(ov[c] / Ls);
+              orow[c] = *reinterpret_cast<uint16_t *>(&v);
+            }
+            if (dd == 0 && a.lse) a.lse[out_row0 + hd] = (s_mm[hd] + log2f(s_ll[hd])) * kLn2;
+          }
+        } else {  // more parts than the factor buffer holds: straight loops
+          for (int e = etid; e < g * D; e += NET) {
+            const int hd = e / D, dd = e % D;
+            float M = -INFINITY;
+            for (int p = 0; p < np; ++p) M = fmaxf(M, __ldcg(pml + ((size_t)p * g + hd) * 2));
+            float Ls = 0.f, O = 0.f;
+            for (int p = 0; p < np; ++p) {
+              const float f = ex2(__ldcg(pml + ((size_t)p * g + hd) * 2) - M);
+              Ls += __ldcg(pml + ((size_t)p * g + hd) * 2 + 1) * f;
+              O += __ldcg(po + (size_t)p * g * D + e) * f;
+            }
+            __nv_bfloat16 v = __float2bfloat16_rn(O / Ls);
+            a.out[(out_row0 + hd) * D + dd] = *reinterpret_cast<uint16_t *>(&v);
+            if (dd == 0 && a.lse) a.lse[out_row0 + hd] = (M + log2f(Ls)) * kLn2;
+          }
+        }
+        if (etid == 0) atomicExch(&a.counters[it.b * a.H + it.h], 0);
+      }
+      epilogue_sync<NET>();  // the flag, the factors and (M, L) are reused by the next item
+    }
+  }
+  if (etid == 0 && a.cta_time) {
+    a.cta_time[2 * cta] = (int64_t)*s_t0;
+    a.cta_time[2 * cta + 1] = (int64_t)globaltimer_ns();
+  }
 }
 
 

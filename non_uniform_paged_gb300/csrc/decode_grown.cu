@@ -54,9 +54,9 @@ struct Layout4 {
   static constexpr int TILE = D / 128 * kTile4;  // 16 tokens
   static constexpr int STAGE = 2 * TILE;
   static constexpr int RING = NW * R * STAGE;
-  // as Layout: barriers, start time, items and their page-table bases and order, hand-off (m, l), merged (M, L), flags
-  static constexpr int SMALL = NW * R * 8 + 4 * 8 + 8 + kMaxItems * (8 + (int)sizeof(tg_work_item)) +
-                               kMaxItems * 4 + 2 * NW * 8 * 4 * 2 + 8 * 4 * 2 + 16;
+  // as Layout: barriers, start time, items and the bounds of their page lists, hand-off (m, l), merged (M, L), flags
+  static constexpr int SMALL = NW * R * 8 + 4 * 8 + 8 + kMaxItems * (16 + (int)sizeof(tg_work_item)) +
+                               2 * NW * 8 * 4 * 2 + 8 * 4 * 2 + 16;
   static constexpr int MOST = 227 * 1024;
   __host__ __device__ static int ostride(int g) { return g <= 4 ? D + 4 : D; }
   __host__ __device__ static int comb_floats(int g) { return NW * g * ostride(g); }
@@ -95,7 +95,7 @@ __device__ __forceinline__ uint32_t lds16(uint32_t addr) {
 
 struct Pool4 {
   const uint8_t *base;
-  int64_t head_bytes;  // of a head in a page
+  int p16;  // tiles of a head in a page
   float v_unit;
   int buffers;  // hand-off buffers
 };
@@ -104,20 +104,20 @@ template <int D>
 __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const DecodeArgs a, const Pool4 pool) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   using LY = Layout4<D>;
-  constexpr int NW = LY::NW, R = LY::R, NE = LY::NE, NT = LY::THREADS, C = D / 128;  // C: tiles side by side
+  constexpr int NW = LY::NW, R = LY::R, NE = LY::NE, C = D / 128;  // C: tiles side by side
   constexpr int NS = NW * 32, NET = NE * 32;
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem_raw);                 // [NW][R] copy stages
   uint64_t *full = bars + NW * R;                                          // [2] hand-off buffer written
   uint64_t *empty = full + 2;                                              // [2] hand-off buffer read
   uint64_t *s_t0 = empty + 2;                                              // CTA start (globaltimer)
-  int64_t *s_base = reinterpret_cast<int64_t *>(s_t0 + 1);                 // [kMaxItems]
-  tg_work_item *s_items = reinterpret_cast<tg_work_item *>(s_base + kMaxItems);
-  int *s_order = reinterpret_cast<int *>(s_items + kMaxItems);             // [kMaxItems] processing order
-  float *comb_m = reinterpret_cast<float *>(s_order + kMaxItems);          // [2][NW][8]
+  int64_t *s_base = reinterpret_cast<int64_t *>(s_t0 + 1);                 // [kMaxItems] first entry of the page list
+  int64_t *s_end = s_base + kMaxItems;                                     // [kMaxItems] and behind its last
+  tg_work_item *s_items = reinterpret_cast<tg_work_item *>(s_end + kMaxItems);  // [kMaxItems] in processing order
+  float *comb_m = reinterpret_cast<float *>(s_items + kMaxItems);          // [2][NW][8]
   float *comb_l = comb_m + 2 * NW * 8;                                     // [2][NW][8]
   float *s_mm = comb_l + 2 * NW * 8;                                       // [8]
   float *s_ll = s_mm + 8;                                                  // [8]
-  int *flag = reinterpret_cast<int *>(s_ll + 8);                           // last CTA of a shared run
+  int *flag = reinterpret_cast<int *>(s_ll + 8);
   volatile int *s_dead = flag + 1;                                         // a hand-off wait gave up
   uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + LY::SMALL + 127) & ~uintptr_t(127));
   const int ostride = LY::ostride(a.g), cfl = LY::comb_floats(a.g);
@@ -131,14 +131,11 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
   const tg_work_item lead = a.lead[blockIdx.x];
   const int n_items = lead.reserved[0], i_begin = lead.reserved[1];
   const bool items_in_smem = n_items <= kMaxItems;
-  if (items_in_smem) {
-    tg_work_item first = lead;
-    first.reserved[0] = first.reserved[1] = 0;
-    for (int i = tid; i < n_items; i += NT) s_items[i] = i == 0 ? first : a.items[i_begin + i];
-  }
+  tg_work_item mine = lead;  // of warp 0's lanes: item `lane`
+  if (items_in_smem && warp == 0 && lane > 0 && lane < n_items) mine = a.items[i_begin + lane];
   if (warp < NW && lane == 0)
     for (int s = 0; s < R; ++s) mbar_init(&bars[warp * R + s], 1);
-  if (tid == 0) {
+  if (tid == NS) {
     for (int b = 0; b < 2; ++b) {
       mbar_init(&full[b], NS);
       mbar_init(&empty[b], NET);
@@ -148,26 +145,22 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
   fence_barrier_init();
   griddep_wait();
   griddep_launch_dependents();
-  if (items_in_smem)
-    for (int i = tid; i < n_items; i += NT) {
-      s_items[i] = grown_item(a, s_items[i]);
-      s_base[i] = __ldcg(a.pt_off + s_items[i].b * a.G + s_items[i].g);
+  if (warp == 0 && items_in_smem) {
+    // shared-run pieces first, then owned runs, each in plan order
+    const bool have = lane < n_items;
+    const unsigned all = __ballot_sync(0xffffffffu, have), shared = __ballot_sync(0xffffffffu, have && mine.nparts > 1);
+    const unsigned before = (1u << lane) - 1;
+    const int at = shared >> lane & 1 ? __popc(shared & before) : __popc(shared) + __popc(all & ~shared & before);
+    if (have) {
+      const int64_t *off = a.pt_off + (int64_t)mine.b * a.G + mine.g;
+      const int64_t base = __ldcg(off), end = __ldcg(off + 1);
+      s_items[at] = grown_item(a, mine);
+      s_base[at] = base;
+      s_end[at] = end;
     }
-  __syncthreads();
-  if (tid == 0 && items_in_smem) {  // shared-run pieces first, then owned runs, each in plan order
-    int c = 0;
-    for (int i = 0; i < n_items; ++i)
-      if (s_items[i].nparts > 1) s_order[c++] = i;
-    for (int i = 0; i < n_items; ++i)
-      if (s_items[i].nparts <= 1) s_order[c++] = i;
   }
   __syncthreads();
-  auto get_item = [&](int k) -> tg_work_item {
-    return items_in_smem ? s_items[s_order[k]] : grown_item(a, a.items[i_begin + k]);
-  };
-  auto get_base = [&](int k, const tg_work_item &it) -> int64_t {
-    return items_in_smem ? s_base[s_order[k]] : __ldcg(a.pt_off + it.b * a.G + it.g);
-  };
+  auto get_item = [&](int k) -> tg_work_item { return items_in_smem ? s_items[k] : grown_item(a, a.items[i_begin + k]); };
 
   if (warp < NW) {
     // ================================================================ streaming warps
@@ -177,39 +170,60 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
       const int n = it.t1 > it.t0 ? ((it.t1 + 31) >> 5) - lo : 0;
       return n > warp ? (n - warp + NW - 1) / NW : 0;
     };
-    int total = 0;
-    for (int k = 0; k < n_items; ++k) {
+    // where a warp's steps of item k end: of up to 16 items in lane k, of more they are counted again
+    int total = 0, ends = 0;
+    if (items_in_smem) {
       int lo;
-      total += warp_steps(get_item(k), lo);
-    }
-    // where the two tiles of a step of this warp lie: sixteen steps looked up at a time, a tile by each lane, a batch
-    // ahead; kNone: no token of the item in it
-    constexpr int64_t kBad = -1, kNone = -2;
-    auto tile_at = [&](int n) -> int64_t {
-      if (n >= 2 * total) return kNone;
-      int rem = n >> 1;
-      for (int k = 0; k < n_items; ++k) {
-        const tg_work_item it = get_item(k);
-        int lo;
-        const int cnt = warp_steps(it, lo);
-        if (rem < cnt) {
-          const int tok = 32 * (lo + warp + NW * rem) + 16 * (n & 1);
-          if (tok + 16 <= it.t0 || tok >= it.t1) return kNone;
-          const int64_t at = get_base(k, it) + tok / a.P;
-          if (at >= __ldcg(a.pt_off + it.b * a.G + it.g + 1)) return kBad;  // a list too short
-          const int32_t page = __ldcg(a.pt_ids + at);
-          if (page < 0 || page >= a.pool_pages) return kBad;
-          return ((int64_t)page * a.H_p + it.hpos) * pool.head_bytes + (tok % a.P / 16) * LY::TILE;
-        }
-        rem -= cnt;
+      ends = lane < n_items ? warp_steps(s_items[lane], lo) : 0;
+#pragma unroll
+      for (int d = 1; d < kMaxItems; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, ends, d);
+        if (lane >= d) ends += v;
       }
-      return kNone;
+      total = __shfl_sync(0xffffffffu, ends, kMaxItems - 1);
+    } else {
+      for (int k = 0; k < n_items; ++k) {
+        int lo;
+        total += warp_steps(get_item(k), lo);
+      }
+    }
+    // The two tiles of a step of this warp, by their number in the pool: sixteen steps looked up at a time by the whole
+    // warp, a tile by each lane, a batch ahead.  kNone: no token of the item in it.
+    constexpr int kBad = -1, kNone = -2;
+    auto tile_at = [&](int n) -> int {
+      int step = n >> 1, lo;
+      tg_work_item it;
+      int64_t base, end;
+      if (items_in_smem) {
+        int k = 0;
+        for (int i = 0; i < n_items - 1; ++i) k += step >= __shfl_sync(0xffffffffu, ends, i);
+        const int first = __shfl_sync(0xffffffffu, ends, max(k - 1, 0));
+        if (n >= 2 * total) return kNone;
+        step -= k > 0 ? first : 0;
+        it = s_items[k], base = s_base[k], end = s_end[k];
+      } else {
+        if (n >= 2 * total) return kNone;
+        for (int k = 0; k < n_items; ++k) {
+          it = get_item(k);
+          const int cnt = warp_steps(it, lo);
+          if (step < cnt) break;
+          step -= cnt;
+        }
+        base = __ldcg(a.pt_off + it.b * a.G + it.g), end = __ldcg(a.pt_off + it.b * a.G + it.g + 1);
+      }
+      const int tok = 32 * ((it.t0 >> 5) + warp + NW * step) + 16 * (n & 1);
+      if (tok + 16 <= it.t0 || tok >= it.t1) return kNone;
+      const int t = tok >> 4, in_list = pool.p16 == 1 ? t : t / pool.p16;
+      if (base + in_list >= end) return kBad;  // a list too short
+      const int32_t page = __ldcg(a.pt_ids + base + in_list);
+      if (page < 0 || page >= a.pool_pages) return kBad;
+      return (page * a.H_p + it.hpos) * pool.p16 + t - in_list * pool.p16;
     };
-    int64_t at_cur = tile_at(lane), at_nxt = tile_at(32 + lane);
+    int at_cur = tile_at(lane), at_nxt = tile_at(32 + lane);
     int issued = 0, consumed = 0;
     auto issue = [&]() {  // whole warp: step number `issued` of this warp into stage issued % R
       const int from = 2 * (issued & 15);
-      const int64_t at0 = __shfl_sync(0xffffffffu, at_cur, from), at1 = __shfl_sync(0xffffffffu, at_cur, from + 1);
+      const int at0 = __shfl_sync(0xffffffffu, at_cur, from), at1 = __shfl_sync(0xffffffffu, at_cur, from + 1);
       if (lane == 0) {
         const int s = issued % R;
         uint64_t *bar = &bars[warp * R + s];
@@ -217,8 +231,8 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
         if (at0 == kBad || at1 == kBad) report(a.status, TG_STATUS_BAD_PAGE);
         // (a phase without data completes at once)
         mbar_arrive_expect_tx(bar, (at0 >= 0 ? LY::TILE : 0) + (at1 >= 0 ? LY::TILE : 0));
-        if (at0 >= 0) bulk_load(to, pool.base + at0, LY::TILE, bar);
-        if (at1 >= 0) bulk_load(to + LY::TILE, pool.base + at1, LY::TILE, bar);
+        if (at0 >= 0) bulk_load(to, pool.base + (int64_t)at0 * LY::TILE, LY::TILE, bar);
+        if (at1 >= 0) bulk_load(to + LY::TILE, pool.base + (int64_t)at1 * LY::TILE, LY::TILE, bar);
       }
       ++issued;
       if ((issued & 15) == 0) {
@@ -280,9 +294,7 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
         for (int i = 0; i < steps; ++i) {
           const int kk = lo + warp + i * NW;
           const int s = consumed % R;
-          bool ok = mbar_wait(&bars[warp * R + s], (uint32_t)((consumed / R) & 1), kWaitLimitNs);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) {
+          if (!__all_sync(0xffffffffu, mbar_wait_suspended(&bars[warp * R + s], (uint32_t)((consumed / R) & 1), kWaitLimitNs))) {
             if (lane == 0) report(a.status, TG_STATUS_TIMEOUT);
             dead = true;
             break;
@@ -462,8 +474,8 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
     __syncwarp();
     return;
   }
-  decode_epilogue<D, NW, NE, true>(a, get_item, n_items, pool.buffers, comb_m, comb_l, comb_o, cfl, ostride, fac, s_mm, s_ll, flag,
-                                   s_dead, full, empty, s_t0);
+  grown_epilogue<D, NW, NE>(a, get_item, n_items, pool.buffers, comb_m, comb_l, comb_o, cfl, ostride, fac, s_mm, s_ll, flag,
+                            s_dead, full, empty, s_t0);
 }
 
 template <int D>
@@ -528,7 +540,7 @@ extern "C" int tg_decode_grown(tg_stream_t stream, const void *plan_host, const 
   args.ntok = ntok, args.added = added, args.plus = plus, args.reserve = reserve;
   args.wait_tables = 1;  // the kernel before it may have written pages, queries and added
   CUtensorMap map;
-  Pool4 p4 = {static_cast<const uint8_t *>(pool), (int64_t)(hd->P / 16) * (hd->d / 128) * kTile4, v_unit, 2};
+  Pool4 p4 = {static_cast<const uint8_t *>(pool), hd->P / 16, v_unit, 2};
   if (format == TG_PAGES_BF16) {
     rc = make_pool_map(&map, static_cast<const uint16_t *>(pool), pool_pages, hd, fn);
     if (rc) return rc;
@@ -536,8 +548,8 @@ extern "C" int tg_decode_grown(tg_stream_t stream, const void *plan_host, const 
     if (!unit_ok(k_unit) || !unit_ok(v_unit))
       return fail(TG_ERR_INVALID_ARG, "%s: k_unit=%g, v_unit=%g (powers of two in [2^-60, 2^60])", fn, (double)k_unit,
                   (double)v_unit);
-    if (pool_pages <= 0 || pool_pages > INT32_MAX)
-      return fail(TG_ERR_CAPACITY, "%s: pool_pages=%lld (1..2^31-1)", fn, (long long)pool_pages);
+    if (pool_pages <= 0 || pool_pages > INT32_MAX / hd->H_p / p4.p16)
+      return fail(TG_ERR_CAPACITY, "%s: pool_pages=%lld gives more than 2^31-1 tiles, or none", fn, (long long)pool_pages);
     args.scale_log2 *= k_unit;
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
