@@ -537,7 +537,7 @@ def _setup():
         _calls.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
                       for n in ("tg_qk_norm_rope", "tg_prefill_attn", "tg_prefix_attn")))
         _calls.bind_pages(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
-                            for n in ("tg_append_rope", "tg_decode_grown")))
+                            for n in ("tg_append_rope", "tg_decode_grown", "tg_quant_pages", "tg_dequant_pages")))
         _fast = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, _calls)
     return _fast
 
@@ -747,75 +747,28 @@ def tg_decode_grown(plan: DecodePlan, layer: int, fmt: int, q, pool, pool_pages:
         _check(rc)
 
 
-def _here(*tensors):
-    """The tensors' device is the current one: their pointers are of it."""
-    import torch
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
-
-
-def _pool_pages(t, name, page_bytes, pages):
-    if t.numel() * t.element_size() < pages * page_bytes:
-        raise ValueError(f"{name} holds {t.numel() * t.element_size() // page_bytes} pages, not {pages}")
-
-
-def _lists(t, name, n):
-    if t.numel() != n:
-        raise ValueError(f"{name} has {t.numel()} entries, not {n}")
-
-
-def _convert_args(head_order, ntok, src_off, src_ids, src, src_pages, dst_off, dst_ids, dst, dst_pages, H_p, P, d, dev_status,
-                  to4):
-    """What both conversions check of their tensors -> (batch, H)."""
-    import torch
-    for t, n in ((head_order, "head_order"), (ntok, "ntok"), (src_off, "src_off"), (src_ids, "src_ids"), (src, "src"),
-                 (dst_off, "dst_off"), (dst_ids, "dst_ids"), (dst, "dst")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{n} must be a CUDA torch.Tensor")
-    if ntok.dim() != 2:
-        raise ValueError("ntok must be [batch][H]")
-    batch, H = ntok.shape
-    _here(head_order, ntok, src_off, src_ids, src, dst_off, dst_ids, dst, dev_status)
-    _lists(head_order, "head_order", H)
-    if H_p > 0:
-        for t, n in ((src_off, "src_off"), (dst_off, "dst_off")):
-            _lists(t, n, batch * (H // H_p) + 1)
-    _pool_pages(src, "src", tg_page_bytes(PAGES_BF16 if to4 else PAGES_E2M1, H_p, P, d), src_pages)
-    _pool_pages(dst, "dst", tg_page_bytes(PAGES_E2M1 if to4 else PAGES_BF16, H_p, P, d), dst_pages)
-    return batch, H
-
-
 def tg_quant_pages(head_order, ntok, H_p, P, d, src_off, src_ids, src, src_pages, dst_off, dst_ids, dst, dst_pages,
                    k_unit=1.0, v_unit=1.0, dev_status=None, stream=None):
     """Retained tokens of one layer from bf16 pages into 4-bit pages (tg.h: tg_quant_pages): src bf16, dst uint8."""
-    import torch
-    batch, H = _convert_args(head_order, ntok, src_off, src_ids, src, src_pages, dst_off, dst_ids, dst, dst_pages, H_p, P, d,
-                             dev_status, True)
-    _check(load().tg_quant_pages(_stream(stream), batch, H, H_p, P, d, _dev(head_order, torch.int32, "head_order"),
-                                 _dev(ntok, torch.int32, "ntok"), _dev(src_off, torch.int64, "src_off"),
-                                 _dev(src_ids, torch.int32, "src_ids"), _dev(src, torch.bfloat16, "src"), int(src_pages),
-                                 _dev(dst_off, torch.int64, "dst_off"), _dev(dst_ids, torch.int32, "dst_ids"),
-                                 _dev(dst, torch.uint8, "dst"), int(dst_pages), float(k_unit), float(v_unit),
-                                 _dev(dev_status, torch.int32, "dev_status")))
+    device, current, calls = _fast or _setup()
+    dev = device()
+    rc = calls.convert_pages(current(dev) if stream is None else _raw_stream(stream), dev, True, head_order, ntok, None, 0, 0,
+                             H_p, P, d, src_off, src_ids, src, src_pages, dst_off, dst_ids, dst, dst_pages, k_unit, v_unit,
+                             dev_status)
+    if rc:
+        _check(rc)
 
 
 def tg_dequant_pages(head_order, ntok, H_p, P, d, src_off, src_ids, src, src_pages, dst_off, dst_ids, dst, dst_pages,
                      added=None, plus=0, reserve=0, k_unit=1.0, v_unit=1.0, dev_status=None, stream=None):
     """Tokens of one layer from 4-bit pages into bf16 pages (tg.h: tg_dequant_pages): src uint8, dst bf16."""
-    import torch
-    batch, H = _convert_args(head_order, ntok, src_off, src_ids, src, src_pages, dst_off, dst_ids, dst, dst_pages, H_p, P, d,
-                             dev_status, False)
-    if added is not None:
-        _here(added)
-        _lists(added, "added", batch)
-    _check(load().tg_dequant_pages(_stream(stream), batch, H, H_p, P, d, _dev(head_order, torch.int32, "head_order"),
-                                   _dev(ntok, torch.int32, "ntok"), _dev(added, torch.int32, "added"), int(plus),
-                                   int(reserve), _dev(src_off, torch.int64, "src_off"), _dev(src_ids, torch.int32, "src_ids"),
-                                   _dev(src, torch.uint8, "src"), int(src_pages), _dev(dst_off, torch.int64, "dst_off"),
-                                   _dev(dst_ids, torch.int32, "dst_ids"), _dev(dst, torch.bfloat16, "dst"), int(dst_pages),
-                                   float(k_unit), float(v_unit), _dev(dev_status, torch.int32, "dev_status")))
+    device, current, calls = _fast or _setup()
+    dev = device()
+    rc = calls.convert_pages(current(dev) if stream is None else _raw_stream(stream), dev, False, head_order, ntok, added, plus,
+                             reserve, H_p, P, d, src_off, src_ids, src, src_pages, dst_off, dst_ids, dst, dst_pages, k_unit,
+                             v_unit, dev_status)
+    if rc:
+        _check(rc)
 
 
 def tg_check_status(dev_status) -> int:

@@ -1,6 +1,6 @@
 // Calls of a decode step's latency path without ctypes: checks of the tensors and the call into
-// libtg, for tg_qk_norm_rope, tg_prefill_attn and tg_prefix_attn, and for tg_append_rope and
-// tg_decode_grown.  Marshalling only, like the
+// libtg, for tg_qk_norm_rope, tg_prefill_attn and tg_prefix_attn, and for tg_append_rope,
+// tg_decode_grown, tg_quant_pages and tg_dequant_pages.  Marshalling only, like the
 // ctypes binding beside it; a dozen tensors checked from Python and passed through ctypes took
 // 9 us a call, more than the kernels of a small step.
 //
@@ -22,8 +22,12 @@ Prefill prefill_fn = nullptr;
 Prefix prefix_fn = nullptr;
 using Append = decltype(&tg_append_rope);
 using Grown = decltype(&tg_decode_grown);
+using Quant = decltype(&tg_quant_pages);
+using Dequant = decltype(&tg_dequant_pages);
 Append append_fn = nullptr;
 Grown grown_fn = nullptr;
+Quant quant_fn = nullptr;
+Dequant dequant_fn = nullptr;
 
 struct Refused {};  // a Python exception is set
 
@@ -251,27 +255,30 @@ PyObject *prefix_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
-// bind_pages(append, grown): addresses of the libtg functions
+// bind_pages(append, grown, quant, dequant): addresses of the libtg functions
 PyObject *bind_pages(PyObject *, PyObject *const *a, Py_ssize_t n) {
-  return guarded(n, 2, [&] {
+  return guarded(n, 4, [&] {
     append_fn = reinterpret_cast<Append>(pointer(a[0]));
     grown_fn = reinterpret_cast<Grown>(pointer(a[1]));
+    quant_fn = reinterpret_cast<Quant>(pointer(a[2]));
+    dequant_fn = reinterpret_cast<Dequant>(pointer(a[3]));
     return 0;
   });
 }
 
 // A pool of `pages` pages of the format: bf16, or bytes for 4-bit pages.
-void *pool_arg(PyObject *o, int64_t dev, int format, int64_t pages, int64_t H_p, int64_t P, int64_t d) {
-  const at::Tensor &pool = tensor(o, "pool", dev);
+void *pool_arg(PyObject *o, int64_t dev, int format, int64_t pages, int64_t H_p, int64_t P, int64_t d,
+               const char *name = "pool") {
+  const at::Tensor &pool = tensor(o, name, dev);
   const bool bf16 = format == TG_PAGES_BF16;
-  check_type(pool, "pool", bf16 ? kBf16 : at::kByte);
+  check_type(pool, name, bf16 ? kBf16 : at::kByte);
   const int64_t page = bf16 ? H_p * 2 * P * d : H_p * (P / 16) * (d / 128) * TG_TILE4_BYTES;
   const int64_t held = page > 0 ? pool.numel() / page : 0;
   if (pages > held) {
-    PyErr_Format(PyExc_ValueError, "pool holds %lld pages, not %lld", (long long)held, (long long)pages);
+    PyErr_Format(PyExc_ValueError, "%s holds %lld pages, not %lld", name, (long long)held, (long long)pages);
     throw Refused();
   }
-  return address<void>(pool, "pool");
+  return address<void>(pool, name);
 }
 
 // (stream, device, qkv, cu_q, cos_sin, q, pool, pool_pages, head_order, ntok, added, reserve, pt_off, pt_ids, H_p, P,
@@ -343,6 +350,37 @@ PyObject *append_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// (stream, device, to 4 bits, head_order, ntok, added, plus, reserve, H_p, P, d, src_off, src_ids, src, src_pages, dst_off,
+//  dst_ids, dst, dst_pages, k_unit, v_unit, dev_status)
+PyObject *convert_pages(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 22, [&] {
+    const int64_t dev = integer(a[1]), src_pages = integer(a[14]), dst_pages = integer(a[18]);
+    const bool to4 = PyObject_IsTrue(a[2]) == 1;
+    const at::Tensor &ntok = tensor(a[4], "ntok", dev);
+    check_dims(ntok, "ntok", 2);
+    const int batch = small(ntok.size(0), "batch"), H = small(ntok.size(1), "H");
+    const int H_p = small(integer(a[8]), "H_p"), P = small(integer(a[9]), "P"), d = small(integer(a[10]), "d");
+    const int64_t lists = H_p > 0 ? (int64_t)batch * (H / H_p) : 0;
+    const tg_stream_t stream = stream_of(a[0]);
+    const int32_t *order = arg<int32_t>(a[3], "head_order", dev, kI32, {H}), *counts = arg<int32_t>(a[4], "ntok", dev, kI32);
+    const int32_t *added = opt<int32_t>(a[5], "added", dev, kI32, std::initializer_list<int64_t>{batch});
+    const int plus = small(integer(a[6]), "plus"), reserve = small(integer(a[7]), "reserve");
+    const int64_t *src_off = arg<int64_t>(a[11], "src_off", dev, at::kLong, {lists + 1});
+    const int64_t *dst_off = arg<int64_t>(a[15], "dst_off", dev, at::kLong, {lists + 1});
+    const int32_t *src_ids = arg<int32_t>(a[12], "src_ids", dev, kI32), *dst_ids = arg<int32_t>(a[16], "dst_ids", dev, kI32);
+    void *src = pool_arg(a[13], dev, to4 ? TG_PAGES_BF16 : TG_PAGES_E2M1, src_pages, H_p, P, d, "src");
+    void *dst = pool_arg(a[17], dev, to4 ? TG_PAGES_E2M1 : TG_PAGES_BF16, dst_pages, H_p, P, d, "dst");
+    const float k_unit = (float)real(a[19]), v_unit = (float)real(a[20]);
+    int32_t *status = opt<int32_t>(a[21], "dev_status", dev, kI32);
+    if (to4)
+      return unlocked(quant_fn, stream, batch, H, H_p, P, d, order, counts, src_off, src_ids,
+                      static_cast<const uint16_t *>(src), src_pages, dst_off, dst_ids, dst, dst_pages, k_unit, v_unit, status);
+    return unlocked(dequant_fn, stream, batch, H, H_p, P, d, order, counts, added, plus, reserve, src_off, src_ids,
+                    static_cast<const void *>(src), src_pages, dst_off, dst_ids, static_cast<uint16_t *>(dst), dst_pages, k_unit,
+                    v_unit, status);
+  });
+}
+
 // (stream, device, plan host, plan device, layer, format, q, pool, pool_pages, pt_off, pt_ids, ntok, added, plus, reserve,
 //  scale, k_unit, v_unit, out, lse, workspace, dev_status, cta_time)
 PyObject *decode_grown(PyObject *, PyObject *const *a, Py_ssize_t n) {
@@ -377,6 +415,8 @@ PyMethodDef methods[] = {{"bind", reinterpret_cast<PyCFunction>(reinterpret_cast
                          {"bind_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind_pages)),
                           METH_FASTCALL, nullptr},
                          {"append_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append_rope)),
+                          METH_FASTCALL, nullptr},
+                         {"convert_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(convert_pages)),
                           METH_FASTCALL, nullptr},
                          {"decode_grown", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(decode_grown)),
                           METH_FASTCALL, nullptr},

@@ -164,7 +164,7 @@ __device__ __forceinline__ void grown_epilogue(const DecodeArgs &a, GetItem get_
     const int np = it.nparts;
     const float *pml = a.ws_ml + (size_t)it.slot0 * g * 2;  // [nparts][g][2]
     const float *po = a.ws_o + (size_t)it.slot0 * g * D;     // [nparts][g][D]
-    constexpr int U = 16;
+    constexpr int U = 8;
     auto load = [&](float4(&v)[U], int e, int p) {
 #pragma unroll
       for (int u = 0; u < U; ++u)

@@ -50,6 +50,7 @@ struct Cfg4<256> {
 template <int D>
 struct Layout4 {
   static constexpr int NW = Cfg4<D>::NW, R = Cfg4<D>::R, NE = Cfg4<D>::NE;
+  static_assert(R < 16, "the second batch of tiles is looked up behind the first copies");
   static constexpr int THREADS = (NW + NE) * 32;
   static constexpr int TILE = D / 128 * kTile4;  // 16 tokens
   static constexpr int STAGE = 2 * TILE;
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
       if (page < 0 || page >= a.pool_pages) return kBad;
       return (page * a.H_p + it.hpos) * pool.p16 + t - in_list * pool.p16;
     };
-    int at_cur = tile_at(lane), at_nxt = tile_at(32 + lane);
+    int at_cur = tile_at(lane), at_nxt = 0;
     int issued = 0, consumed = 0;
     auto issue = [&]() {  // whole warp: step number `issued` of this warp into stage issued % R
       const int from = 2 * (issued & 15);
@@ -241,6 +242,7 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
       }
     };
     for (int s = 0; s < R && issued < total; ++s) issue();
+    at_nxt = tile_at(32 + lane);  // (looked up behind the first copies, which are fewer than sixteen steps)
 
     bool dead = false;  // a copy wait timed out: skip all further tiles, keep handing off
     // the reference of each head's weights, 8 less it, and their sum
