@@ -7,14 +7,20 @@
 //
 // A block is a warp: one token, or one batch of a token's heads where there are few tokens.  A head is d / 8
 // lanes; a lane's 8 values are 4 first and the 4 second ones of its pairs (i, i + rot/2), so that the rotation
-// exchanges nothing, or 8 consecutive ones (pairs (2i, 2i + 1), values behind rot, V).  Each batch's heads have
-// their rows looked up by as many lanes at once, before their values are needed.
+// exchanges nothing, or 8 consecutive ones (pairs (2i, 2i + 1), values behind rot, V).  Where the heads' rows lie is
+// looked up once, for 32 places of the groups at a time, each by a lane; K and V lie side by side.  A batch's
+// projections are on their way while the one before it is worked on.
 //
 // 4-bit pages.  A head's rotated values go through shared memory, so that a lane has 8 consecutive ones and a pair
-// of lanes a block of 16.  float32 leaves a value z off by some 2^-20 of the row's largest, which decides a
-// code or a scale wrongly where z / s comes that close to the border of two.  So both are taken of the value moved
-// down and up by 2^-18 of the row's largest; where they differ (a row in a hundred) the row is computed
-// again in float64, from the projections in registers.  V is exact and needs none of this.
+// of lanes a block of 16.  float32 leaves a value z = f (u c x_u - v s x_v) off by at most 15 2^-24 t,
+// t = f (|u c x_u| + |v s x_v|): 11 in f (13 additions of squares halved by the root, 4 in rsqrtf), four roundings in the
+// rest; z / s adds three, and two are to spare.  That decides a code or a scale wrongly where z / s comes so close
+// to the border of two.  So both are taken of the value moved down and up by as much, with the block's
+// largest t; where they differ (a row in some hundred) the row is computed again in float64, from the projections in
+// registers, and what was open is taken from that.  V is exact and needs none of this.  (2600 tokens of 16 + 16 heads
+// of 256: with a bound by the row's largest value and float64 divisions 23 us of 56; with the keys'
+// loop unrolled, 16 more, waiting for instructions.)
+#include "packed.cuh"
 #include "page4.cuh"
 #include "ptx.cuh"
 #include "tg_internal.h"
@@ -38,10 +44,10 @@ struct AppendArgs {
   uint8_t *pool;
   uint16_t *q, *K, *V;
   int32_t *status;
-  int batch, H_q, H, H_p, P, Nmax, rot, max_pos, axes, reserve;
+  int batch, H_q, H, H_p, G, P, Nmax, rot, max_pos, axes, reserve;
   int q_batches, kv_batches;  // batches of the query heads, and of the key (and of the value) heads
-  int parts;                  // warps of a token: one, or one for each of its batches
-  float eps, k_unit, v_unit;
+  int parts;                  // warps of a token: 1, 3 (queries, keys, values), or one for each of its batches
+  float eps, k_unit, v_unit, k_to_unit, v_to_unit;  // to: the reciprocals
   uint32_t axis[8];  // two bits for each pair
 };
 
@@ -52,15 +58,8 @@ struct Head8 {  // a lane's 8 values of a head
 __device__ __forceinline__ float2 unpack2(uint32_t v) {
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
-__device__ __forceinline__ void unpack8(const Head8 &h, float (&x)[8]) {
-  const uint32_t w[4] = {h.a.x, h.a.y, h.b.x, h.b.y};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack2(w[i]);
-    x[2 * i] = f.x, x[2 * i + 1] = f.y;
-  }
-}
-// a float64 value in float32 for a rounding to a few bits: cut off, the last bit set where something was
+// A float64 value in float32 for a rounding to a few bits: cut off, the last bit set where something was, so that the
+// rounding knows a tie.
 __device__ __forceinline__ float sticky(double v) {
   float f = __double2float_rz(v);
   if ((double)f != v) f = __uint_as_float(__float_as_uint(f) | 1u);
@@ -68,23 +67,21 @@ __device__ __forceinline__ float sticky(double v) {
 }
 
 template <int D, bool PAIRS, bool E2M1>
-__global__ void __launch_bounds__(32, E2M1 ? 20 : 24) append_rope_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(32, E2M1 ? 20 : 24) append_rope_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int LANES = D / 8, PER = 32 / LANES;  // lanes of a head, heads side by side
-  constexpr int BATCH = kSteps * PER;             // heads of a batch
-  __shared__ __align__(16) float zs[E2M1 ? PER * D : 1];
+  constexpr int BATCH = kSteps * PER;             // heads of a batch: divides 32
+  __shared__ __align__(16) float zs[E2M1 ? PER * D : 1], ts[E2M1 ? PER * D / 4 : 1];
   __shared__ __align__(16) double zd[E2M1 ? PER * D : 1];
   const int lane = threadIdx.x, sub = lane % LANES, side = lane / LANES;
-  const int all = a.q_batches + 2 * a.kv_batches;
-  const int t = blockIdx.x / a.parts, part = blockIdx.x - t * a.parts;
-  const int first = part, last = a.parts == 1 ? all : part + 1;
+  const int t = a.parts == 1 ? blockIdx.x : blockIdx.x / a.parts, part = blockIdx.x - t * a.parts;
+  // the token's batches [first, last) of this warp: queries, then keys, then values
+  const int k_first = a.q_batches, v_first = k_first + a.kv_batches, all = v_first + a.kv_batches;
+  const int first = a.parts == 1 || (a.parts == 3 && part == 0) ? 0 : a.parts != 3 ? part : part == 1 ? k_first : v_first;
+  const int last = a.parts == 1 ? all : a.parts != 3 ? part + 1 : part == 0 ? k_first : part == 1 ? v_first : all;
   // the two groups of this lane in a query or key head; of a value head they are 8 consecutive values
   const bool turned = sub * 8 < a.rot;
   const int ga = !PAIRS && turned ? sub * 4 : sub * 8, gb = !PAIRS && turned ? sub * 4 + a.rot / 2 : sub * 8 + 4;
   const uint16_t *src = a.qkv + (int64_t)t * a.stride;
-  auto kind_of = [&](int k) { return k < a.q_batches ? 0 : k < a.q_batches + a.kv_batches ? 1 : 2; };
-  auto head_of = [&](int k, int kind) {  // first head, or place in the groups, of batch k
-    return (k - (kind == 0 ? 0 : kind == 1 ? a.q_batches : a.q_batches + a.kv_batches)) * BATCH;
-  };
   griddep_wait();  // a programmatic dependent of the kernel before it: set up while that one ends
 
   // the request: how many end at or before t, 32 at a time
@@ -97,13 +94,41 @@ __global__ void __launch_bounds__(32, E2M1 ? 20 : 24) append_rope_kernel(const A
   }
   if (b >= a.batch) return;  // behind the last request
   const int i = t - __ldg(a.cu_q + b);
-  const int64_t grown = a.added ? __ldg(a.added + b) : 0;
+  const int grown = a.added ? __ldg(a.added + b) : 0;
   const int64_t row = a.K ? (int64_t)__ldg(a.start + b) + i : 0;
-  bool bad = grown < 0 || grown + i >= a.reserve || (a.K && (row < 0 || row >= a.Nmax));
+
+  // 32 places of the groups from p0 on, lane j's p0 + j: the head there (-1: none), and the number of the token's row in its
+  // pages, counting rows of d values (bf16: K's; V's is P behind) or tokens of a head (4 bits); -1: none.
+  int p0 = 0, head = -1, rows = -1;
+  auto places = [&](int from, bool quiet) {
+    p0 = from, head = rows = -1;
+    const int p = p0 + lane;
+    if (p >= a.H) return;
+    const int h = __ldg(a.head_order + p);
+    if (h < 0 || h >= a.H) {
+      report(a.status, TG_STATUS_BAD_INPUT);
+      return;
+    }
+    head = h;
+    const int64_t far = (int64_t)__ldg(a.ntok + (int64_t)b * a.H + h) + grown + i;
+    const unsigned group = (unsigned)p / (unsigned)a.H_p, hp = p - group * a.H_p;
+    const int64_t *off = a.pt_off + (int64_t)b * a.G + group;
+    const int64_t at0 = __ldg(off), at1 = __ldg(off + 1);
+    const unsigned slot = (unsigned)far, pg = slot / (unsigned)a.P, r = slot - pg * a.P;
+    const int32_t page = far >= 0 && far <= INT32_MAX && at0 + pg < at1 ? __ldg(a.pt_ids + at0 + pg) : -1;
+    if (page < 0 || page >= a.pool_pages) {
+      if (!quiet) report(a.status, TG_STATUS_BAD_PAGE);
+      return;
+    }
+    rows = (page * a.H_p + (int)hp) * (E2M1 ? a.P : 2 * a.P) + (int)r;
+  };
+  bool bad = grown < 0 || (int64_t)grown + i >= a.reserve || (a.K && (row < 0 || row >= a.Nmax));
+  // (a token that is refused below reports nothing of its pages)
+  if (last > k_first) places(first <= k_first ? 0 : ((first - (first >= v_first ? v_first : k_first)) * BATCH) & ~31, bad);
   // this lane's four pairs
   float c[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
   if (a.rot > 0) {
-    const int64_t half = a.rot / 2;
+    const int half = a.rot / 2;
     if (a.axes == 1) {
       const int64_t pos = a.positions ? (int64_t)__ldg(a.positions + t) : (int64_t)__ldg(a.origin + b) + grown + i;
       bad = bad || pos < 0 || pos >= a.max_pos;
@@ -114,15 +139,15 @@ __global__ void __launch_bounds__(32, E2M1 ? 20 : 24) append_rope_kernel(const A
       }
     } else if (turned) {
       const uint32_t ax = a.axis[sub / 4] >> (8 * (sub & 3));
+      int pos[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) pos[j] = __ldg(a.positions + (int64_t)t * a.axes + (ax >> (2 * j) & 3));
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int64_t pos = __ldg(a.positions + (int64_t)t * a.axes + (ax >> (2 * j) & 3));
-        const bool out = pos < 0 || pos >= a.max_pos;
+        const bool out = pos[j] < 0 || pos[j] >= a.max_pos;
         bad = bad || out;
-        if (!out) {
-          const float2 u = __ldg(reinterpret_cast<const float2 *>(a.table + (pos * half + sub * 4 + j) * 2));
-          c[j] = u.x, sn[j] = u.y;
-        }
+        const float2 u = __ldg(reinterpret_cast<const float2 *>(a.table + ((int64_t)(out ? 0 : pos[j]) * half + sub * 4 + j) * 2));
+        c[j] = u.x, sn[j] = u.y;
       }
     }
   }
@@ -130,79 +155,17 @@ __global__ void __launch_bounds__(32, E2M1 ? 20 : 24) append_rope_kernel(const A
     if (lane == 0) report(a.status, TG_STATUS_BAD_INPUT);
     return;
   }
+  // a lane's values of unit s of batch k (PER heads side by side): of a query or key head, or of a value head
+  auto load_turned = [&](Head8 &x, const uint16_t *from, int h) {
+    x.a = __ldcs(reinterpret_cast<const uint2 *>(from + h * D + ga));
+    x.b = __ldcs(reinterpret_cast<const uint2 *>(from + h * D + gb));
+  };
+  auto dense = [&](uint16_t *base, int h) { return base + (((int64_t)b * a.H + h) * a.Nmax + row) * D; };
 
-  // Lane j < BATCH looks up place p0 + j of the groups: its head, and the token's row in its pages: of bf16 pages a row
-  // number (K; V is P behind it), of 4-bit pages the byte of its tile times 16 plus its row there; -1: none.
-  auto look_up = [&](int p0, int &head, int64_t &at) {
-    head = -1, at = -1;
-    const int p = p0 + lane;
-    if (lane >= BATCH || p >= a.H) return;
-    head = __ldg(a.head_order + p);
-    if (head < 0 || head >= a.H) {
-      head = -1;
-      report(a.status, TG_STATUS_BAD_INPUT);
-      return;
-    }
-    const int64_t slot = __ldg(a.ntok + (int64_t)b * a.H + head) + grown + i;
-    const int64_t *off = a.pt_off + (int64_t)b * (a.H / a.H_p) + p / a.H_p;
-    const int64_t at0 = __ldg(off), at1 = __ldg(off + 1), pg = slot / a.P;
-    const int r = (int)(slot - pg * a.P), hp = p % a.H_p;
-    const int32_t page = slot >= 0 && at0 + pg < at1 ? __ldg(a.pt_ids + at0 + pg) : -1;
-    if (page < 0 || page >= a.pool_pages) {
-      report(a.status, TG_STATUS_BAD_PAGE);
-      return;
-    }
-    const int64_t in = (int64_t)page * a.H_p + hp;
-    at = E2M1 ? (in * (a.P / 16) + r / 16) * (D / 128 * kTile4) * 16 + r % 16 : in * 2 * a.P + r;
-  };
-  auto load = [&](Head8 *x, int kind, int h0, int head) {
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      const int h = kind == 0 ? h0 + s * PER + side : __shfl_sync(0xffffffffu, head, s * PER + side);
-      if (h < 0 || (kind == 0 && h >= a.H_q)) continue;
-      const uint16_t *p = src + ((kind == 0 ? 0 : kind == 1 ? a.H_q : a.H_q + a.H) + h) * D;
-      x[s].a = __ldcs(reinterpret_cast<const uint2 *>(p + (kind == 2 ? sub * 8 : ga)));
-      x[s].b = __ldcs(reinterpret_cast<const uint2 *>(p + (kind == 2 ? sub * 8 + 4 : gb)));
-    }
-  };
-  auto store4 = [&](const Code8 &o, int64_t at, int kind) {
-    uint8_t *tile = a.pool + (at >> 4) + sub / 16 * kTile4;
-    const int r = (int)(at & 15), e = sub % 16;
-    *reinterpret_cast<uint32_t *>(tile + (kind == 1 ? k_codes4(r, e) : v_codes4(r, e))) = o.codes;
-    if (!(e & 1)) tile[kind == 1 ? k_scale4(r, e / 2) : v_scale4(r, e / 2)] = (uint8_t)o.scale;
-  };
-  auto dense = [&](int kind, int h) { return (kind == 1 ? a.K : a.V) + (((int64_t)b * a.H + h) * a.Nmax + row) * D; };
-
-  for (int k = first; k < last; ++k) {
-    const int kind = kind_of(k), h0 = head_of(k, kind);
-    int head = -1;
-    int64_t at = -1;
-    if (kind != 0) look_up(h0, head, at);
-    Head8 in[kSteps] = {};
-    load(in, kind, h0, head);
-    if (kind == 2) {
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const int h = __shfl_sync(0xffffffffu, head, s * PER + side);
-        const int64_t to = __shfl_sync(0xffffffffu, at, s * PER + side);
-        const uint4 raw = make_uint4(in[s].a.x, in[s].a.y, in[s].b.x, in[s].b.y);
-        if (!E2M1) {
-          if (to >= 0) *reinterpret_cast<uint4 *>(a.pool + ((to + a.P) * D + sub * 8) * 2) = raw;
-          if (a.V && h >= 0 && to >= 0) *reinterpret_cast<uint4 *>(dense(2, h) + sub * 8) = raw;
-          continue;
-        }
-        float x[8];
-        unpack8(in[s], x);
-        bool odd = false;
-        const Code8 o = encode_exact(x, a.v_unit, odd);
-        if (odd) report(a.status, TG_STATUS_NONFINITE);
-        if (h < 0 || to < 0) continue;
-        store4(o, to, 2);
-        if (a.V) *reinterpret_cast<uint4 *>(dense(2, h) + sub * 8) = held8(o, a.v_unit);
-      }
-      continue;
-    }
-    const float *w = kind == 0 ? a.qw : a.kw;
+  // The rotation with the weights multiplied in: z_u = uc x_u + vs x_v, z_v = vc x_v + us x_u; u, v: a lane's first and
+  // second values of its pairs
+  float2 uc[2], us[2], vc[2], vs[2];
+  auto weigh = [&](const float *w) {
     float wu[4] = {1.f, 1.f, 1.f, 1.f}, wv[4] = {1.f, 1.f, 1.f, 1.f};
     if (w) {
       const float4 p = __ldg(reinterpret_cast<const float4 *>(w + ga)), q = __ldg(reinterpret_cast<const float4 *>(w + gb));
@@ -211,128 +174,275 @@ __global__ void __launch_bounds__(32, E2M1 ? 20 : 24) append_rope_kernel(const A
       for (int j = 0; j < 4; ++j) wu[j] = e[PAIRS ? 2 * j : j], wv[j] = e[PAIRS ? 2 * j + 1 : j + 4];
     }
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      const int h = kind == 0 ? (h0 + s * PER + side < a.H_q ? h0 + s * PER + side : -1)
-                              : __shfl_sync(0xffffffffu, head, s * PER + side);
-      const int64_t to = kind == 0 ? 0 : __shfl_sync(0xffffffffu, at, s * PER + side);
-      if (h0 + s * PER >= (kind == 0 ? a.H_q : a.H)) break;
-      float x[8], xu[4], xv[4], zu[4], zv[4];
-      unpack8(in[s], x);
+    for (int j = 0; j < 2; ++j) {
+      const float2 cc = {c[2 * j], c[2 * j + 1]}, ss = {sn[2 * j], sn[2 * j + 1]};
+      const float2 u = {wu[2 * j], wu[2 * j + 1]}, v = {wv[2 * j], wv[2 * j + 1]};
+      uc[j] = mul2(u, cc), us[j] = mul2(u, ss), vc[j] = mul2(v, cc), vs[j] = mul2(v, make_float2(-ss.x, -ss.y));
+    }
+  };
+  auto split = [&](const Head8 &in, float2(&xu)[2], float2(&xv)[2]) {
+    const float2 x[4] = {unpack2(in.a.x), unpack2(in.a.y), unpack2(in.b.x), unpack2(in.b.y)};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        xu[j] = x[PAIRS ? 2 * j : j], xv[j] = x[PAIRS ? 2 * j + 1 : j + 4];
-        zu[j] = wu[j] * c[j] * xu[j], zv[j] = wv[j] * c[j] * xv[j];
+    for (int j = 0; j < 2; ++j) {
+      xu[j] = PAIRS ? make_float2(x[2 * j].x, x[2 * j + 1].x) : x[j];
+      xv[j] = PAIRS ? make_float2(x[2 * j].y, x[2 * j + 1].y) : x[j + 2];
+    }
+  };
+  auto root = [&](const float2(&xu)[2], const float2(&xv)[2]) {
+    float2 sq = mul2(xu[0], xu[0]);
+    sq = fma2(xu[1], xu[1], sq), sq = fma2(xv[0], xv[0], sq), sq = fma2(xv[1], xv[1], sq);
+    float ss = sq.x + sq.y;
+#pragma unroll
+    for (int d = LANES / 2; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+    return rsqrtf(fmaf(ss, 1.f / D, a.eps));
+  };
+
+  // ---- queries, and keys of bf16 pages
+  {
+    auto load = [&](Head8(&x)[kSteps], int k) {
+      const bool query = k < k_first;
+      const int h0 = (query ? k : k - k_first) * BATCH + side;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int h = query ? (h0 + s * PER < a.H_q ? h0 + s * PER : -1) : __shfl_sync(0xffffffffu, head, (h0 + s * PER) & 31);
+        if (h >= 0) load_turned(x[s], src + (query ? 0 : a.H_q * D), h);
+      }
+    };
+    auto work = [&](const Head8(&x)[kSteps], int k) {
+      const bool query = k < k_first;
+      const int h0 = (query ? k : k - k_first) * BATCH, n = query ? a.H_q : a.H;
+      const float *w = query ? a.qw : a.kw;
+      weigh(w);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        if (h0 + s * PER >= n) break;
+        const int at = h0 + s * PER + side;
+        float2 xu[2], xv[2], zu[2], zv[2];
+        split(x[s], xu, xv);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) zu[j] = mul2(uc[j], xu[j]), zv[j] = mul2(vc[j], xv[j]);
         if (turned) {  // behind rot a value meets no other: 0 times an infinite one would be NaN
-          zu[j] = fmaf(-sn[j] * wv[j], xv[j], zu[j]);
-          zv[j] = fmaf(sn[j] * wu[j], xu[j], zv[j]);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) zu[j] = fma2(vs[j], xv[j], zu[j]), zv[j] = fma2(us[j], xu[j], zv[j]);
         }
+        if (w) {
+          const float f = root(xu, xv);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) zu[j] = mul2(zu[j], make_float2(f, f)), zv[j] = mul2(zv[j], make_float2(f, f));
+        }
+        uint2 oa, ob;
+        if (PAIRS) {
+          oa = make_uint2(pack_bf16x2(zu[0].x, zv[0].x), pack_bf16x2(zu[0].y, zv[0].y));
+          ob = make_uint2(pack_bf16x2(zu[1].x, zv[1].x), pack_bf16x2(zu[1].y, zv[1].y));
+        } else {
+          oa = make_uint2(pack_bf16x2(zu[0].x, zu[0].y), pack_bf16x2(zu[1].x, zu[1].y));
+          ob = make_uint2(pack_bf16x2(zv[0].x, zv[0].y), pack_bf16x2(zv[1].x, zv[1].y));
+        }
+        if (query) {
+          if (at >= n) continue;
+          uint16_t *dst = a.q + ((int64_t)t * a.H_q + h0 + side) * D + s * PER * D;
+          *reinterpret_cast<uint2 *>(dst + ga) = oa;
+          *reinterpret_cast<uint2 *>(dst + gb) = ob;
+        } else {
+          const int to = __shfl_sync(0xffffffffu, rows, at & 31);
+          const int h = __shfl_sync(0xffffffffu, head, at & 31);
+          if (to < 0) continue;
+          uint16_t *dst = reinterpret_cast<uint16_t *>(a.pool) + (int64_t)to * D;
+          *reinterpret_cast<uint2 *>(dst + ga) = oa;
+          *reinterpret_cast<uint2 *>(dst + gb) = ob;
+          if (a.K) {
+            dst = dense(a.K, h);
+            *reinterpret_cast<uint2 *>(dst + ga) = oa;
+            *reinterpret_cast<uint2 *>(dst + gb) = ob;
+          }
+        }
+      }
+    };
+    const int end = min(last, E2M1 ? k_first : v_first);
+    Head8 x[kSteps] = {};
+    for (int k = first; k < end; ++k) {
+      if (k >= k_first && ((k - k_first) * BATCH & ~31) != p0) places((k - k_first) * BATCH & ~31, false);
+      load(x, k);
+      work(x, k);
+    }
+  }
+  // ---- keys of 4-bit pages: one unit in a turn of the loop (what unrolling it adds to the code costs more than it hides)
+  if (E2M1) {
+    const int end = min(last, v_first) - k_first;
+    auto load = [&](Head8 &x, int u) {
+      const int h = __shfl_sync(0xffffffffu, head, (u * PER + side) & 31);
+      if (h >= 0) load_turned(x, src + a.H_q * D, h);
+    };
+    if (first < v_first && last > k_first) weigh(a.kw);
+    const int u_end = min(end * kSteps, (a.H + PER - 1) / PER);
+    Head8 nx = {};
+    for (int u = max(first - k_first, 0) * kSteps; u < u_end; ++u) {
+      if ((u * PER & ~31) != p0) places(u * PER & ~31, false);
+      load(nx, u);
+      const int to = __shfl_sync(0xffffffffu, rows, (u * PER + side) & 31);
+      const int h = __shfl_sync(0xffffffffu, head, (u * PER + side) & 31);
+      const bool w = a.kw != nullptr;
+      float2 xu[2], xv[2], zu[2], zv[2];
+      split(nx, xu, xv);
+      float ta, tb;  // the largest |first product| + |second one| of the first and of the second group
+#pragma unroll
+      for (int j = 0; j < 2; ++j) zu[j] = mul2(uc[j], xu[j]), zv[j] = mul2(vc[j], xv[j]);
+      if (turned) {  // behind rot a value meets no other: 0 times an infinite one would be NaN
+        float2 tu[2], tv[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float2 su = mul2(vs[j], xv[j]), sv = mul2(us[j], xu[j]);
+          tu[j] = make_float2(fabsf(zu[j].x) + fabsf(su.x), fabsf(zu[j].y) + fabsf(su.y));
+          tv[j] = make_float2(fabsf(zv[j].x) + fabsf(sv.x), fabsf(zv[j].y) + fabsf(sv.y));
+          zu[j] = fma2(vs[j], xv[j], zu[j]), zv[j] = fma2(us[j], xu[j], zv[j]);
+        }
+        ta = fmaxf(fmaxf(tu[0].x, tu[0].y), fmaxf(tu[1].x, tu[1].y));
+        tb = fmaxf(fmaxf(tv[0].x, tv[0].y), fmaxf(tv[1].x, tv[1].y));
+        if (PAIRS) ta = tb = fmaxf(ta, tb);
+      } else {
+        ta = tb = fmaxf(fmaxf(fmaxf(fabsf(zu[0].x), fabsf(zu[0].y)), fmaxf(fabsf(zu[1].x), fabsf(zu[1].y))),
+                        fmaxf(fmaxf(fabsf(zv[0].x), fabsf(zv[0].y)), fmaxf(fabsf(zv[1].x), fabsf(zv[1].y))));
       }
       if (w) {
-        float ss = 0.f;
+        const float f = root(xu, xv);
+        const float2 ff = {f, f};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-#pragma unroll
-        for (int d = LANES / 2; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-        const float f = rsqrtf(fmaf(ss, 1.f / D, a.eps));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) zu[j] *= f, zv[j] *= f;
+        for (int j = 0; j < 2; ++j) zu[j] = mul2(zu[j], ff), zv[j] = mul2(zv[j], ff);
+        ta *= f, tb *= f;
       }
-      if (kind == 0 || !E2M1) {
-        if (h < 0 || to < 0) continue;
-        Head8 o;
-        if (PAIRS) {
-          o.a = make_uint2(pack_bf16x2(zu[0], zv[0]), pack_bf16x2(zu[1], zv[1]));
-          o.b = make_uint2(pack_bf16x2(zu[2], zv[2]), pack_bf16x2(zu[3], zv[3]));
-        } else {
-          o.a = make_uint2(pack_bf16x2(zu[0], zu[1]), pack_bf16x2(zu[2], zu[3]));
-          o.b = make_uint2(pack_bf16x2(zv[0], zv[1]), pack_bf16x2(zv[2], zv[3]));
-        }
-        uint16_t *dst = kind == 0 ? a.q + ((int64_t)t * a.H_q + h) * D : reinterpret_cast<uint16_t *>(a.pool) + to * D;
-        *reinterpret_cast<uint2 *>(dst + ga) = o.a;
-        *reinterpret_cast<uint2 *>(dst + gb) = o.b;
-        if (kind == 1 && a.K) {
-          dst = dense(1, h);
-          *reinterpret_cast<uint2 *>(dst + ga) = o.a;
-          *reinterpret_cast<uint2 *>(dst + gb) = o.b;
-        }
-        continue;
+      // the values in order, 8 consecutive ones to a lane
+      __syncwarp();
+      {
+        float4 *p = reinterpret_cast<float4 *>(zs + side * D + ga), *q = reinterpret_cast<float4 *>(zs + side * D + gb);
+        *p = PAIRS ? make_float4(zu[0].x, zv[0].x, zu[0].y, zv[0].y) : make_float4(zu[0].x, zu[0].y, zu[1].x, zu[1].y);
+        *q = PAIRS ? make_float4(zu[1].x, zv[1].x, zu[1].y, zv[1].y) : make_float4(zv[0].x, zv[0].y, zv[1].x, zv[1].y);
+        ts[(side * D + ga) / 4] = ta, ts[(side * D + gb) / 4] = tb;
       }
-      // ---- 4-bit K
+      __syncwarp();
       float z[8];
-      __syncwarp();
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        zs[side * D + ga + (PAIRS ? 2 * j : j)] = zu[j];
-        zs[side * D + (PAIRS ? ga + 2 * j + 1 : gb + j)] = zv[j];
+      float most;  // how far a value of the block may be off
+      // (values that only passed through, behind rot without a norm, are exact: their ties are no doubt)
+      const bool passed = !w && sub * 8 >= a.rot;
+      {
+        const float4 *p = reinterpret_cast<const float4 *>(zs + side * D + sub * 8);
+        const float4 p1 = p[0], p2 = p[1], q = *reinterpret_cast<const float4 *>(ts + side * D / 4 + (sub & ~1) * 2);
+        z[0] = p1.x, z[1] = p1.y, z[2] = p1.z, z[3] = p1.w, z[4] = p2.x, z[5] = p2.y, z[6] = p2.z, z[7] = p2.w;
+        most = passed ? 0.f : fmaxf(fmaxf(q.x, q.y), fmaxf(q.z, q.w)) * (20.f * 0x1p-24f);
       }
-      __syncwarp();
+      float top = max_abs_nan(max_abs_nan(max_abs_nan(z[0], z[1]), max_abs_nan(z[2], z[3])),
+                              max_abs_nan(max_abs_nan(z[4], z[5]), max_abs_nan(z[6], z[7])));
+      bool odd = false;
+      if (!(top < __uint_as_float(0x7f800000u))) {  // infinite, or a NaN, which counts for nothing in the scale
+        odd = true;
+        top = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) z[j] = zs[side * D + sub * 8 + j];
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(z[j]));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       Code8 o;
-      if (!w && a.rot == 0) {  // the projections themselves
-        bool odd = false;
-        o = encode_exact(z, a.k_unit, odd);
-        if (odd) report(a.status, TG_STATUS_NONFINITE);
-      } else {
-        const float to_unit = 1.f / a.k_unit;  // exact
-        float top = 0.f;
-        bool odd = false;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(z[j])), odd = odd || not_finite(z[j]);
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        float most = top;
-#pragma unroll
-        for (int d = 2; d < LANES; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-        // (values that only passed through, behind rot without a norm, are exact: their ties are no doubt)
-        const bool passed = !w && sub * 8 >= a.rot;
-        const float off = passed ? 0.f : most * 0x1p-18f;
-        o.scale = max(e4m3_of(__fdiv_rn(fmaxf(top - off, 0.f) * to_unit, 6.f)), 1u);
-        bool near = o.scale != max(e4m3_of(__fdiv_rn((top + off) * to_unit, 6.f)), 1u);
-        const float inv = 1.f / e4m3_to_float(o.scale) * to_unit, move = off * inv;
-        o.codes = 0;
-        uint32_t up = 0;
+      o.scale = scale_of(fmaxf(top - most, 0.f) * a.k_to_unit);
+      const uint32_t scale_up = scale_of((top + most) * a.k_to_unit);
+      uint32_t up;
+      auto codes = [&]() {  // of the scale, with the values moved down and up
+        const float inv = rcp(e4m3_to_float(o.scale)) * a.k_to_unit;
+        const float2 move = {most * inv, most * inv};
+        float lo[8], hi[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float r0 = passed ? over_scale_exact(z[2 * j], inv) : z[2 * j] * inv;
-          const float r1 = passed ? over_scale_exact(z[2 * j + 1], inv) : z[2 * j + 1] * inv;
-          o.codes |= e2m1x2_of(r0 - move, r1 - move) << (8 * j);
-          up |= e2m1x2_of(r0 + move, r1 + move) << (8 * j);
+          const float2 zj = {z[2 * j], z[2 * j + 1]};
+          float2 r = mul2(zj, make_float2(inv, inv));
+          if (!w && passed) r = over_scale_exact(zj, inv);
+          const float2 u = add2(r, move), d = add2(r, make_float2(-move.x, -move.y));
+          lo[2 * j] = d.x, lo[2 * j + 1] = d.y, hi[2 * j] = u.x, hi[2 * j + 1] = u.y;
         }
-        near = near || o.codes != up;
-        if (odd) report(a.status, TG_STATUS_NONFINITE);
-        if (__any_sync(0xffffffffu, near)) {
-          // the row again in float64
-          double f = 1.0;
-          if (w) {
-            double ss = 0.0;
+        o.codes = e2m1x8_of(lo), up = e2m1x8_of(hi);
+      };
+      codes();
+      if (__any_sync(0xffffffffu, o.scale != scale_up || o.codes != up)) {
+        // the row again in float64; the root's reciprocal by a Newton step from float32's (2^-43 off at most)
+        double f = 1.0;
+        if (w) {
+          double ss = 0.0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) ss += (double)x[j] * (double)x[j];
-#pragma unroll
-            for (int d = LANES / 2; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-            f = 1.0 / sqrt(ss / D + (double)a.eps);
+          for (int j = 0; j < 2; ++j) {
+            ss = fma((double)xu[j].x, (double)xu[j].x, ss), ss = fma((double)xu[j].y, (double)xu[j].y, ss);
+            ss = fma((double)xv[j].x, (double)xv[j].x, ss), ss = fma((double)xv[j].y, (double)xv[j].y, ss);
           }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const double yu = (double)xu[j] * f * wu[j], yv = (double)xv[j] * f * wv[j];
-            const double u = turned ? yu * c[j] - yv * sn[j] : yu, v = turned ? yv * c[j] + yu * sn[j] : yv;
-            zd[side * D + ga + (PAIRS ? 2 * j : j)] = u;
-            zd[side * D + (PAIRS ? ga + 2 * j + 1 : gb + j)] = v;
-          }
-          __syncwarp();
-          double zz[8], dt = 0.0;
+          for (int e = LANES / 2; e; e >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, e);
+          const double mean = fma(ss, 1.0 / D, (double)a.eps);
+          f = (double)rsqrtf((float)mean);
+          f = f * fma(-0.5 * mean, f * f, 1.5);
+        }
+        double *zp = zd + side * D;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) zz[j] = zd[side * D + sub * 8 + j], dt = fmax(dt, fabs(zz[j]));
-          dt = fmax(dt, __shfl_xor_sync(0xffffffffu, dt, 1));
+        for (int j = 0; j < 4; ++j) {
+          const int iu = PAIRS ? ga + 2 * j : ga + j, iv = PAIRS ? ga + 2 * j + 1 : gb + j;
+          const double yu = (double)(j & 1 ? xu[j / 2].y : xu[j / 2].x) * f * (w ? a.kw[iu] : 1.f);
+          const double yv = (double)(j & 1 ? xv[j / 2].y : xv[j / 2].x) * f * (w ? a.kw[iv] : 1.f);
+          zp[iu] = turned ? yu * c[j] - yv * sn[j] : yu;
+          zp[iv] = turned ? yv * c[j] + yu * sn[j] : yv;
+        }
+        __syncwarp();
+        if (o.scale != scale_up) {  // the scale first (its block's two lanes agree), then the codes over it
+          const double *block = zp + (sub & ~1) * 8;
+          double dt = 0.0;
+          for (int j = 0; j < 16; ++j) dt = fmax(dt, fabs(block[j]));
           o.scale = max(e4m3_of(sticky(dt / (6.0 * a.k_unit))), 1u);
-          const double sc = (double)e4m3_to_float(o.scale) * a.k_unit;
-          o.codes = 0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) o.codes |= e2m1x2_of(sticky(zz[2 * j] / sc), sticky(zz[2 * j + 1] / sc)) << (8 * j);
+          codes();
+        }
+        uint32_t differ = o.codes ^ up;
+        const double unit_s = (double)e4m3_to_float(o.scale) * a.k_unit;
+        while (differ) {
+          const int j = (__ffs(differ) - 1) >> 2;
+          o.codes = (o.codes & ~(15u << (4 * j))) | e2m1_of(sticky(zp[sub * 8 + j] / unit_s)) << (4 * j);
+          differ &= ~(15u << (4 * j));
         }
       }
-      if (h < 0 || to < 0) continue;
-      store4(o, to, 1);
-      if (a.K) *reinterpret_cast<uint4 *>(dense(1, h) + sub * 8) = held8(o, a.k_unit);
+      if (to < 0) continue;
+      if (odd) report(a.status, TG_STATUS_NONFINITE);
+      uint8_t *tile = a.pool + ((int64_t)(to >> 4) * (D / 128) + sub / 16) * kTile4;
+      const int r = to & 15, e = sub % 16;
+      *reinterpret_cast<uint32_t *>(tile + k_codes4(r, e)) = o.codes;
+      if (!(e & 1)) tile[k_scale4(r, e / 2)] = (uint8_t)o.scale;
+      if (a.K) *reinterpret_cast<uint4 *>(dense(a.K, h) + sub * 8) = held8(o, a.k_unit);
+    }
+  }
+  // ---- values
+  const uint16_t *from = src + (a.H_q + a.H) * D + sub * 8;
+  for (int k = max(first, v_first); k < last; ++k) {
+    const int h0 = (k - v_first) * BATCH;
+    if ((h0 & ~31) != p0) places(h0 & ~31, false);
+    uint4 x[kSteps] = {};
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int h = __shfl_sync(0xffffffffu, head, (h0 + s * PER + side) & 31);
+      if (h >= 0) x[s] = __ldcs(reinterpret_cast<const uint4 *>(from + h * D));
+    }
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int to = __shfl_sync(0xffffffffu, rows, (h0 + s * PER + side) & 31);
+      const int h = __shfl_sync(0xffffffffu, head, (h0 + s * PER + side) & 31);
+      uint4 held = x[s];
+      if (!E2M1) {
+        if (to < 0) continue;
+        *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(a.pool) + (int64_t)(to + a.P) * D + sub * 8) = held;
+      } else {
+        const uint32_t v[4] = {held.x, held.y, held.z, held.w};
+        float2 f[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = unpack2(v[j]);
+        bool odd = false;
+        const Code8 o = encode_exact(f, a.v_to_unit, odd);
+        if (to < 0) continue;
+        if (odd) report(a.status, TG_STATUS_NONFINITE);
+        uint8_t *tile = a.pool + ((int64_t)(to >> 4) * (D / 128) + sub / 16) * kTile4;
+        const int r = to & 15, e = sub % 16;
+        *reinterpret_cast<uint32_t *>(tile + v_codes4(r, e)) = o.codes;
+        if (!(e & 1)) tile[v_scale4(r, e / 2)] = (uint8_t)o.scale;
+        if (a.V) held = held8(o, a.v_unit);
+      }
+      if (a.V) *reinterpret_cast<uint4 *>(dense(a.V, h) + sub * 8) = held;
     }
   }
 }
@@ -380,8 +490,8 @@ extern "C" int tg_append_rope(tg_stream_t stream, int batch, int T, int H_q, int
                 (long long)(heads * d));
   if (!std::isfinite(eps)) return fail(TG_ERR_NONFINITE, "%s: eps is not finite", fn);
   if (eps < 0.f) return fail(TG_ERR_INVALID_ARG, "%s: eps=%g < 0", fn, (double)eps);
-  if (pool_pages <= 0 || pool_pages > INT32_MAX)
-    return fail(TG_ERR_CAPACITY, "%s: pool_pages=%lld (1..2^31-1)", fn, (long long)pool_pages);
+  if (pool_pages <= 0 || pool_pages > INT32_MAX / H_p / (e2m1 ? P : 2 * (int64_t)P))
+    return fail(TG_ERR_CAPACITY, "%s: pool_pages=%lld gives more than 2^31-1 rows, or none", fn, (long long)pool_pages);
   if (!K != !V) return fail(TG_ERR_INVALID_ARG, "%s: K and V go together", fn);
   if (K && (Nmax <= 0 || !start)) return fail(TG_ERR_INVALID_ARG, "%s: dense rows without Nmax and start", fn);
   AppendArgs a = {};
@@ -403,8 +513,9 @@ extern "C" int tg_append_rope(tg_stream_t stream, int batch, int T, int H_q, int
   a.cu_q = cu_q, a.positions = positions, a.origin = origin, a.head_order = head_order, a.ntok = ntok, a.added = added;
   a.pt_ids = pt_ids, a.start = start, a.pt_off = pt_off, a.qkv = qkv, a.stride = qkv_stride, a.pool_pages = pool_pages;
   a.qw = q_weight, a.kw = k_weight, a.table = cos_sin, a.pool = static_cast<uint8_t *>(pool), a.q = q, a.K = K, a.V = V;
-  a.status = dev_status, a.batch = batch, a.H_q = H_q, a.H = H, a.H_p = H_p, a.P = P, a.Nmax = Nmax, a.rot = rot;
+  a.status = dev_status, a.batch = batch, a.H_q = H_q, a.H = H, a.H_p = H_p, a.G = H / H_p, a.P = P, a.Nmax = Nmax, a.rot = rot;
   a.max_pos = max_pos, a.axes = axes, a.reserve = reserve, a.eps = eps, a.k_unit = k_unit, a.v_unit = v_unit;
+  if (e2m1) a.k_to_unit = 1.f / k_unit, a.v_to_unit = 1.f / v_unit;  // exact
   // a warp a token, or, below 2048 tokens, one for each of its batches, as in tg_qk_norm_rope
   const int per = kSteps * (d == 128 ? 2 : 1);
   a.q_batches = (H_q + per - 1) / per;

@@ -8,6 +8,7 @@
 #pragma once
 
 #include "../../include/tg.h"
+#include "packed.cuh"
 #include "ptx.cuh"
 
 #include <cstdint>
@@ -44,11 +45,21 @@ __device__ __forceinline__ float f16_to_float(uint32_t h) {
 }
 __device__ __forceinline__ float e4m3_to_float(uint32_t e) { return f16_to_float(e4m3x2_to_f16x2(e)); }
 
-// two e2m1 codes of x0 (low) and x1 (ties to the even code, at most 6 in magnitude)
-__device__ __forceinline__ uint32_t e2m1x2_of(float x0, float x1) {
-  uint16_t r;
-  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u16.u8 %0, b;\n\t}" : "=h"(r) : "f"(x1), "f"(x0));
+// the e2m1 codes of eight values, the first in the lowest bits (ties to the even code, at most 6 in magnitude, NaN as 6)
+__device__ __forceinline__ uint32_t e2m1x8_of(const float (&x)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(r)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
   return r;
+}
+__device__ __forceinline__ uint32_t e2m1_of(float x) {
+  uint16_t r;
+  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u16.u8 %0, b;\n\t}" : "=h"(r) : "f"(0.f), "f"(x));
+  return r & 15u;
 }
 // eight codes of a word as four f16 pairs, the lower codes first
 __device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&h)[4]) {
@@ -64,32 +75,57 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// Codes of a bf16 value over a scale s: x / s, by the reciprocal of s.  Where x / s is the border of two
-// codes the product may be an ulp off it, and a value that is not on the border is 2^-9 of it or more away
-// (x has 8 significant bits, border times s at most 7): a multiple of 2^-14 tells them apart.
-__device__ __forceinline__ float over_scale_exact(float x, float inv) { return (x * inv + 512.f) - 512.f; }
+// the larger magnitude, NaN if either is one
+__device__ __forceinline__ float max_abs_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+// 1 / x, off by an ulp at most
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// A block's scale from its largest magnitude (over the unit): e4m3 of a sixth of it.  Where a sixth of a bf16 number is
+// halfway between two e4m3 numbers, the product with 1/6 in float32 is that, exactly (all 16 such mantissas are
+// tested); any other is 2^-9 of it or more away, so the product's rounding decides nothing.
+__device__ __forceinline__ uint32_t scale_of(float top) { return max(e4m3_of(top * (1.f / 6.f)), 1u); }
 
-__device__ __forceinline__ bool not_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
+// A bf16 value over a scale s, by the reciprocal of s (inv): where x / s is the border of two codes the product may be
+// some ulps off it, and a value that is not on the border is 2^-9 of it or more away (x has 8 significant bits,
+// border times s at most 7): a multiple of 2^-14 tells them apart.
+__device__ __forceinline__ float2 over_scale_exact(float2 x, float inv) {
+  const float2 r = add2(mul2(x, make_float2(inv, inv)), make_float2(512.f, 512.f));
+  return add2(r, make_float2(-512.f, -512.f));
+}
 
-struct Code8 {      // eight consecutive values in 4 bits
-  uint32_t codes;   // a nibble each
-  uint32_t scale;   // of their block of 16, e4m3
+struct Code8 {     // eight consecutive values in 4 bits
+  uint32_t codes;  // a nibble each
+  uint32_t scale;  // of their block of 16, e4m3
 };
-// eight consecutive bf16 values, their block's other eight in the neighbouring lane (lane ^ 1); odd is set where
-// one of these eight is not finite
-__device__ __forceinline__ Code8 encode_exact(const float (&x)[8], float unit, bool &odd) {
-  const float to = 1.f / unit;  // exact
-  float top = 0.f;
+// eight consecutive bf16 values, their block's other eight in the neighbouring lane (lane ^ 1); to_unit: 1 / unit; odd is
+// set where one of these eight is not finite
+__device__ __forceinline__ Code8 encode_exact(const float2 (&x)[4], float to_unit, bool &odd) {
+  float top = max_abs_nan(max_abs_nan(max_abs_nan(x[0].x, x[0].y), max_abs_nan(x[1].x, x[1].y)),
+                          max_abs_nan(max_abs_nan(x[2].x, x[2].y), max_abs_nan(x[3].x, x[3].y)));
+  if (!(top < __uint_as_float(0x7f800000u))) {  // infinite, or a NaN, which counts for nothing in the scale
+    odd = true;
+    top = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e])), odd = odd || not_finite(x[e]);
+    for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
+  }
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
   Code8 o;
-  o.scale = max(e4m3_of(__fdiv_rn(top * to, 6.f)), 1u);
-  const float inv = 1.f / e4m3_to_float(o.scale) * to;
-  o.codes = 0;
+  o.scale = scale_of(top * to_unit);
+  const float inv = rcp(e4m3_to_float(o.scale)) * to_unit;
+  float r[8];
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    o.codes |= e2m1x2_of(over_scale_exact(x[2 * e], inv), over_scale_exact(x[2 * e + 1], inv)) << (8 * e);
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = over_scale_exact(x[e], inv);
+    r[2 * e] = f.x, r[2 * e + 1] = f.y;
+  }
+  o.codes = e2m1x8_of(r);
   return o;
 }
 // what they stand for, as bf16 (exact: at most 6 significant bits)

@@ -28,7 +28,7 @@ struct PagesArgs {
   int64_t src_pages, dst_pages;
   int32_t *status;
   int batch, H, H_p, P, plus, reserve;
-  float k_unit, v_unit;
+  float k_unit, v_unit;  // into 4 bits: their reciprocals
 };
 
 // tokens of the head at place p of request b
@@ -140,10 +140,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) convert_pages_kernel(c
           for (int s = 0; s < GO; ++s) {
             const int r = (s0 + s) * PER + side;
             const uint32_t w[4] = {v[s].x, v[s].y, v[s].z, v[s].w};
-            float x[8];
+            float2 x[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            const Code8 o = encode_exact(x, kv ? a.v_unit : a.k_unit, odd);
+            for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+            const Code8 o = encode_exact(x, kv ? a.v_unit : a.k_unit, odd);  // (the units' reciprocals)
             uint8_t *tile = mine + sub / 16 * kTile4;
             const int c = sub % 16;
             *reinterpret_cast<uint32_t *>(tile + (kv ? v_codes4(r, c) : k_codes4(r, c))) = o.codes;
@@ -197,6 +197,8 @@ int convert(const char *fn, bool to4, tg_stream_t stream, int d, const PagesArgs
     return fail(TG_ERR_INVALID_ARG, "%s: NULL pointer argument", fn);
   if ((reinterpret_cast<uintptr_t>(a.src) | reinterpret_cast<uintptr_t>(a.dst)) & 15)
     return fail(TG_ERR_INVALID_ARG, "%s: pools must be 16-byte aligned", fn);
+  PagesArgs b = a;
+  if (to4) b.k_unit = 1.f / a.k_unit, b.v_unit = 1.f / a.v_unit;  // exact
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -211,9 +213,9 @@ int convert(const char *fn, bool to4, tg_stream_t stream, int d, const PagesArgs
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (d == 128)
-    e = to4 ? cudaLaunchKernelEx(&cfg, convert_pages_kernel<128, true>, a) : cudaLaunchKernelEx(&cfg, convert_pages_kernel<128, false>, a);
+    e = to4 ? cudaLaunchKernelEx(&cfg, convert_pages_kernel<128, true>, b) : cudaLaunchKernelEx(&cfg, convert_pages_kernel<128, false>, b);
   else
-    e = to4 ? cudaLaunchKernelEx(&cfg, convert_pages_kernel<256, true>, a) : cudaLaunchKernelEx(&cfg, convert_pages_kernel<256, false>, a);
+    e = to4 ? cudaLaunchKernelEx(&cfg, convert_pages_kernel<256, true>, b) : cudaLaunchKernelEx(&cfg, convert_pages_kernel<256, false>, b);
   if (e != cudaSuccess) return fail(TG_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
   return tgi::ok();
 }
