@@ -67,7 +67,7 @@ __device__ __forceinline__ float sticky(double v) {
 }
 
 template <int D, bool PAIRS, bool E2M1>
-__global__ void __launch_bounds__(32, E2M1 ? 20 : 24) append_rope_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(32, E2M1 ? 20 : 28) append_rope_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int LANES = D / 8, PER = 32 / LANES;  // lanes of a head, heads side by side
   constexpr int BATCH = kSteps * PER;             // heads of a batch: divides 32
   __shared__ __align__(16) float zs[E2M1 ? PER * D : 1], ts[E2M1 ? PER * D / 4 : 1];

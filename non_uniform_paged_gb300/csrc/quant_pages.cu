@@ -4,9 +4,10 @@
 // bound by memory.
 //
 // The work is tiles of 16 tokens of every (request, place in the groups); their number is known on the device
-// alone.  Each block of threads adds up the tiles of all heads, takes an even share of them, and its warps walk over that
-// share.  A tile's 4-bit side passes through shared memory, because its 16-byte pieces (V by blocks of
-// values, scales) are not the pieces of 8 values that a lane has of a bf16 row.
+// alone.  Each block of threads adds up the tiles of all heads; each warp takes an even share of them, one after the
+// other in the lists, and looks up 32 of them at a time, a tile by each lane, so that the chain counts -> list -> page
+// is waited for once in 32 tiles.  A tile's 4-bit side passes through shared memory, because its 16-byte pieces (V by blocks
+// of values, scales) are not the pieces of 8 values that a lane has of a bf16 row.
 #include "page4.cuh"
 #include "ptx.cuh"
 #include "tg_internal.h"
@@ -18,7 +19,9 @@ namespace {
 using namespace tgk;
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
+// Blocks to an SM, of 80 registers (1.26M rows of 128: into 4 bits 136 us, with 4 blocks of 64 registers 150; out of them 140 and 146).
 constexpr int kBlocksPerSm = 3;
+constexpr int kEntries = 1024;  // heads whose first tile shared memory keeps; of more it is counted again
 
 struct PagesArgs {
   const int32_t *head_order, *ntok, *added, *src_ids, *dst_ids;
@@ -60,15 +63,16 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) convert_pages_kernel(c
   constexpr int CHUNKS = TILE / 16;  // 16-byte pieces of a tile
   __shared__ __align__(16) uint8_t tiles[kWarps][TILE];
   __shared__ int64_t sums[kWarps], s_at[2];
+  __shared__ int64_t s_first[kEntries + 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sub = lane % LANES, side = lane / LANES;
   const int entries = a.batch * a.H;
+  const bool kept = entries <= kEntries;
   griddep_wait();
   // tiles of an entry (request, place): of 16 tokens that are there, or of all pages that hold one
   auto tiles_of = [&](int e) -> int64_t {
     const int64_t n = tokens_of(a, e / a.H, e % a.H);
     return TO4 ? (n + 15) / 16 : (n + a.P - 1) / a.P * (a.P / 16);
   };
-  // all tiles, then the entry and the tile in it at which this block's share begins
   auto block_scan = [&](int64_t v, int64_t &before) -> int64_t {  // exclusive prefix of v, and the block's sum
     int64_t incl = v;
 #pragma unroll
@@ -88,91 +92,146 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) convert_pages_kernel(c
     return total;
   };
   int64_t all = 0, before;
-  for (int e = 0; e < entries; e += kThreads) all += block_scan(e + tid < entries ? tiles_of(e + tid) : 0, before);
+  for (int e = 0; e < entries; e += kThreads) {
+    const int64_t total = block_scan(e + tid < entries ? tiles_of(e + tid) : 0, before);
+    if (kept && e + tid < entries) s_first[e + tid] = all + before;
+    all += total;
+  }
+  // this block's tiles [lo, hi), and this warp's [from, to) of them
   const int64_t lo = all / gridDim.x * blockIdx.x + min((int64_t)blockIdx.x, all % gridDim.x);
   const int64_t hi = lo + all / gridDim.x + (blockIdx.x < all % gridDim.x);
   if (lo >= hi) return;
-  int64_t sum = 0;
-  for (int e = 0; e < entries; e += kThreads) {
-    const int64_t n = e + tid < entries ? tiles_of(e + tid) : 0;
-    const int64_t total = block_scan(n, before);
-    if (sum + before <= lo && lo < sum + before + n) s_at[0] = e + tid, s_at[1] = sum + before;
-    sum += total;
+  if (!kept) {
+    int64_t sum = 0;
+    for (int e = 0; e < entries; e += kThreads) {
+      const int64_t n = e + tid < entries ? tiles_of(e + tid) : 0;
+      const int64_t total = block_scan(n, before);
+      if (sum + before <= lo && lo < sum + before + n) s_at[0] = e + tid, s_at[1] = sum + before;
+      sum += total;
+    }
   }
   __syncthreads();
-  int e = (int)s_at[0];
-  int64_t begin = s_at[1], count = tiles_of(e);
+  const int64_t mine_lo = lo + (hi - lo) * warp / kWarps, mine_hi = lo + (hi - lo) * (warp + 1) / kWarps;
   uint8_t *mine = tiles[warp];
+  // the entry of tile n and the entry's first tile
+  auto entry_of = [&](int64_t n, int64_t &begin) -> int {
+    if (kept) {  // the last entry that begins at or before n
+      int l = 0, h = entries;
+      while (h - l > 1) {
+        const int m = (l + h) / 2;
+        if (s_first[m] <= n) l = m;
+        else h = m;
+      }
+      begin = s_first[l];
+      return l;
+    }
+    int e = (int)s_at[0];
+    begin = s_at[1];
+    for (int64_t count = tiles_of(e); n >= begin + count; count = tiles_of(e)) begin += count, ++e;
+    return e;
+  };
 
-  for (int64_t n = lo + warp; n < hi; n += kWarps) {
-    while (n >= begin + count) {
-      begin += count;
-      count = tiles_of(++e);
+  for (int64_t n0 = mine_lo; n0 < mine_hi; n0 += 32) {
+    // lane's tile n0 + lane: its pages (-1: none), its place in them and its tokens
+    int l_from = -1, l_to = -1, l_in = 0, l_left = 0;
+    if (n0 + lane < mine_hi) {
+      int64_t begin;
+      const int e = entry_of(n0 + lane, begin);
+      const int b = e / a.H, p = e - b * a.H, group = p / a.H_p;
+      const int64_t list = (int64_t)b * (a.H / a.H_p) + group, token = (n0 + lane - begin) * 16;
+      l_from = (int)page_of(a, a.src_off, a.src_ids, a.src_pages, list, token);
+      l_to = (int)page_of(a, a.dst_off, a.dst_ids, a.dst_pages, list, token);
+      l_in = (p - group * a.H_p) * (a.P / 16) + (int)(token % a.P / 16);  // tile of the page
+      l_left = (int)min(max(tokens_of(a, b, p) - token, (int64_t)0), (int64_t)16);
+      if (l_from < 0 || l_to < 0) report(a.status, TG_STATUS_BAD_PAGE);
     }
-    const int b = e / a.H, p = e % a.H;
-    const int64_t list = (int64_t)b * (a.H / a.H_p) + p / a.H_p, token = (n - begin) * 16;
-    const int64_t from = page_of(a, a.src_off, a.src_ids, a.src_pages, list, token);
-    const int64_t to = page_of(a, a.dst_off, a.dst_ids, a.dst_pages, list, token);
-    if (from < 0 || to < 0) {
-      if (lane == 0) report(a.status, TG_STATUS_BAD_PAGE);
-      continue;
-    }
-    const int r0 = (int)(token % a.P), hp = p % a.H_p;
-    const int64_t left = tokens_of(a, b, p) - token;  // rows [0, left) are tokens
-    const int64_t bf16_at = (((TO4 ? from : to) * a.H_p + hp) * 2 * a.P + r0) * D;
-    const int64_t e2m1_at = (((TO4 ? to : from) * a.H_p + hp) * (a.P / 16) + r0 / 16) * TILE;
-    __syncwarp();
+    const int here = (int)min((int64_t)32, mine_hi - n0);
+    const int p16 = a.P / 16;
     if (TO4) {
-      const uint16_t *src = reinterpret_cast<const uint16_t *>(a.src) + bf16_at + sub * 8;
-      bool odd = false;
+      // groups of 4 rows to a lane (K's, then V's), the next one, of the next tile too, on its way while one is encoded
+      constexpr int GROUP = 4, GROUPS = 2 * 16 / PER / GROUP;
+      auto fetch = [&](uint4(&v)[GROUP], int j, int g) {
+        const int from = __shfl_sync(0xffffffffu, l_from, j), in = __shfl_sync(0xffffffffu, l_in, j);
+        const int left = from < 0 ? 0 : __shfl_sync(0xffffffffu, l_left, j);
+        const int hp = p16 == 1 ? in : in / p16, r0 = (in - hp * p16) * 16, kv = g / (GROUPS / 2);
+        const uint16_t *src = reinterpret_cast<const uint16_t *>(a.src) + (((int64_t)from * a.H_p + hp) * 2 * a.P + kv * a.P + r0) * D;
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        constexpr int STEPS = 16 / PER, GO = STEPS < 8 ? STEPS : 8;
+        for (int s = 0; s < GROUP; ++s) {
+          const int r = (g % (GROUPS / 2) * GROUP + s) * PER + side;
+          v[s] = r < left ? __ldcs(reinterpret_cast<const uint4 *>(src + r * D + sub * 8)) : make_uint4(0, 0, 0, 0);
+        }
+      };
+      uint4 v[2][GROUP];
+      fetch(v[0], 0, 0);
+      for (int j = 0; j < here; ++j) {
+        const int from = __shfl_sync(0xffffffffu, l_from, j), to = __shfl_sync(0xffffffffu, l_to, j);
+        const int in = __shfl_sync(0xffffffffu, l_in, j);
+        bool odd = false;
+        __syncwarp();
 #pragma unroll
-        for (int s0 = 0; s0 < STEPS; s0 += GO) {
-          uint4 v[GO];
+        for (int g = 0; g < GROUPS; ++g) {
+          if (g + 1 < GROUPS) fetch(v[(g + 1) & 1], j, g + 1);
+          else if (j + 1 < here) fetch(v[0], j + 1, 0);
+          const int kv = g / (GROUPS / 2);
 #pragma unroll
-          for (int s = 0; s < GO; ++s) {
-            const int r = (s0 + s) * PER + side;
-            v[s] = r < left ? __ldcs(reinterpret_cast<const uint4 *>(src + ((int64_t)kv * a.P + r) * D)) : make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int s = 0; s < GO; ++s) {
-            const int r = (s0 + s) * PER + side;
-            const uint32_t w[4] = {v[s].x, v[s].y, v[s].z, v[s].w};
+          for (int s = 0; s < GROUP; ++s) {
+            const int r = (g % (GROUPS / 2) * GROUP + s) * PER + side, c = sub % 16;
+            const uint32_t w[4] = {v[g & 1][s].x, v[g & 1][s].y, v[g & 1][s].z, v[g & 1][s].w};
             float2 x[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
             const Code8 o = encode_exact(x, kv ? a.v_unit : a.k_unit, odd);  // (the units' reciprocals)
             uint8_t *tile = mine + sub / 16 * kTile4;
-            const int c = sub % 16;
             *reinterpret_cast<uint32_t *>(tile + (kv ? v_codes4(r, c) : k_codes4(r, c))) = o.codes;
             if (!(c & 1)) tile[kv ? v_scale4(r, c / 2) : k_scale4(r, c / 2)] = (uint8_t)o.scale;
           }
         }
+        __syncwarp();
+        if (from < 0 || to < 0) continue;
+        if (odd) report(a.status, TG_STATUS_NONFINITE);
+        uint8_t *dst = a.dst + ((int64_t)to * a.H_p * p16 + in) * TILE;
+        for (int i = lane; i < CHUNKS; i += 32)
+          *reinterpret_cast<uint4 *>(dst + 16 * i) = *reinterpret_cast<const uint4 *>(mine + 16 * i);
       }
-      if (odd) report(a.status, TG_STATUS_NONFINITE);
-      __syncwarp();
-      for (int i = lane; i < CHUNKS; i += 32)
-        *reinterpret_cast<uint4 *>(a.dst + e2m1_at + 16 * i) = *reinterpret_cast<const uint4 *>(mine + 16 * i);
     } else {
-      for (int i = lane; i < CHUNKS; i += 32)
-        *reinterpret_cast<uint4 *>(mine + 16 * i) = __ldcs(reinterpret_cast<const uint4 *>(a.src + e2m1_at + 16 * i));
-      __syncwarp();
-      uint16_t *dst = reinterpret_cast<uint16_t *>(a.dst) + bf16_at + sub * 8;
+      // a tile's pieces, the next tile's on their way while one is written out
+      constexpr int PIECES = (CHUNKS + 31) / 32;
+      auto fetch = [&](uint4(&v)[PIECES], int j) {
+        const int from = __shfl_sync(0xffffffffu, l_from, j), in = __shfl_sync(0xffffffffu, l_in, j);
+        if (from < 0) return;
+        const uint8_t *src = a.src + ((int64_t)from * a.H_p * p16 + in) * TILE + 16 * lane;
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv)
+        for (int i = 0; i < PIECES; ++i)
+          if (32 * i + lane < CHUNKS) v[i] = __ldcs(reinterpret_cast<const uint4 *>(src + 512 * i));
+      };
+      uint4 v[PIECES];
+      fetch(v, 0);
+      for (int j = 0; j < here; ++j) {
+        const int from = __shfl_sync(0xffffffffu, l_from, j), to = __shfl_sync(0xffffffffu, l_to, j);
+        const int in = __shfl_sync(0xffffffffu, l_in, j), left = __shfl_sync(0xffffffffu, l_left, j);
+        const int hp = p16 == 1 ? in : in / p16, r0 = (in - hp * p16) * 16;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i)
+          if (32 * i + lane < CHUNKS) *reinterpret_cast<uint4 *>(mine + 16 * (32 * i + lane)) = v[i];
+        __syncwarp();
+        if (j + 1 < here) fetch(v, j + 1);
+        if (from < 0 || to < 0) continue;
+        uint16_t *dst = reinterpret_cast<uint16_t *>(a.dst) + (((int64_t)to * a.H_p + hp) * 2 * a.P + r0) * D + sub * 8;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv)
 #pragma unroll 4
-        for (int s = 0; s < 16 / PER; ++s) {
-          const int r = s * PER + side, c = sub % 16;
-          const uint8_t *tile = mine + sub / 16 * kTile4;
-          Code8 o;
-          o.codes = *reinterpret_cast<const uint32_t *>(tile + (kv ? v_codes4(r, c) : k_codes4(r, c)));
-          o.scale = tile[kv ? v_scale4(r, c / 2) : k_scale4(r, c / 2)];
-          uint4 v = held8(o, kv ? a.v_unit : a.k_unit);
-          if (r >= left) v = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4 *>(dst + ((int64_t)kv * a.P + r) * D) = v;
-        }
+          for (int s = 0; s < 16 / PER; ++s) {
+            const int r = s * PER + side, c = sub % 16;
+            const uint8_t *tile = mine + sub / 16 * kTile4;
+            Code8 o;
+            o.codes = *reinterpret_cast<const uint32_t *>(tile + (kv ? v_codes4(r, c) : k_codes4(r, c)));
+            o.scale = tile[kv ? v_scale4(r, c / 2) : k_scale4(r, c / 2)];
+            uint4 x = held8(o, kv ? a.v_unit : a.k_unit);
+            if (r >= left) x = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(dst + ((int64_t)kv * a.P + r) * D) = x;
+          }
+      }
     }
   }
 }
