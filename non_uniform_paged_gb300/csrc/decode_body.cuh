@@ -136,9 +136,9 @@ __device__ __forceinline__ void epilogue_sync() {
 
 // The epilogue warps of a CTA over grown runs: as decode_body's, with one or two hand-off buffers, and with what the
 // short launches of a decode step wait for kept short.  Four outputs to a thread; the first partials of a
-// merge are on their way while its factors are made; and where the next item is already handed over, it is counted
-// before this one's run is merged: a CTA that ends one run and begins the next would else keep the second run's
-// other CTAs' merge waiting for the first's (one request of 18000 tokens: 17 -> 11 us).
+// merge are on their way while its factors are made; and where the next piece of a shared run is already handed over,
+// its partial is written too before both are counted, behind one fence, and before either run is merged: a CTA that ends
+// one run and begins the next would else keep the second run's merge waiting for the first's.
 // A piece of a grown run may hold no token: it leaves a partial of no weight.
 template <int D, int NW, int NE, typename GetItem>
 __device__ __forceinline__ void grown_epilogue(const DecodeArgs &a, GetItem get_item, int n_items, int buffers,
@@ -164,7 +164,7 @@ __device__ __forceinline__ void grown_epilogue(const DecodeArgs &a, GetItem get_
     const int np = it.nparts;
     const float *pml = a.ws_ml + (size_t)it.slot0 * g * 2;  // [nparts][g][2]
     const float *po = a.ws_o + (size_t)it.slot0 * g * D;     // [nparts][g][D]
-    constexpr int U = 8;
+    constexpr int U = 12;
     auto load = [&](float4(&v)[U], int e, int p) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -229,60 +229,66 @@ __device__ __forceinline__ void grown_epilogue(const DecodeArgs &a, GetItem get_
     if (etid == 0) a.counters[it.b * a.H + it.h] = 0;
     epilogue_sync<NET>();  // the factors and (M, L) are used again
   };
-  int waiting = -1;  // an item whose run this CTA has yet to merge
-  for (int k = 0; k <= n_items; ++k) {
-    int now = -1, later = -1;  // item k, if its run is to be merged now, or after the next item
-    if (k < n_items) {
-      const tg_work_item it = get_item(k);
-      const int hb = buffers == 2 ? k & 1 : 0, use = buffers == 2 ? k >> 1 : k;
-      if (!*s_dead && !mbar_wait_suspended(&full[hb], (uint32_t)(use & 1), kWaitLimitNs)) {
-        if (etid == 0) report(a.status, TG_STATUS_TIMEOUT);
-        *s_dead = 1;
-      }
-      const float *cm = comb_m + hb * NW * 8, *cl = comb_l + hb * NW * 8, *co = comb_o + hb * cfl;
-      const size_t row0 = (size_t)it.b * a.H_q + (size_t)it.h * g;
-      const int slot = it.slot0 + it.part;
-      for (int e = 4 * etid; e < g * D; e += 4 * NET) {
-        const int hd = e / D, dd = e % D;
-        float M = -INFINITY;
+  int held = -1;  // an item whose partial is written, to be counted with the next one's
+  for (int k = 0; k < n_items; ++k) {
+    const tg_work_item it = get_item(k);
+    const int hb = buffers == 2 ? k & 1 : 0, use = buffers == 2 ? k >> 1 : k;
+    if (!*s_dead && !mbar_wait_suspended(&full[hb], (uint32_t)(use & 1), kWaitLimitNs)) {
+      if (etid == 0) report(a.status, TG_STATUS_TIMEOUT);
+      *s_dead = 1;
+    }
+    const float *cm = comb_m + hb * NW * 8, *cl = comb_l + hb * NW * 8, *co = comb_o + hb * cfl;
+    const size_t row0 = (size_t)it.b * a.H_q + (size_t)it.h * g;
+    const int slot = it.slot0 + it.part;
+    for (int e = 4 * etid; e < g * D; e += 4 * NET) {
+      const int hd = e / D, dd = e % D;
+      float M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) M = fmaxf(M, cm[w * 8 + hd]);
-        float L = 0.f;
-        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 0; w < NW; ++w) M = fmaxf(M, cm[w * 8 + hd]);
+      float L = 0.f;
+      float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          const float f = weight(cm[w * 8 + hd], M);
-          const float4 v = *reinterpret_cast<const float4 *>(co + (w * g + hd) * ostride + dd);
-          L += cl[w * 8 + hd] * f;
-          O.x += v.x * f, O.y += v.y * f, O.z += v.z * f, O.w += v.w * f;
-        }
-        if (it.nparts == 1) {
-          store4(row0 + hd, dd, O, M, L);
-        } else {
-          *reinterpret_cast<float4 *>(a.ws_o + ((size_t)slot * g + hd) * D + dd) = O;
-          if (dd == 0) *reinterpret_cast<float2 *>(a.ws_ml + ((size_t)slot * g + hd) * 2) = make_float2(M, L);
-        }
+      for (int w = 0; w < NW; ++w) {
+        const float f = weight(cm[w * 8 + hd], M);
+        const float4 v = *reinterpret_cast<const float4 *>(co + (w * g + hd) * ostride + dd);
+        L += cl[w * 8 + hd] * f;
+        O.x += v.x * f, O.y += v.y * f, O.z += v.z * f, O.w += v.w * f;
       }
-      mbar_arrive(&empty[hb]);  // (release: this thread's reads of the buffer come first)
-      if (it.nparts > 1) {
-        epilogue_sync<NET>();
-        if (etid == 0) {
-          __threadfence();  // the partial, which the barrier has seen written, before the count
-          flag[0] = atomicAdd(&a.counters[it.b * a.H + it.h], 1) == it.nparts - 1;
-          __threadfence();  // the count before the other partials are read
-          const int nb = buffers == 2 ? (k + 1) & 1 : 0, nu = buffers == 2 ? (k + 1) >> 1 : k + 1;
-          flag[2] = k + 1 < n_items && mbar_try_wait(&full[nb], (uint32_t)(nu & 1));
-        }
-        epilogue_sync<NET>();
-        if (flag[0]) (flag[2] ? later : now) = k;
+      if (it.nparts == 1) {
+        store4(row0 + hd, dd, O, M, L);
+      } else {
+        *reinterpret_cast<float4 *>(a.ws_o + ((size_t)slot * g + hd) * D + dd) = O;
+        if (dd == 0) *reinterpret_cast<float2 *>(a.ws_ml + ((size_t)slot * g + hd) * 2) = make_float2(M, L);
       }
     }
+    mbar_arrive(&empty[hb]);  // (release: this thread's reads of the buffer come first)
+    if (it.nparts == 1) continue;  // (pieces of shared runs come first: none is held here)
+    // (one of two words, by k: a thread may read it as late as at the next item's barrier)
+    volatile int *ready = flag + 2 + (k & 1);
+    if (etid == 0) {
+      const int nb = buffers == 2 ? (k + 1) & 1 : 0, nu = buffers == 2 ? (k + 1) >> 1 : k + 1;
+      *ready = held < 0 && k + 1 < n_items && get_item(k + 1).nparts > 1 && mbar_test_wait(&full[nb], (uint32_t)(nu & 1));
+    }
+    epilogue_sync<NET>();  // the partial is written
+    if (*ready) {
+      held = k;
+      continue;
+    }
+    if (etid == 0) {
+      auto last = [&](int i) {  // whether item i's piece is the last of its run
+        const tg_work_item x = get_item(i);
+        return atomicAdd(&a.counters[x.b * a.H + x.h], 1) == x.nparts - 1;
+      };
+      __threadfence();  // the partials, which the barrier has seen written, before the counts
+      flag[0] = (last(k) ? 1 : 0) | (held >= 0 && last(held) ? 2 : 0);
+      __threadfence();  // the counts before the other partials are read
+    }
+    epilogue_sync<NET>();
+    const int mine = flag[0];
 #pragma unroll 1
-    for (int j = 0; j < 2; ++j) {
-      const int m = j ? now : waiting;
-      if (m >= 0) merge(get_item(m));
-    }
-    waiting = later;
+    for (int j = 0; j < 2; ++j)
+      if (mine >> j & 1) merge(get_item(j ? held : k));
+    held = -1;
   }
   if (etid == 0 && a.cta_time) {
     a.cta_time[2 * blockIdx.x] = (int64_t)*s_t0;

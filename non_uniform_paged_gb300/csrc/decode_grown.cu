@@ -72,7 +72,7 @@ constexpr float kWeightLog2 = 8.f, kWeightMost = 15.f;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -336,7 +336,10 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
             for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                y[hf][j] = fmaf(sc[hf][j], j & 1 ? z1 : z0, j & 1 ? d1 : d0);
+                if (!(j & 1)) {
+                  const float2 v = fma2(make_float2(sc[hf][j], sc[hf][j + 1]), make_float2(z0, z1), make_float2(d0, d1));
+                  y[hf][j] = v.x, y[hf][j + 1] = v.y;
+                }
                 if (part) {
                   const int t = 16 * hf + gid + (j & 2 ? 8 : 0);
                   if (t < r0 || t >= r1) y[hf][j] = -INFINITY;
@@ -384,8 +387,8 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const float p0 = ex2(y[hf][0]), p1 = ex2(y[hf][1]), p2 = ex2(y[hf][2]), p3 = ex2(y[hf][3]);
-            l0 += p0 + p2;
-            l1 += p1 + p3;
+            const float2 l = add2(make_float2(l0, l1), add2(make_float2(p0, p1), make_float2(p2, p3)));
+            l0 = l.x, l1 = l.y;
             wt[hf][0] = movmatrix_t(pack_f16x2(p0, p1));
             wt[hf][1] = movmatrix_t(pack_f16x2(p2, p3));
           }

@@ -541,10 +541,15 @@ class GrowingLists(_OnStreams):
         order = np.array(np.broadcast_to(order, (ntok.shape[0], ntok.shape[2])) if order.ndim == 1 else order, np.int32)
         L, self.batch, H = ntok.shape
         self.H_p, self.P, self.d, self.reserve = H_p, P, d, int(reserve)
-        self.n_cta = int(n_cta) if n_cta else tg_query_ncta(d, H_q // H)
         most = ntok.astype(np.int64) + self.reserve  # the plan's tokens; the split goes by them too
         if most.size and most.max() > 2 ** 31 - 1 - P:
             raise ValueError(f"{most.max()} tokens of a head")
+        # One block of threads an SM, fewer where each would have less than 256 tokens: what the merge of more pieces
+        # takes is then longer than what they save (20000 tokens of 32 + 8 heads, 4 bits and bf16: 76 blocks 10.9 and 13.0
+        # us, 152 blocks 14.0 and 15.6; 74000 tokens: 100 blocks 13.0 and 17.5, 152 blocks 13.9 and 19.1; 290000: 22.9 and
+        # 34.2, 20.2 and 33.2).
+        largest = int(most.sum((1, 2)).max(initial=0))
+        self.n_cta = int(n_cta) if n_cta else max(H // H_p, min(tg_query_ncta(d, H_q // H), -(-largest // 256)))
         Phi = np.stack([most[l][:, order[l]].sum(0).reshape(-1, H_p).sum(1) for l in range(L)])
         plan, workspace = tg_plan_decode(tg_split_map(Phi, self.n_cta), order, most.astype(np.int32), H_q, H_p, P, d)
         self.workspace = torch.zeros(workspace, dtype=torch.uint8, device=self.device)
@@ -611,7 +616,7 @@ class GrowingCache(RaggedCache):
         super().__init__(L, batch, H, H_q, d, P, H_p, alpha, Bhat, N, cluster=cluster, n_cta=n_cta, device=device,
                          alloc_pool=False, allocator=allocator)
         self.lists = GrowingLists(H_q, H_p, P, d, self.pages["order"], self.pages["ntok"], reserve, pages=pages,
-                                  k_unit=k_unit, v_unit=v_unit, n_cta=self.n_cta, device=device)
+                                  k_unit=k_unit, v_unit=v_unit, n_cta=n_cta, device=device)
         self.status = self.lists.status  # one word for all calls
         self.four = self.lists.format == PAGES_E2M1
         page = tg_page_bytes(self.lists.format, H_p, P, d)
