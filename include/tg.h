@@ -739,7 +739,7 @@ int tg_reserve_pages(int L, int batch, int H, int H_p, int P, const int32_t *hea
  *   (host) uint8 [rot/2], each < axes (axes > 1 only); origin int32 [batch] (positions NULL only);
  *   head_order int32 [H], ntok int32 [batch][H], pt_off int64 [batch*G + 1] of this layer, pt_ids; added
  *   int32 [batch] (NULL: zeros); reserve the tokens a head may hold behind its ntok;
- *   pool: the pages, written; k_unit, v_unit: of TG_PAGES_E2M1 (any for bf16);
+ *   pool: the pages, written (its rows fit int32); k_unit, v_unit: of TG_PAGES_E2M1 (any for bf16);
  *   K, V bf16 [batch][H][Nmax][d] (both or neither NULL): if given, row start[b] + i of each head also
  *   gets what the pages hold of the token, for tg_prefill_attn over the pass's own tokens: bf16 pages their
  *   row, 4-bit pages the values they stand for; start int32 [batch].
@@ -747,7 +747,8 @@ int tg_reserve_pages(int L, int batch, int H, int H_p, int P, const int32_t *hea
  *   may not overlap qkv.
  *   Host sizes: d in {128, 256}, rot % 16 == 0, P % 16 == 0, H % H_p == 0.
  *   4-bit pages: a K value is rounded to 4 bits from what float32 arithmetic gives, or, where that is too
- *   close to the border of two codes or scales to tell, from float64 arithmetic: the codes are those of the formulas.
+ *   close to the border of two codes or scales to tell, from float64 arithmetic: the codes are those of the formulas
+ *   (of projections below 2^59 in magnitude, whose squares' sum float32 holds).
  *   A token with added[b] < 0, added[b] + i >= reserve, a position outside [0, max_pos) (rot > 0) or a dense
  *   row outside [0, Nmax) sets TG_STATUS_BAD_INPUT and writes nothing.  A head whose list is too short
  *   or names a page outside [0, pool_pages) sets TG_STATUS_BAD_PAGE and none of its rows is written.
@@ -792,8 +793,8 @@ int tg_dequant_pages(tg_stream_t stream, int batch, int H, int H_p, int P, int d
  * The plan is tg_plan_decode's for ntok + reserve tokens a head.  A piece [t0, t1) of a run takes the same share of
  *   the tokens that are there: with n tokens of c = ntok + reserve, [t0 n / c, t1 n / c) in float32, a
  *   partition of [0, n) into pieces as even as the plan's.
- * Arguments: plan, q, pt_off, pt_ids, scale, workspace, out, lse, dev_status, cta_time as tg_decode_attn; format
- *   and pool (16-byte aligned); ntok int32 [batch][H] of this layer; added int32 [batch] (NULL: zeros);
+ * Arguments: plan, q, pt_off, pt_ids, scale, workspace, out, lse, dev_status, cta_time as tg_decode_attn, q and
+ *   out 16-byte aligned; format and pool (16-byte aligned; tokens of all its heads fit int32); ntok int32 [batch][H] of this layer; added int32 [batch] (NULL: zeros);
  *   plus >= 0; k_unit, v_unit as tg_append_rope.  added[b] + plus outside [0, reserve] sets
  *   TG_STATUS_BAD_INPUT and counts as the nearer end.  Rows behind the last token may hold anything.
  *   A list too short for its tokens, or a page id outside the pool, sets TG_STATUS_BAD_PAGE (out is then

@@ -276,14 +276,17 @@ __global__ void __launch_bounds__(32, E2M1 ? 20 : 28) append_rope_kernel(const _
     if (first < v_first && last > k_first) weigh(a.kw);
     const int u_end = min(end * kSteps, (a.H + PER - 1) / PER);
     Head8 nx = {};
+    int loaded = -1;  // the unit in nx
     for (int u = max(first - k_first, 0) * kSteps; u < u_end; ++u) {
       if ((u * PER & ~31) != p0) places(u * PER & ~31, false);
-      load(nx, u);
+      if (loaded != u) load(nx, u);
+      const Head8 in = nx;
+      if (u + 1 < u_end && ((u + 1) * PER & ~31) == p0) load(nx, loaded = u + 1);  // on its way meanwhile
       const int to = __shfl_sync(0xffffffffu, rows, (u * PER + side) & 31);
       const int h = __shfl_sync(0xffffffffu, head, (u * PER + side) & 31);
       const bool w = a.kw != nullptr;
       float2 xu[2], xv[2], zu[2], zv[2];
-      split(nx, xu, xv);
+      split(in, xu, xv);
       float ta, tb;  // the largest |first product| + |second one| of the first and of the second group
 #pragma unroll
       for (int j = 0; j < 2; ++j) zu[j] = mul2(uc[j], xu[j]), zv[j] = mul2(vc[j], xv[j]);

@@ -55,7 +55,7 @@ __device__ __forceinline__ tg_work_item grown_item(const DecodeArgs &a, tg_work_
   const int extra = (int)min(max(asked, (int64_t)0), (int64_t)a.reserve);
   if (extra != asked) report(a.status, TG_STATUS_BAD_INPUT);
   const int64_t cap = (int64_t)n0 + a.reserve;
-  const int n = n0 + extra;
+  const int n = (int)min((int64_t)n0 + extra, (int64_t)INT32_MAX - 31);
   const float f = cap > 0 ? (float)n / (float)cap : 0.f;
   it.t0 = it.t0 >= cap ? n : min(n, (int)((float)it.t0 * f));
   it.t1 = it.t1 >= cap ? n : min(n, (int)((float)it.t1 * f));

@@ -61,7 +61,7 @@ struct Layout4 {
   static constexpr int MOST = 227 * 1024;
   __host__ __device__ static int ostride(int g) { return g <= 4 ? D + 4 : D; }
   __host__ __device__ static int comb_floats(int g) { return NW * g * ostride(g); }
-  // two hand-off buffers, or one where two do not fit (d = 256 with more than five query heads)
+  // two hand-off buffers, or one where two do not fit (d = 256 with more than four query heads)
   static int buffers(int g) { return bytes(g, 2) <= MOST ? 2 : 1; }
   static int bytes(int g, int nb) { return SMALL + 128 + RING + nb * comb_floats(g) * 4 + kFacMax * 4; }
 };
@@ -534,7 +534,8 @@ extern "C" int tg_decode_grown(tg_stream_t stream, const void *plan_host, const 
   const tg_plan_layer *lt;
   int rc = check_decode_call(fn, plan_host, plan_dev, layer, q, static_cast<const uint16_t *>(pool), scale, &hd, &lt);
   if (rc) return rc;
-  if (reinterpret_cast<uintptr_t>(q) & 15) return fail(TG_ERR_INVALID_ARG, "%s: q must be 16-byte aligned", fn);
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15)
+    return fail(TG_ERR_INVALID_ARG, "%s: q and out must be 16-byte aligned", fn);
   if (workspace_bytes < hd->workspace_bytes)
     return fail(TG_ERR_CAPACITY, "%s: workspace %lld < %lld bytes", fn, (long long)workspace_bytes,
                 (long long)hd->workspace_bytes);

@@ -624,6 +624,11 @@ class GrowingCache(RaggedCache):
         self.pool = torch.empty(max(self.n_pages, 1) * page // kind.itemsize, dtype=kind, device=self.device)
         self._layer_pages = None
 
+    def algorithmic_bytes(self, layer=None) -> int:
+        """As RaggedCache's, before any token is appended: 4-bit pages hold 9/16 of a byte a value."""
+        total = super().algorithmic_bytes(layer)
+        return total - self.retained_tokens(layer) * 2 * self.d * 23 // 16 if self.four else total
+
     def _build_pages(self, pages):
         """The same heads' lists with the reserve."""
         off, ids, n = tg_reserve_pages(pages["order"], pages["ntok"], self.H_p, self.P, self.reserve)

@@ -202,6 +202,18 @@ def test_units(lib, cuda):
     assert c.V[0, 0, int(c.start[0]):int(c.start[0]) + 20].any()
 
 
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("far", [1e2, 1e4, 1e6])
+def test_a_pair_of_very_unlike_values(lib, cuda, far, pairs):
+    """A value whose partner is far larger: what float32 leaves open is then wide against the block's scale."""
+    values = torch.randn((300, 3 * 128), device=cuda, generator=torch.Generator(device=cuda).manual_seed(9)).to(torch.bfloat16)
+    values[:, 128 + 64:256] *= far
+    values[::3, 128:128 + 16] *= 1 / far
+    c = Case(cuda, 1, [300], [[5]], 1, 1, 128, values=values, pairs=pairs, dense=True, qw=False)
+    assert c.call(lib) == 0
+    c.verify()
+
+
 def test_values_that_are_not_finite_set_the_status(lib, cuda):
     """An infinite V value is held as the largest, a NaN as the block's +6; neighbours in other blocks are untouched."""
     values = torch.randn((3, 3 * 128), device=cuda).to(torch.bfloat16)
@@ -244,6 +256,15 @@ def test_tokens_outside_the_limits_write_nothing(lib, cuda, fmt):
     c = Case(cuda, fmt, [4], [[6]], 2, 1, 128, axes=2)
     c.positions[2, c.axis_of[0]] = 600
     assert c.call(lib) == lib.STATUS_BAD_INPUT and written(c) == [True, True, False, True]
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_more_heads_than_places_looked_up_at_once(lib, cuda, fmt):
+    """70 KV heads in groups of 5 and 14: three lookups of 32 places, with one warp a token and with several."""
+    for H_p, T in ((5, 3), (14, 2100)):
+        c = Case(cuda, fmt, [T], [[(7 * h) % 40 for h in range(70)]], 3, 70, 128, H_p=H_p, max_pos=3000, dense=T < 10, seed=T)
+        assert c.call(lib) == 0
+        c.verify()
 
 
 @pytest.mark.parametrize("fmt", [0, 1])

@@ -223,6 +223,22 @@ def test_counts_outside_the_reserve_are_reported_and_clamped(lib, cuda, pages):
 
 
 @pytest.mark.parametrize("pages", FORMATS)
+def test_counts_that_are_not_the_plans_stay_in_the_lists(lib, cuda, pages):
+    """Device counts other than those planned for: nothing outside the lists is read, the other requests are right."""
+    x = Lists(cuda, pages, [[100], [100], [100]], 2, 128, reserve=10, n_cta=5, hostile=False)
+    kept = x.lists.ntok[0].clone()
+    for wrong, status in ((-7, 0), (2 ** 31 - 1, None), (0, 0), (95, 0)):
+        x.lists.status.zero_()
+        x.lists.ntok[0][1, 0] = wrong
+        out, lse, got = x.run([3, 4, 5])
+        assert got in ((0, lib.STATUS_BAD_PAGE) if status is None else (status,))
+        x.compare(out, lse, [3, 4, 5], requests=[0, 2])
+    x.lists.ntok[0].copy_(kept)
+    x.lists.status.zero_()
+    x.check(lib, [1, 2, 3])
+
+
+@pytest.mark.parametrize("pages", FORMATS)
 def test_bad_pages_are_reported_and_the_others_are_right(lib, cuda, pages):
     x = Lists(cuda, pages, [[100], [100], [100]], 2, 128, reserve=10, n_cta=5, hostile=False)
     ids = x.ids.clone()

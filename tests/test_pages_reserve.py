@@ -175,7 +175,7 @@ def test_decode_grown_refusals(lib):
     junk = np.zeros_like(plan)
     cases = [(dict(format=2), INVALID), (dict(plus=-1), INVALID), (dict(reserve=-1, plus=0), INVALID), (dict(plus=5), INVALID),
              (dict(layer=1), INVALID), (dict(layer=-1), INVALID), (dict(plan_host=junk.ctypes.data), INVALID),
-             (dict(scale=float("nan")), NONFINITE), (dict(q=FAKE + 8), INVALID), (dict(pool=FAKE + 8), INVALID),
+             (dict(scale=float("nan")), NONFINITE), (dict(q=FAKE + 8), INVALID), (dict(out=FAKE + 8), INVALID), (dict(pool=FAKE + 8), INVALID),
              (dict(plan_dev=FAKE + 8), INVALID), (dict(workspace=FAKE + 128), INVALID), (dict(workspace_bytes=ws - 1), CAPACITY),
              (dict(k_unit=1.5), INVALID), (dict(v_unit=2.0 ** -61), INVALID), (dict(pool_pages=0), CAPACITY),
              (dict(pool_pages=2 ** 31), CAPACITY)]
