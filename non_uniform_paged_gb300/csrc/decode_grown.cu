@@ -94,6 +94,12 @@ __device__ __forceinline__ uint32_t lds16(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 struct Pool4 {
   const uint8_t *base;
   int p16;  // tiles of a head in a page
@@ -222,6 +228,7 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
     };
     int at_cur = tile_at(lane), at_nxt = 0;
     int issued = 0, consumed = 0;
+    const uint32_t stage0 = smem_addr(ring + warp * R * LY::STAGE);
     auto issue = [&]() {  // whole warp: step number `issued` of this warp into stage issued % R
       const int from = 2 * (issued & 15);
       const int at0 = __shfl_sync(0xffffffffu, at_cur, from), at1 = __shfl_sync(0xffffffffu, at_cur, from + 1);
@@ -301,7 +308,7 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
             dead = true;
             break;
           }
-          const uint32_t stage = smem_addr(ring + (warp * R + s) * LY::STAGE);
+          const uint32_t stage = stage0 + s * LY::STAGE;
           const int r0 = it.t0 - kk * 32, r1 = it.t1 - kk * 32;  // valid rows [r0, r1) of the step
           const bool part = r0 > 0 || r1 < 32;
 
@@ -330,6 +337,15 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
               }
             }
           }
+          // the codes of V, on their way during the softmax
+          uint4 vx[C][2], vy[C][2];
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const uint32_t vt = stage + hf * LY::TILE + c * kTile4 + kVCodes4;
+              vx[c][hf] = lds128(vt + 64 * gid + 16 * tig), vy[c][hf] = lds128(vt + 512 + 64 * gid + 16 * tig);
+            }
           // online softmax, base 2; y = x - m + 8
           auto logits = [&](float(&y)[2][4]) {
 #pragma unroll
@@ -348,9 +364,8 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
           };
           float y[2][4];
           logits(y);
-          const float top0 = fmaxf(fmaxf(y[0][0], y[0][2]), fmaxf(y[1][0], y[1][2]));
-          const float top1 = fmaxf(fmaxf(y[0][1], y[0][3]), fmaxf(y[1][1], y[1][3]));
-          if (__any_sync(0xffffffffu, fmaxf(top0, top1) > kWeightMost)) {
+          const float top = max3(max3(y[0][0], y[0][1], y[0][2]), max3(y[0][3], y[1][0], y[1][1]), fmaxf(y[1][2], y[1][3]));
+          if (__any_sync(0xffffffffu, top > kWeightMost)) {
             // the reference moves to the maximum so far
             float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
@@ -398,8 +413,8 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
           for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-              const uint32_t tile = stage + hf * LY::TILE + c * kTile4, vt = tile + kVCodes4;
-              const uint4 x = lds128(vt + 64 * gid + 16 * tig), yv = lds128(vt + 512 + 64 * gid + 16 * tig);
+              const uint32_t tile = stage + hf * LY::TILE + c * kTile4;
+              const uint4 x = vx[c][hf], yv = vy[c][hf];
               uint32_t sx = e4m3x2_to_f16x2(lds16(tile + kVScales4 + 16 * gid + 2 * tig));
               uint32_t sy = e4m3x2_to_f16x2(lds16(tile + kVScales4 + 16 * gid + 2 * tig + 8));
               if (part) {  // rows that are no token of this piece may hold anything: 0 times a code is 0
