@@ -100,6 +100,15 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+__device__ __forceinline__ void arrive_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_load_at(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
 struct Pool4 {
   const uint8_t *base;
   int p16;  // tiles of a head in a page
@@ -141,7 +150,7 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
   tg_work_item mine = lead;  // of warp 0's lanes: item `lane`
   if (items_in_smem && warp == 0 && lane > 0 && lane < n_items) mine = a.items[i_begin + lane];
   if (warp < NW && lane == 0)
-    for (int s = 0; s < R; ++s) mbar_init(&bars[warp * R + s], 1);
+    for (int s = 0; s < R; ++s) mbar_init(&bars[warp * R + s], 2);  // (a lane for each half)
   if (tid == NS) {
     for (int b = 0; b < 2; ++b) {
       mbar_init(&full[b], NS);
@@ -229,18 +238,17 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
     int at_cur = tile_at(lane), at_nxt = 0;
     int issued = 0, consumed = 0;
     const uint32_t stage0 = smem_addr(ring + warp * R * LY::STAGE);
+    // lanes 0 and 1 copy a tile each into their half of the stage
+    const uint32_t bar0 = smem_addr(&bars[warp * R]), to0 = stage0 + (lane & 1) * LY::TILE;
     auto issue = [&]() {  // whole warp: step number `issued` of this warp into stage issued % R
-      const int from = 2 * (issued & 15);
-      const int at0 = __shfl_sync(0xffffffffu, at_cur, from), at1 = __shfl_sync(0xffffffffu, at_cur, from + 1);
-      if (lane == 0) {
+      const int at = __shfl_sync(0xffffffffu, at_cur, 2 * (issued & 15) + (lane & 1));
+      if (lane < 2) {
+        fence_proxy_async_smem();  // what was read of this stage comes before the refill
         const int s = issued % R;
-        uint64_t *bar = &bars[warp * R + s];
-        uint8_t *to = ring + (warp * R + s) * LY::STAGE;
-        if (at0 == kBad || at1 == kBad) report(a.status, TG_STATUS_BAD_PAGE);
-        // (a phase without data completes at once)
-        mbar_arrive_expect_tx(bar, (at0 >= 0 ? LY::TILE : 0) + (at1 >= 0 ? LY::TILE : 0));
-        if (at0 >= 0) bulk_load(to, pool.base + (int64_t)at0 * LY::TILE, LY::TILE, bar);
-        if (at1 >= 0) bulk_load(to + LY::TILE, pool.base + (int64_t)at1 * LY::TILE, LY::TILE, bar);
+        if (at == kBad) report(a.status, TG_STATUS_BAD_PAGE);
+        // (an arrival without data)
+        arrive_expect(bar0 + 8 * s, at >= 0 ? LY::TILE : 0);
+        if (at >= 0) bulk_load_at(to0 + s * LY::STAGE, pool.base + (int64_t)at * LY::TILE, LY::TILE, bar0 + 8 * s);
       }
       ++issued;
       if ((issued & 15) == 0) {
@@ -337,6 +345,19 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
               }
             }
           }
+          if (part) {
+            // Rows that are no token of this piece may hold anything.  Their scores are replaced below; their V's scales
+            // are cleared here, for a weight of 0 times a code times 0 is 0.
+            if (lane < r0 || lane >= r1) {
+#pragma unroll
+              for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  asm volatile("st.shared.u8 [%0], %1;" ::"r"(stage + (lane >> 4) * LY::TILE + c * kTile4 + v_scale4(lane & 15, j)),
+                               "r"(0) : "memory");
+            }
+            __syncwarp();
+          }
           // the codes of V, on their way during the softmax
           uint4 vx[C][2], vy[C][2];
 #pragma unroll
@@ -351,16 +372,19 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                if (!(j & 1)) {
-                  const float2 v = fma2(make_float2(sc[hf][j], sc[hf][j + 1]), make_float2(z0, z1), make_float2(d0, d1));
-                  y[hf][j] = v.x, y[hf][j + 1] = v.y;
-                }
-                if (part) {
+              for (int j = 0; j < 4; j += 2) {
+                const float2 v = fma2(make_float2(sc[hf][j], sc[hf][j + 1]), make_float2(z0, z1), make_float2(d0, d1));
+                y[hf][j] = v.x, y[hf][j + 1] = v.y;
+              }
+            if (part) {
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
                   const int t = 16 * hf + gid + (j & 2 ? 8 : 0);
                   if (t < r0 || t >= r1) y[hf][j] = -INFINITY;
                 }
-              }
+            }
           };
           float y[2][4];
           logits(y);
@@ -415,15 +439,8 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
             for (int hf = 0; hf < 2; ++hf) {
               const uint32_t tile = stage + hf * LY::TILE + c * kTile4;
               const uint4 x = vx[c][hf], yv = vy[c][hf];
-              uint32_t sx = e4m3x2_to_f16x2(lds16(tile + kVScales4 + 16 * gid + 2 * tig));
-              uint32_t sy = e4m3x2_to_f16x2(lds16(tile + kVScales4 + 16 * gid + 2 * tig + 8));
-              if (part) {  // rows that are no token of this piece may hold anything: 0 times a code is 0
-                auto kept = [&](int t) {
-                  return (t >= r0 && t < r1 ? 0xffffu : 0u) | (t + 1 >= r0 && t + 1 < r1 ? 0xffff0000u : 0u);
-                };
-                sx &= kept(16 * hf + 2 * tig);
-                sy &= kept(16 * hf + 2 * tig + 8);
-              }
+              const uint32_t sx = e4m3x2_to_f16x2(lds16(tile + kVScales4 + 16 * gid + 2 * tig));
+              const uint32_t sy = e4m3x2_to_f16x2(lds16(tile + kVScales4 + 16 * gid + 2 * tig + 8));
 #pragma unroll
               for (int w = 0; w < 2; ++w) {  // values 8 w .. 8 w + 7 of the block
                 const uint32_t xa = w ? x.y : x.x, xb = w ? x.w : x.z, ya = w ? yv.y : yv.x, yb = w ? yv.w : yv.z;
@@ -441,10 +458,7 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
             }
           ++consumed;
           __syncwarp();
-          if (issued < total) {
-            if (lane == 0) fence_proxy_async_smem();  // our reads of this stage come before the refill
-            issue();
-          }
+          if (issued < total) issue();
         }
       }
 
