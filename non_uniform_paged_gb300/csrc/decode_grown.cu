@@ -358,15 +358,13 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
             }
             __syncwarp();
           }
-          // the codes of V, on their way during the softmax
-          uint4 vx[C][2], vy[C][2];
+          // the codes of V (of the first 128 values: of 256 they would spill), on their way during the softmax
+          uint4 vx[2], vy[2];
 #pragma unroll
-          for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              const uint32_t vt = stage + hf * LY::TILE + c * kTile4 + kVCodes4;
-              vx[c][hf] = lds128(vt + 64 * gid + 16 * tig), vy[c][hf] = lds128(vt + 512 + 64 * gid + 16 * tig);
-            }
+          for (int hf = 0; hf < 2; ++hf) {
+            const uint32_t vt = stage + hf * LY::TILE + kVCodes4;
+            vx[hf] = lds128(vt + 64 * gid + 16 * tig), vy[hf] = lds128(vt + 512 + 64 * gid + 16 * tig);
+          }
           // online softmax, base 2; y = x - m + 8
           auto logits = [&](float(&y)[2][4]) {
 #pragma unroll
@@ -438,7 +436,8 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               const uint32_t tile = stage + hf * LY::TILE + c * kTile4;
-              const uint4 x = vx[c][hf], yv = vy[c][hf];
+              const uint4 x = c == 0 ? vx[hf] : lds128(tile + kVCodes4 + 64 * gid + 16 * tig);
+              const uint4 yv = c == 0 ? vy[hf] : lds128(tile + kVCodes4 + 512 + 64 * gid + 16 * tig);
               const uint32_t sx = e4m3x2_to_f16x2(lds16(tile + kVScales4 + 16 * gid + 2 * tig));
               const uint32_t sy = e4m3x2_to_f16x2(lds16(tile + kVScales4 + 16 * gid + 2 * tig + 8));
 #pragma unroll
