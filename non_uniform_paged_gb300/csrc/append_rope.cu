@@ -197,73 +197,92 @@ __global__ void __launch_bounds__(32, E2M1 ? 20 : 28) append_rope_kernel(const _
     return rsqrtf(fmaf(ss, 1.f / D, a.eps));
   };
 
-  // ---- queries, and keys of bf16 pages
-  {
-    auto load = [&](Head8(&x)[kSteps], int k) {
-      const bool query = k < k_first;
-      const int h0 = (query ? k : k - k_first) * BATCH + side;
+  // a lane's rotated values of a head, as bf16
+  auto turn = [&](const Head8 &in, bool norm, uint2 &oa, uint2 &ob) {
+    float2 xu[2], xv[2], zu[2], zv[2];
+    split(in, xu, xv);
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const int h = query ? (h0 + s * PER < a.H_q ? h0 + s * PER : -1) : __shfl_sync(0xffffffffu, head, (h0 + s * PER) & 31);
-        if (h >= 0) load_turned(x[s], src + (query ? 0 : a.H_q * D), h);
-      }
+    for (int j = 0; j < 2; ++j) zu[j] = mul2(uc[j], xu[j]), zv[j] = mul2(vc[j], xv[j]);
+    if (turned) {  // behind rot a value meets no other: 0 times an infinite one would be NaN
+#pragma unroll
+      for (int j = 0; j < 2; ++j) zu[j] = fma2(vs[j], xv[j], zu[j]), zv[j] = fma2(us[j], xu[j], zv[j]);
+    }
+    if (norm) {
+      const float f = root(xu, xv);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) zu[j] = mul2(zu[j], make_float2(f, f)), zv[j] = mul2(zv[j], make_float2(f, f));
+    }
+    if (PAIRS) {
+      oa = make_uint2(pack_bf16x2(zu[0].x, zv[0].x), pack_bf16x2(zu[0].y, zv[0].y));
+      ob = make_uint2(pack_bf16x2(zu[1].x, zv[1].x), pack_bf16x2(zu[1].y, zv[1].y));
+    } else {
+      oa = make_uint2(pack_bf16x2(zu[0].x, zu[0].y), pack_bf16x2(zu[1].x, zu[1].y));
+      ob = make_uint2(pack_bf16x2(zv[0].x, zv[0].y), pack_bf16x2(zv[1].x, zv[1].y));
+    }
+  };
+
+  // ---- queries: a batch is loaded while the one ahead of it is worked on
+  if (first < k_first) {
+    const int end = min(last, k_first);
+    auto load = [&](Head8(&x)[kSteps], int k) {
+      const int h0 = k * BATCH + side;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+        if (h0 + s * PER < a.H_q) load_turned(x[s], src + s * PER * D, h0);
     };
     auto work = [&](const Head8(&x)[kSteps], int k) {
-      const bool query = k < k_first;
-      const int h0 = (query ? k : k - k_first) * BATCH, n = query ? a.H_q : a.H;
-      const float *w = query ? a.qw : a.kw;
-      weigh(w);
+      uint16_t *dst = a.q + ((int64_t)t * a.H_q + k * BATCH + side) * D;
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        if (h0 + s * PER >= n) break;
-        const int at = h0 + s * PER + side;
-        float2 xu[2], xv[2], zu[2], zv[2];
-        split(x[s], xu, xv);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) zu[j] = mul2(uc[j], xu[j]), zv[j] = mul2(vc[j], xv[j]);
-        if (turned) {  // behind rot a value meets no other: 0 times an infinite one would be NaN
-#pragma unroll
-          for (int j = 0; j < 2; ++j) zu[j] = fma2(vs[j], xv[j], zu[j]), zv[j] = fma2(us[j], xu[j], zv[j]);
-        }
-        if (w) {
-          const float f = root(xu, xv);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) zu[j] = mul2(zu[j], make_float2(f, f)), zv[j] = mul2(zv[j], make_float2(f, f));
-        }
+      for (int s = 0; s < kSteps; ++s, dst += PER * D) {
+        if (k * BATCH + s * PER >= a.H_q) break;
         uint2 oa, ob;
-        if (PAIRS) {
-          oa = make_uint2(pack_bf16x2(zu[0].x, zv[0].x), pack_bf16x2(zu[0].y, zv[0].y));
-          ob = make_uint2(pack_bf16x2(zu[1].x, zv[1].x), pack_bf16x2(zu[1].y, zv[1].y));
-        } else {
-          oa = make_uint2(pack_bf16x2(zu[0].x, zu[0].y), pack_bf16x2(zu[1].x, zu[1].y));
-          ob = make_uint2(pack_bf16x2(zv[0].x, zv[0].y), pack_bf16x2(zv[1].x, zv[1].y));
-        }
-        if (query) {
-          if (at >= n) continue;
-          uint16_t *dst = a.q + ((int64_t)t * a.H_q + h0 + side) * D + s * PER * D;
-          *reinterpret_cast<uint2 *>(dst + ga) = oa;
-          *reinterpret_cast<uint2 *>(dst + gb) = ob;
-        } else {
-          const int to = __shfl_sync(0xffffffffu, rows, at & 31);
-          const int h = __shfl_sync(0xffffffffu, head, at & 31);
-          if (to < 0) continue;
-          uint16_t *dst = reinterpret_cast<uint16_t *>(a.pool) + (int64_t)to * D;
-          *reinterpret_cast<uint2 *>(dst + ga) = oa;
-          *reinterpret_cast<uint2 *>(dst + gb) = ob;
-          if (a.K) {
-            dst = dense(a.K, h);
-            *reinterpret_cast<uint2 *>(dst + ga) = oa;
-            *reinterpret_cast<uint2 *>(dst + gb) = ob;
-          }
-        }
+        turn(x[s], a.qw != nullptr, oa, ob);
+        if (k * BATCH + s * PER + side >= a.H_q) continue;
+        *reinterpret_cast<uint2 *>(dst + ga) = oa;
+        *reinterpret_cast<uint2 *>(dst + gb) = ob;
       }
     };
-    const int end = min(last, E2M1 ? k_first : v_first);
-    Head8 x[kSteps] = {};
-    for (int k = first; k < end; ++k) {
-      if (k >= k_first && ((k - k_first) * BATCH & ~31) != p0) places((k - k_first) * BATCH & ~31, false);
-      load(x, k);
-      work(x, k);
+    Head8 x0[kSteps] = {}, x1[kSteps] = {};
+    load(x0, first);
+    weigh(a.qw);
+    for (int k = first; k < end; k += 2) {
+      if (k + 1 < end) load(x1, k + 1);
+      work(x0, k);
+      if (k + 1 >= end) break;
+      if (k + 2 < end) load(x0, k + 2);
+      work(x1, k + 1);
+    }
+  }
+  // ---- keys of bf16 pages
+  if (!E2M1) {
+    const int begin = max(first, k_first), end = min(last, v_first);
+    if (begin < end) weigh(a.kw);
+    for (int k = begin; k < end; ++k) {
+      const int h0 = (k - k_first) * BATCH;
+      if ((h0 & ~31) != p0) places(h0 & ~31, false);
+      Head8 x[kSteps] = {};
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int h = __shfl_sync(0xffffffffu, head, (h0 + s * PER + side) & 31);
+        if (h >= 0) load_turned(x[s], src + a.H_q * D, h);
+      }
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        if (h0 + s * PER >= a.H) break;
+        uint2 oa, ob;
+        turn(x[s], a.kw != nullptr, oa, ob);
+        const int to = __shfl_sync(0xffffffffu, rows, (h0 + s * PER + side) & 31);
+        const int h = __shfl_sync(0xffffffffu, head, (h0 + s * PER + side) & 31);
+        if (to < 0) continue;
+        uint16_t *dst = reinterpret_cast<uint16_t *>(a.pool) + (int64_t)to * D;
+        *reinterpret_cast<uint2 *>(dst + ga) = oa;
+        *reinterpret_cast<uint2 *>(dst + gb) = ob;
+        if (a.K) {
+          dst = dense(a.K, h);
+          *reinterpret_cast<uint2 *>(dst + ga) = oa;
+          *reinterpret_cast<uint2 *>(dst + gb) = ob;
+        }
+      }
     }
   }
   // ---- keys of 4-bit pages: one unit in a turn of the loop (what unrolling it adds to the code costs more than it hides)
