@@ -8,8 +8,10 @@
 // A block is a warp: one token, or one batch of a token's heads where there are few tokens.  A head is d / 8
 // lanes; a lane's 8 values are 4 first and the 4 second ones of its pairs (i, i + rot/2), so that the rotation
 // exchanges nothing, or 8 consecutive ones (pairs (2i, 2i + 1), values behind rot, V).  Where the heads' rows lie is
-// looked up once, for 32 places of the groups at a time, each by a lane; K and V lie side by side.  A batch's
-// projections are on their way while the one before it is worked on.
+// looked up once, for 32 places of the groups at a time, each by a lane; K and V lie side by side.  Queries, keys and
+// values have a loop each; a batch of queries (a unit of 4-bit keys) is on its way while the one before it is worked
+// on.  15000 tokens of 16 + 8 + 8 heads of 128 into bf16 pages, 372 MB: 68 us, 5.5 TB/s (71.5 with one loop for all
+// three; 70.1 with 24 blocks to an SM and 72.9 with 20, for 28; 72.6 with batches of 2 loads for 4).
 //
 // 4-bit pages.  A head's rotated values go through shared memory, so that a lane has 8 consecutive ones and a pair
 // of lanes a block of 16.  float32 leaves a value z = f (u c x_u - v s x_v) off by at most 15 2^-24 t,
@@ -18,8 +20,8 @@
 // to the border of two.  So both are taken of the value moved down and up by as much, with the block's
 // largest t; where they differ (a row in some hundred) the row is computed again in float64, from the projections in
 // registers, and what was open is taken from that.  V is exact and needs none of this.  (2600 tokens of 16 + 16 heads
-// of 256: with a bound by the row's largest value and float64 divisions 23 us of 56; with the keys'
-// loop unrolled, 16 more, waiting for instructions.)
+// of 256: 30.8 us.  A bound by the row's largest value with float64 divisions costs 23 more; the keys'
+// loop unrolled 16 more, waiting for instructions.)
 #include "packed.cuh"
 #include "page4.cuh"
 #include "ptx.cuh"
@@ -46,7 +48,7 @@ struct AppendArgs {
   int32_t *status;
   int batch, H_q, H, H_p, G, P, Nmax, rot, max_pos, axes, reserve;
   int q_batches, kv_batches;  // batches of the query heads, and of the key (and of the value) heads
-  int parts;                  // warps of a token: 1, 3 (queries, keys, values), or one for each of its batches
+  int parts;                  // warps of a token: 1, or one for each of its batches
   float eps, k_unit, v_unit, k_to_unit, v_to_unit;  // to: the reciprocals
   uint32_t axis[8];  // two bits for each pair
 };
@@ -76,8 +78,7 @@ __global__ void __launch_bounds__(32, E2M1 ? 20 : 28) append_rope_kernel(const _
   const int t = a.parts == 1 ? blockIdx.x : blockIdx.x / a.parts, part = blockIdx.x - t * a.parts;
   // the token's batches [first, last) of this warp: queries, then keys, then values
   const int k_first = a.q_batches, v_first = k_first + a.kv_batches, all = v_first + a.kv_batches;
-  const int first = a.parts == 1 || (a.parts == 3 && part == 0) ? 0 : a.parts != 3 ? part : part == 1 ? k_first : v_first;
-  const int last = a.parts == 1 ? all : a.parts != 3 ? part + 1 : part == 0 ? k_first : part == 1 ? v_first : all;
+  const int first = part, last = a.parts == 1 ? all : part + 1;
   // the two groups of this lane in a query or key head; of a value head they are 8 consecutive values
   const bool turned = sub * 8 < a.rot;
   const int ga = !PAIRS && turned ? sub * 4 : sub * 8, gb = !PAIRS && turned ? sub * 4 + a.rot / 2 : sub * 8 + 4;
@@ -122,7 +123,7 @@ __global__ void __launch_bounds__(32, E2M1 ? 20 : 28) append_rope_kernel(const _
     }
     rows = (page * a.H_p + (int)hp) * (E2M1 ? a.P : 2 * a.P) + (int)r;
   };
-  bool bad = grown < 0 || (int64_t)grown + i >= a.reserve || (a.K && (row < 0 || row >= a.Nmax));
+  bool bad = i < 0 || grown < 0 || (int64_t)grown + i >= a.reserve || (a.K && (row < 0 || row >= a.Nmax));
   // (a token that is refused below reports nothing of its pages)
   if (last > k_first) places(first <= k_first ? 0 : ((first - (first >= v_first ? v_first : k_first)) * BATCH) & ~31, bad);
   // this lane's four pairs
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(32, E2M1 ? 20 : 28) append_rope_kernel(const _
     if (lane == 0) report(a.status, TG_STATUS_BAD_INPUT);
     return;
   }
-  // a lane's values of unit s of batch k (PER heads side by side): of a query or key head, or of a value head
+  // a lane's values of a query or key head
   auto load_turned = [&](Head8 &x, const uint16_t *from, int h) {
     x.a = __ldcs(reinterpret_cast<const uint2 *>(from + h * D + ga));
     x.b = __ldcs(reinterpret_cast<const uint2 *>(from + h * D + gb));

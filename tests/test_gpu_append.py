@@ -250,6 +250,12 @@ def test_tokens_outside_the_limits_write_nothing(lib, cuda, fmt):
     assert bool((c.pool == (0x5b if fmt else c.mark)).all())
     c, status = run(positions=[0, -1, 600, 599])
     assert status == lib.STATUS_BAD_INPUT and written(c) == [True, False, False, True]
+    # tokens ahead of their request would be rows that it retained
+    c, status = run(change={"cu_q": torch.tensor([2, 4], dtype=torch.int32, device=cuda)})
+    assert status == lib.STATUS_BAD_INPUT and written(c) == [False, False, True, True]
+    c, status = run(change={"cu_q": torch.tensor([4, 4], dtype=torch.int32, device=cuda)})
+    assert status == lib.STATUS_BAD_INPUT and written(c) == [False] * 4
+    assert bool((c.pool == (0x5b if fmt else c.mark)).all())
     c, status = run(dense=True, change={"start": torch.tensor([6], dtype=torch.int32, device=cuda)})  # rows 6 .. 9 of 9
     assert status == lib.STATUS_BAD_INPUT and written(c) == [True, True, True, False]
     c, status = run(axes=2)
