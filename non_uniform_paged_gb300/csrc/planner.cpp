@@ -12,6 +12,8 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <memory>
+#include <new>
 #include <numeric>
 #include <string>
 #include <vector>
@@ -193,28 +195,25 @@ extern "C" int tg_reserve_pages(int L, int batch, int H, int H_p, int P, const i
   if (n_pages) *n_pages = total;
   if (pt_ids && pt_cap < total)
     return fail(TG_ERR_CAPACITY, "%s: pt_cap=%lld < %lld pages", fn, (long long)pt_cap, (long long)total);
+  std::unique_ptr<int64_t[]> next(new (std::nothrow) int64_t[batch]);  // id of each request's next page
+  if (!next) return fail(TG_ERR_CAPACITY, "%s: no host memory for %d requests", fn, batch);
+  int64_t first = 0;
+  for (int b = 0; b < batch; ++b) {
+    next[b] = first;
+    for (int l = 0; l < L; ++l)
+      for (int g = 0; g < G; ++g) first += pages_of(l, b, g);
+  }
   int64_t at = 0;
-  for (int l = 0; l < L; ++l) {
-    int64_t before = 0;  // pages of the earlier requests and, in this one, of the earlier layers
-    for (int b = 0; b < batch; ++b) {
-      if (pt_ids) {
-        for (int i = 0; i < l; ++i)
-          for (int g = 0; g < G; ++g) before += pages_of(i, b, g);
-      }
+  for (int l = 0; l < L; ++l)
+    for (int b = 0; b < batch; ++b)
       for (int g = 0; g < G; ++g) {
         const int64_t n = pages_of(l, b, g);
         if (pt_off) pt_off[((int64_t)l * batch + b) * G + g] = at;
         if (pt_ids)
-          for (int64_t p = 0; p < n; ++p) pt_ids[at + p] = (int32_t)(before + p);
+          for (int64_t p = 0; p < n; ++p) pt_ids[at + p] = (int32_t)(next[b] + p);
         at += n;
-        before += n;
+        next[b] += n;
       }
-      if (pt_ids) {
-        for (int i = l + 1; i < L; ++i)
-          for (int g = 0; g < G; ++g) before += pages_of(i, b, g);
-      }
-    }
-  }
   if (pt_off) pt_off[(int64_t)L * batch * G] = at;
   return tgi::ok();
 }
@@ -223,6 +222,7 @@ extern "C" int tg_page_bytes(int format, int H_p, int P, int d, int64_t *bytes) 
   if (!bytes || H_p <= 0 || P <= 0 || P % 16) return fail(TG_ERR_INVALID_ARG, "tg_page_bytes: H_p=%d, P=%d or NULL", H_p, P);
   if (d != 128 && d != 256) return fail(TG_ERR_SHAPE, "tg_page_bytes: d=%d (128 or 256)", d);
   if (format != TG_PAGES_BF16 && format != TG_PAGES_E2M1) return fail(TG_ERR_INVALID_ARG, "tg_page_bytes: format=%d", format);
+  if ((int64_t)H_p * P > INT32_MAX) return fail(TG_ERR_CAPACITY, "tg_page_bytes: H_p=%d of P=%d tokens", H_p, P);
   *bytes = format == TG_PAGES_BF16 ? (int64_t)H_p * 2 * P * d * 2 : (int64_t)H_p * (P / 16) * (d / 128) * TG_TILE4_BYTES;
   return tgi::ok();
 }

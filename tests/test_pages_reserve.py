@@ -57,10 +57,26 @@ def test_refused_tables(lib):
     assert n.value == 8 and not ids.any()
 
 
+def test_owners_refuse_before_they_take_anything(lib):
+    from non_uniform_paged_gb300.ragged import GrowingCache, GrowingLists
+
+    class Never:
+        def admit(self, counts):
+            raise AssertionError("pages were taken")
+
+    for bad in (dict(pages="e4m3"), dict(reserve=-1)):
+        with pytest.raises(ValueError):
+            GrowingLists(**dict(dict(H_q=4, H_p=1, P=16, d=128, order=[0, 1], ntok=[[5, 5]], reserve=3, n_cta=4, device="cpu"), **bad))
+        w = synth.small()
+        with pytest.raises(ValueError):
+            GrowingCache(w.L, w.batch, w.H, w.H_q, w.d, w.P, w.H_p, w.alpha, synth.budgets_hat(w), synth.contexts(w), n_cta=24,
+                         device="cpu", allocator=Never(), **dict(dict(reserve=3), **bad))
+
+
 def test_page_bytes(lib):
     assert lib.tg_page_bytes(lib.PAGES_BF16, 4, 16, 128) == 4 * 2 * 16 * 128 * 2
     assert lib.tg_page_bytes(lib.PAGES_E2M1, 4, 48, 256) == 4 * 3 * 2 * 2304
-    for bad in ((2, 4, 16, 128), (1, 0, 16, 128), (1, 4, 24, 128), (0, 4, 16, 64)):
+    for bad in ((2, 4, 16, 128), (1, 0, 16, 128), (1, 4, 24, 128), (0, 4, 16, 64), (0, 2 ** 30, 2 ** 30, 256)):
         with pytest.raises(lib.TGError):
             lib.tg_page_bytes(*bad)
 
