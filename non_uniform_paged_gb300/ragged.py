@@ -520,6 +520,14 @@ class SharedPrefix(_OnStreams):
 PAGE_FORMATS = {"bf16": PAGES_BF16, "e2m1": PAGES_E2M1}
 
 
+def _page_format(pages, reserve):
+    if pages not in PAGE_FORMATS:
+        raise ValueError(f"pages={pages!r} (one of {sorted(PAGE_FORMATS)})")
+    if int(reserve) < 0:
+        raise ValueError(f"reserve={reserve} < 0")
+    return PAGE_FORMATS[pages]
+
+
 class GrowingLists(_OnStreams):
     """Page lists that grow behind their retained tokens: the plan, counts and workspace of tg_append_rope
     and tg_decode_grown, over pages of either format ("bf16", or "e2m1": 4 bits).  order int32 [H] or [L][H] and
@@ -531,10 +539,8 @@ class GrowingLists(_OnStreams):
     used and dropped as a PrefillPass."""
 
     def __init__(self, H_q, H_p, P, d, order, ntok, reserve, pages="bf16", k_unit=1.0, v_unit=1.0, n_cta=None, device="cuda"):
-        if pages not in PAGE_FORMATS:
-            raise ValueError(f"pages={pages!r} (one of {sorted(PAGE_FORMATS)})")
+        self.format, self.k_unit, self.v_unit = _page_format(pages, reserve), float(k_unit), float(v_unit)
         self.device = torch.device(device)
-        self.format, self.k_unit, self.v_unit = PAGE_FORMATS[pages], float(k_unit), float(v_unit)
         ntok = np.asarray(ntok, np.int32)
         ntok = ntok[None] if ntok.ndim == 2 else ntok
         order = np.asarray(order, np.int32)
@@ -566,6 +572,8 @@ class GrowingLists(_OnStreams):
     def append(self, layer, qkv, cos_sin, q, pool, pool_pages, pt_off, pt_ids, cu_q=None, origin=None, positions=None,
                axis_of=None, q_weight=None, k_weight=None, eps=1e-6, pairs=False, K=None, V=None, start=None, stream=None):
         """One layer's new tokens (tg_append_rope): one for each request, or those of cu_q."""
+        if cu_q is None and q.size(0) < self.batch:
+            raise ValueError(f"q has {q.size(0)} tokens of {self.batch} requests")
         tg_append_rope(qkv, self.one_each if cu_q is None else cu_q, cos_sin, q, pool, pool_pages, self.order[layer],
                        self.ntok[layer], self.added, self.reserve, pt_off, pt_ids, self.H_p, self.P, fmt=self.format,
                        k_unit=self.k_unit, v_unit=self.v_unit, q_weight=q_weight, k_weight=k_weight, eps=eps, pairs=pairs,
@@ -612,16 +620,16 @@ class GrowingCache(RaggedCache):
 
     def __init__(self, L, batch, H, H_q, d, P, H_p, alpha, Bhat, N, reserve, pages="bf16", k_unit=1.0, v_unit=1.0,
                  cluster=False, n_cta=None, device="cuda", allocator=None):
-        self.reserve = int(reserve)
+        self.reserve, self.four = int(reserve), _page_format(pages, reserve) == PAGES_E2M1  # refused before pages are taken
         super().__init__(L, batch, H, H_q, d, P, H_p, alpha, Bhat, N, cluster=cluster, n_cta=n_cta, device=device,
                          alloc_pool=False, allocator=allocator)
+        page = tg_page_bytes(PAGE_FORMATS[pages], H_p, P, d)
+        kind = torch.uint8 if self.four else torch.bfloat16
+        self.pool = torch.empty(max(self.n_pages, 1) * page // kind.itemsize, dtype=kind, device=self.device)
+        # after the pool: the uploads wait for what the current stream still has to do with its memory
         self.lists = GrowingLists(H_q, H_p, P, d, self.pages["order"], self.pages["ntok"], reserve, pages=pages,
                                   k_unit=k_unit, v_unit=v_unit, n_cta=n_cta, device=device)
         self.status = self.lists.status  # one word for all calls
-        self.four = self.lists.format == PAGES_E2M1
-        page = tg_page_bytes(self.lists.format, H_p, P, d)
-        kind = torch.uint8 if self.four else torch.bfloat16
-        self.pool = torch.empty(max(self.n_pages, 1) * page // kind.itemsize, dtype=kind, device=self.device)
         self._layer_pages = None
 
     def algorithmic_bytes(self, layer=None) -> int:
@@ -639,11 +647,12 @@ class GrowingCache(RaggedCache):
         if self._layer_pages is None:
             n = self.batch * self.G
             off = self.pages["pt_off"]
+            most = max(1, *(int(off[(l + 1) * n] - off[l * n]) for l in range(self.L)))
+            pool = torch.empty(most * self.H_p * 2 * self.P * self.d, dtype=torch.bfloat16, device=self.device)
+            # last, as in PrefillPass: the retention may run on another stream than the current one
             tables = [torch.from_numpy(off[l * n:(l + 1) * n + 1] - off[l * n]).to(self.device) for l in range(self.L)]
-            most = max(int(off[(l + 1) * n] - off[l * n]) for l in range(self.L))
-            ids = torch.arange(max(most, 1), dtype=torch.int32, device=self.device)
-            pool = torch.empty(max(most, 1) * self.H_p * 2 * self.P * self.d, dtype=torch.bfloat16, device=self.device)
-            self._layer_pages = (pool, max(most, 1), tables, ids)
+            ids = torch.from_numpy(np.arange(most, dtype=np.int32)).to(self.device)
+            self._layer_pages = (pool, most, tables, ids)
         return self._layer_pages
 
     def _retention_pages(self, layer):

@@ -219,3 +219,41 @@ def test_scale_of_a_head_without_tokens(lib, cuda):
         v = qkv[0, 3].double()
         want = hold(v)[0] if pages == "e2m1" else v
         assert torch.equal(out[0, 0].double(), want) and torch.equal(out[0, 1].double(), want)
+
+
+@pytest.mark.parametrize("pages", ["bf16", "e2m1"])
+def test_retention_on_another_stream_behind_a_busy_one(lib, cuda, pages):
+    """The pages that retention goes through are made at its first call: ready for the stream that it runs on."""
+    w = synth.small(L=2, batch=2, N=300)
+    s, (K, V) = synth.scores(w, 1, cuda), synth.keys_values(w, 1, cuda)
+    rows = []
+    for busy in (False, True):
+        cache, N = _cache(w, cuda, pages, 4)
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        if busy:
+            torch.cuda._sleep(20_000_000)
+        cache.compact_layer(1, s, K, V, stream=side)
+        side.synchronize()
+        pool, n, off, ids = cache.dequantize_layer(1)
+        torch.cuda.synchronize()
+        assert lib.tg_check_status(cache.status) == 0
+        got = []
+        for b in range(w.batch):
+            for p in range(w.H):
+                l = b * cache.G + p // w.H_p
+                mine = ids[int(off[l]):int(off[l + 1])]
+                n = int(cache.pages["ntok"][1, b, int(cache.pages["order"][1, p])])
+                got += [rows_of(pool.view(-1, w.H_p, 2, w.P, w.d), mine, w.H_p, w.P, w.d, p % w.H_p, n, v) for v in (False, True)]
+        rows.append(torch.cat(got))
+    assert torch.equal(*rows) and bool(rows[0].any())
+
+
+def test_a_step_without_a_token_for_each_request_is_refused(lib, cuda):
+    from non_uniform_paged_gb300.ragged import GrowingLists
+    lists = GrowingLists(2, 1, 16, 128, [0], [[3], [4]], 2, n_cta=3, device=cuda)
+    off, ids = torch.tensor([0, 1, 2], device=cuda), torch.arange(2, dtype=torch.int32, device=cuda)
+    pool = torch.zeros((2, 1, 2, 16, 128), dtype=torch.bfloat16, device=cuda)
+    qkv = torch.randn((1, 4, 128), device=cuda).to(torch.bfloat16)
+    with pytest.raises(ValueError):
+        lists.append(0, qkv, None, torch.empty((1, 2, 128), dtype=torch.bfloat16, device=cuda), pool, 2, off, ids)
