@@ -538,9 +538,9 @@ int tg_alloc_query(const void *state, int64_t *n_free, int64_t *n_live);
  * tg_qk_norm_rope -- one layer's packed projections into queries and context rows:
  *   RMS norm of every query and key head (optional), position rotation, and the
  *   placement of the K and V rows in dense contexts, in one pass: the step ahead of
- *   tg_prefill_attn and tg_compact_topk / tg_compact_chunk.  No call puts a row into a page
- *   beside those two, so tg_decode_attn, which reads pages alone, does not see a token that is
- *   only placed; how a new token sees itself and the retained ones is said at tg_prefix_attn.
+ *   tg_prefill_attn and tg_compact_topk / tg_compact_chunk.  tg_decode_attn, which reads pages
+ *   alone, does not see a token that is only placed: tg_append_rope puts a row into a page, and how
+ *   a placed token sees itself and the retained ones is said at tg_prefix_attn.
  *   Request b owns the packed tokens [cu_q[b], cu_q[b+1]); its token cu_q[b] + i is
  *   row start[b] + i of its context.  For a query or key head x of a token:
  *     y = x / sqrt(mean(x^2) + eps) * weight          (weight NULL: y = x)
@@ -749,8 +749,8 @@ int tg_reserve_pages(int L, int batch, int H, int H_p, int P, const int32_t *hea
  *   4-bit pages: a K value is rounded to 4 bits from what float32 arithmetic gives, or, where that is too
  *   close to the border of two codes or scales to tell, from float64 arithmetic: the codes are those of the formulas
  *   (of projections below 2^59 in magnitude, whose squares' sum float32 holds).
- *   A token with added[b] < 0, added[b] + i >= reserve, a position outside [0, max_pos) (rot > 0) or a dense
- *   row outside [0, Nmax) sets TG_STATUS_BAD_INPUT and writes nothing.  A head whose list is too short
+ *   A token ahead of its request's cu_q[b] (cu_q[0] > 0, or one that descends), with added[b] < 0, added[b] + i >= reserve,
+ *   a position outside [0, max_pos) (rot > 0) or a dense row outside [0, Nmax) sets TG_STATUS_BAD_INPUT and writes nothing.  A head whose list is too short
  *   or names a page outside [0, pool_pages) sets TG_STATUS_BAD_PAGE and none of its rows is written.
  *   Rows from cu_q[batch] on are left as they are.  Two tokens never share a row unless lists share pages.
  * Launch: as tg_qk_norm_rope. */
@@ -794,13 +794,14 @@ int tg_dequant_pages(tg_stream_t stream, int batch, int H, int H_p, int P, int d
  *   the tokens that are there: with n tokens of c = ntok + reserve, [t0 n / c, t1 n / c) in float32, a
  *   partition of [0, n) into pieces as even as the plan's.
  * Arguments: plan, q, pt_off, pt_ids, scale, workspace, out, lse, dev_status, cta_time as tg_decode_attn, q and
- *   out 16-byte aligned; format and pool (16-byte aligned; tokens of all its heads fit int32); ntok int32 [batch][H] of this layer; added int32 [batch] (NULL: zeros);
- *   plus >= 0; k_unit, v_unit as tg_append_rope.  added[b] + plus outside [0, reserve] sets
- *   TG_STATUS_BAD_INPUT and counts as the nearer end.  Rows behind the last token may hold anything.
+ *   out 16-byte aligned; format and pool (16-byte aligned; tokens of all its heads fit int32); ntok int32
+ *   [batch][H] of this layer; added int32 [batch] (NULL: zeros); plus >= 0; k_unit, v_unit as tg_append_rope.
+ *   added[b] + plus outside [0, reserve] sets TG_STATUS_BAD_INPUT and counts as the nearer end.  Rows behind the last token may hold anything.
  *   A list too short for its tokens, or a page id outside the pool, sets TG_STATUS_BAD_PAGE (out is then
  *   unspecified).  out = 0 and lse = -inf for a head without tokens.
- *   bf16 pages: arithmetic as tg_decode_attn, but that the sum of the weights is of the unrounded ones.  4-bit pages: products of f16 (codes times scales are exact
- *   in it, q is scaled by a power of two into its range, weights are rounded to it) with float32 sums.
+ *   bf16 pages: arithmetic as tg_decode_attn, but that the sum of the weights is of the unrounded ones.
+ *   4-bit pages: products of f16 (codes times scales are exact in it, q is scaled by a power of two into its
+ *   range, weights are rounded to it) with float32 sums.
  * Launch: programmatic dependent launch; waits for the kernel before it before it reads anything but the
  *   plan, and lets the next kernel start after that. */
 int tg_decode_grown(tg_stream_t stream, const void *plan_host, const void *plan_dev, int layer, int format,
