@@ -563,11 +563,12 @@ class GrowingLists(_OnStreams):
         self.added = torch.zeros(self.batch, dtype=torch.int32, device=self.device)
         # last, as in PrefillPass: the uploads wait for the current stream
         self.plan = DecodePlan(plan, torch.from_numpy(plan).to(self.device))
-        self.order = [torch.from_numpy(o).to(self.device) for o in order]
-        self.ntok = [torch.from_numpy(n).to(self.device) for n in ntok]
-        self.one_each = torch.from_numpy(np.arange(self.batch + 1, dtype=np.int32)).to(self.device)
+        tables = torch.from_numpy(np.concatenate([order.reshape(-1), ntok.reshape(-1),
+                                                  np.arange(self.batch + 1, dtype=np.int32)])).to(self.device)
+        placed, counts, self.one_each = tables.split([order.size, ntok.size, self.batch + 1])
+        self.order, self.ntok = placed.view(L, H).unbind(), counts.view(L, self.batch, H).unbind()
         self.scale = 1.0 / math.sqrt(d)
-        self._own(self.plan.plan_dev, self.workspace, self.status, self.added, self.one_each, *self.order, *self.ntok)
+        self._own(self.plan.plan_dev, self.workspace, self.status, self.added, tables)
 
     def append(self, layer, qkv, cos_sin, q, pool, pool_pages, pt_off, pt_ids, cu_q=None, origin=None, positions=None,
                axis_of=None, q_weight=None, k_weight=None, eps=1e-6, pairs=False, K=None, V=None, start=None, stream=None):
