@@ -5,13 +5,13 @@
 // ntok[b][h] + added[b] + i of the head's page list.  Every projection is read once and written once: bound by
 // memory, and for a decode step by the chain request -> its tokens' count -> page id -> store.
 //
-// A block is a warp: one token, or one batch of a token's heads where there are few tokens.  A head is d / 8
+// A block is a warp: a share of a token's batches of heads (which share: tg_append_rope below).  A head is d / 8
 // lanes; a lane's 8 values are 4 first and the 4 second ones of its pairs (i, i + rot/2), so that the rotation
 // exchanges nothing, or 8 consecutive ones (pairs (2i, 2i + 1), values behind rot, V).  Where the heads' rows lie is
 // looked up once, for 32 places of the groups at a time, each by a lane; K and V lie side by side.  Queries, keys and
 // values have a loop each; a batch of queries (a unit of 4-bit keys) is on its way while the one before it is worked
 // on.  15000 tokens of 16 + 8 + 8 heads of 128 into bf16 pages, 372 MB: 68 us, 5.5 TB/s (71.5 with one loop for all
-// three; 70.1 with 24 blocks to an SM and 72.9 with 20, for 28; 72.6 with batches of 2 loads for 4).
+// three; 70.1 with 24 blocks to an SM and 72.9 with 20, for 28; 72.6 with batches of 2 loads for 4; one warp a token).
 //
 // 4-bit pages.  A head's rotated values go through shared memory, so that a lane has 8 consecutive ones and a pair
 // of lanes a block of 16.  float32 leaves a value z = f (u c x_u - v s x_v) off by at most 15 2^-24 t,
@@ -29,6 +29,7 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 namespace {
@@ -36,6 +37,8 @@ namespace {
 using namespace tgk;
 
 constexpr int kSteps = 4;  // loads of a batch: heads at d = 256, pairs of heads at d = 128
+constexpr int kBlocksPerSm = 28, kBlocksPerSm4 = 20;  // of 72 and, for 4-bit pages, 96 registers
+constexpr int kMaxParts = 512;                        // warps of a token
 
 struct AppendArgs {
   const int32_t *cu_q, *positions, *origin, *head_order, *ntok, *added, *pt_ids, *start;
@@ -48,7 +51,7 @@ struct AppendArgs {
   int32_t *status;
   int batch, H_q, H, H_p, G, P, Nmax, rot, max_pos, axes, reserve;
   int q_batches, kv_batches;  // batches of the query heads, and of the key (and of the value) heads
-  int parts;                  // warps of a token: 1, or one for each of its batches
+  unsigned parts;             // warps of a token, each with an even share of its batches
   float eps, k_unit, v_unit, k_to_unit, v_to_unit;  // to: the reciprocals
   uint32_t axis[8];  // two bits for each pair
 };
@@ -69,16 +72,18 @@ __device__ __forceinline__ float sticky(double v) {
 }
 
 template <int D, bool PAIRS, bool E2M1>
-__global__ void __launch_bounds__(32, E2M1 ? 20 : 28) append_rope_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(32, E2M1 ? kBlocksPerSm4 : kBlocksPerSm) append_rope_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int LANES = D / 8, PER = 32 / LANES;  // lanes of a head, heads side by side
   constexpr int BATCH = kSteps * PER;             // heads of a batch: divides 32
   __shared__ __align__(16) float zs[E2M1 ? PER * D : 1], ts[E2M1 ? PER * D / 4 : 1];
   __shared__ __align__(16) double zd[E2M1 ? PER * D : 1];
   const int lane = threadIdx.x, sub = lane % LANES, side = lane / LANES;
-  const int t = a.parts == 1 ? blockIdx.x : blockIdx.x / a.parts, part = blockIdx.x - t * a.parts;
+  const int t = (int)(blockIdx.x / a.parts);
+  const unsigned part = blockIdx.x - t * a.parts;
   // the token's batches [first, last) of this warp: queries, then keys, then values
   const int k_first = a.q_batches, v_first = k_first + a.kv_batches, all = v_first + a.kv_batches;
-  const int first = part, last = a.parts == 1 ? all : part + 1;
+  // (the product fits: at most 2^24 heads, and kMaxParts)
+  const int first = (unsigned)all * part / a.parts, last = (unsigned)all * (part + 1) / a.parts;
   // the two groups of this lane in a query or key head; of a value head they are 8 consecutive values
   const bool turned = sub * 8 < a.rot;
   const int ga = !PAIRS && turned ? sub * 4 : sub * 8, gb = !PAIRS && turned ? sub * 4 + a.rot / 2 : sub * 8 + 4;
@@ -539,12 +544,29 @@ extern "C" int tg_append_rope(tg_stream_t stream, int batch, int T, int H_q, int
   a.status = dev_status, a.batch = batch, a.H_q = H_q, a.H = H, a.H_p = H_p, a.G = H / H_p, a.P = P, a.Nmax = Nmax, a.rot = rot;
   a.max_pos = max_pos, a.axes = axes, a.reserve = reserve, a.eps = eps, a.k_unit = k_unit, a.v_unit = v_unit;
   if (e2m1) a.k_to_unit = 1.f / k_unit, a.v_to_unit = 1.f / v_unit;  // exact
-  // a warp a token, or, below 2048 tokens, one for each of its batches, as in tg_qk_norm_rope
+  // As many warps a token as let all of them be on the card at once, up to one for each of its batches.  More tokens than
+  // that: two for bf16 pages, which ends the call more evenly, one for 4-bit pages, where each more looks up places and
+  // weights anew beside arithmetic that already counts.  us of 1, 2, 3 and all (6 or 8) warps a token, bf16: 512 tokens
+  // of 32 + 8 + 8 heads of 128: 9.1, 6.4, 5.7, 5.8; 1024: 10.7, 8.1, 7.2, 9.6; 2048: 14.9, 12.6, 13.8, 15.6; 9000: 46.3, 43.7,
+  // 45.0, 54.7; 9000 of 16 + 8 + 8 heads of 256: 69.8, 63.8, 63.9, 72.3.  4 bits, of those: 512: 21.7, 17.6, 15.0, 14.1;
+  // 1024: 23.4, 19.7, 15.9, 18.8; 3000: 31.3, 35.5, 36.9, 42.8; 9000: 78.1, 92.1, 102.4, 113.0.
   const int per = kSteps * (d == 128 ? 2 : 1);
   a.q_batches = (H_q + per - 1) / per;
   a.kv_batches = (H + per - 1) / per;
-  a.parts = T < 2048 ? a.q_batches + 2 * a.kv_batches : 1;
-  const int64_t blocks = (int64_t)T * a.parts;
+  const int all = a.q_batches + 2 * a.kv_batches;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return fail(TG_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+  // (4 bits: one an SM more than are there at once, for 1024 tokens; a few warps behind the others cost less than longer shares)
+  const int fit = sms * (e2m1 ? kBlocksPerSm4 + 1 : kBlocksPerSm) / T;
+  int parts = std::min({std::max(fit, e2m1 ? 1 : 2), all, kMaxParts});
+  if (!e2m1) {  // batches weigh alike: no more warps than the longest share needs (4 bits: keys weigh most)
+    const int share = (all + parts - 1) / parts;
+    parts = (all + share - 1) / share;
+  }
+  a.parts = parts;
+  const int64_t blocks = (int64_t)T * parts;
   if (blocks > INT32_MAX) return fail(TG_ERR_SHAPE, "%s: T=%d with %lld heads", fn, T, (long long)heads);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -556,7 +578,7 @@ extern "C" int tg_append_rope(tg_stream_t stream, int batch, int T, int H_q, int
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const bool pairs = flags & TG_ROPE_PAIRS;
-  const cudaError_t e = d == 128 ? launch<128>(cfg, pairs, e2m1, a) : launch<256>(cfg, pairs, e2m1, a);
+  e = d == 128 ? launch<128>(cfg, pairs, e2m1, a) : launch<256>(cfg, pairs, e2m1, a);
   if (e != cudaSuccess) return fail(TG_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
   return tgi::ok();
 }

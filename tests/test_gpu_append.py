@@ -65,6 +65,10 @@ class Case:
         torch.cuda.synchronize()
         return int(self.status)
 
+    def call_and_verify(self, lib):
+        assert self.call(lib) == 0
+        self.verify()
+
     def _rows(self, b, at, n):
         """Table rows [n][rot/2][2] of request b's tokens."""
         if not self.rot:
@@ -191,6 +195,14 @@ def test_more_tokens_than_one_warp_each_covers(lib, cuda, fmt):
         c = Case(cuda, fmt, [T], [[17] * H], H_q, H, d, seed=T, max_pos=3000)
         assert c.call(lib) == 0
         c.verify()
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("T", [1, 270, 540, 1100, 1700, 2300, 4500])
+def test_every_share_of_a_token_between_warps(lib, cuda, fmt, T):
+    """From a warp for each batch of heads down to one or two for a token, over uneven numbers of batches."""
+    lens = [T - T // 3, T // 3]
+    Case(cuda, fmt, lens, [[1] * 5, [4] * 5], 35, 5, 128, rot=48, max_pos=4000, seed=T).call_and_verify(lib)
 
 
 def test_units(lib, cuda):
