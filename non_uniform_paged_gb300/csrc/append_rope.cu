@@ -50,7 +50,8 @@ struct AppendArgs {
   uint16_t *q, *K, *V;
   int32_t *status;
   int batch, H_q, H, H_p, G, P, Nmax, rot, max_pos, axes, reserve;
-  int q_batches, kv_batches;  // batches of the query heads, and of the key (and of the value) heads
+  // shares of work: batches of the query heads, of the key heads (4-bit pages: units, heads side by side) and of the value heads
+  int q_batches, k_batches, v_batches;
   unsigned parts;             // warps of a token, each with an even share of its batches
   float eps, k_unit, v_unit, k_to_unit, v_to_unit;  // to: the reciprocals
   uint32_t axis[8];  // two bits for each pair
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(32, E2M1 ? kBlocksPerSm4 : kBlocksPerSm) appen
   const int t = (int)(blockIdx.x / a.parts);
   const unsigned part = blockIdx.x - t * a.parts;
   // the token's batches [first, last) of this warp: queries, then keys, then values
-  const int k_first = a.q_batches, v_first = k_first + a.kv_batches, all = v_first + a.kv_batches;
+  const int k_first = a.q_batches, v_first = k_first + a.k_batches, all = v_first + a.v_batches;
   // (the product fits: at most 2^24 heads, and kMaxParts)
   const int first = (unsigned)all * part / a.parts, last = (unsigned)all * (part + 1) / a.parts;
   // the two groups of this lane in a query or key head; of a value head they are 8 consecutive values
@@ -130,7 +131,8 @@ __global__ void __launch_bounds__(32, E2M1 ? kBlocksPerSm4 : kBlocksPerSm) appen
   };
   bool bad = i < 0 || grown < 0 || (int64_t)grown + i >= a.reserve || (a.K && (row < 0 || row >= a.Nmax));
   // (a token that is refused below reports nothing of its pages)
-  if (last > k_first) places(first <= k_first ? 0 : ((first - (first >= v_first ? v_first : k_first)) * BATCH) & ~31, bad);
+  if (last > k_first)
+    places(first <= k_first ? 0 : first >= v_first ? (first - v_first) * BATCH & ~31 : (first - k_first) * (E2M1 ? PER : BATCH) & ~31, bad);
   // this lane's four pairs
   float c[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
   if (a.rot > 0) {
@@ -293,20 +295,19 @@ __global__ void __launch_bounds__(32, E2M1 ? kBlocksPerSm4 : kBlocksPerSm) appen
   }
   // ---- keys of 4-bit pages: one unit in a turn of the loop (what unrolling it adds to the code costs more than it hides)
   if (E2M1) {
-    const int end = min(last, v_first) - k_first;
+    const int end = min(last, v_first) - k_first;  // units
     auto load = [&](Head8 &x, int u) {
       const int h = __shfl_sync(0xffffffffu, head, (u * PER + side) & 31);
       if (h >= 0) load_turned(x, src + a.H_q * D, h);
     };
     if (first < v_first && last > k_first) weigh(a.kw);
-    const int u_end = min(end * kSteps, (a.H + PER - 1) / PER);
     Head8 nx = {};
     int loaded = -1;  // the unit in nx
-    for (int u = max(first - k_first, 0) * kSteps; u < u_end; ++u) {
+    for (int u = max(first - k_first, 0); u < end; ++u) {
       if ((u * PER & ~31) != p0) places(u * PER & ~31, false);
       if (loaded != u) load(nx, u);
       const Head8 in = nx;
-      if (u + 1 < u_end && ((u + 1) * PER & ~31) == p0) load(nx, loaded = u + 1);  // on its way meanwhile
+      if (u + 1 < end && ((u + 1) * PER & ~31) == p0) load(nx, loaded = u + 1);  // on its way meanwhile
       const int to = __shfl_sync(0xffffffffu, rows, (u * PER + side) & 31);
       const int h = __shfl_sync(0xffffffffu, head, (u * PER + side) & 31);
       const bool w = a.kw != nullptr;
@@ -544,24 +545,25 @@ extern "C" int tg_append_rope(tg_stream_t stream, int batch, int T, int H_q, int
   a.status = dev_status, a.batch = batch, a.H_q = H_q, a.H = H, a.H_p = H_p, a.G = H / H_p, a.P = P, a.Nmax = Nmax, a.rot = rot;
   a.max_pos = max_pos, a.axes = axes, a.reserve = reserve, a.eps = eps, a.k_unit = k_unit, a.v_unit = v_unit;
   if (e2m1) a.k_to_unit = 1.f / k_unit, a.v_to_unit = 1.f / v_unit;  // exact
-  // As many warps a token as let all of them be on the card at once, up to one for each of its batches.  More tokens than
-  // that: two for bf16 pages, which ends the call more evenly, one for 4-bit pages, where each more looks up places and
-  // weights anew beside arithmetic that already counts.  us of 1, 2, 3 and all (6 or 8) warps a token, bf16: 512 tokens
-  // of 32 + 8 + 8 heads of 128: 9.1, 6.4, 5.7, 5.8; 1024: 10.7, 8.1, 7.2, 9.6; 2048: 14.9, 12.6, 13.8, 15.6; 9000: 46.3, 43.7,
-  // 45.0, 54.7; 9000 of 16 + 8 + 8 heads of 256: 69.8, 63.8, 63.9, 72.3.  4 bits, of those: 512: 21.7, 17.6, 15.0, 14.1;
-  // 1024: 23.4, 19.7, 15.9, 18.8; 3000: 31.3, 35.5, 36.9, 42.8; 9000: 78.1, 92.1, 102.4, 113.0.
+  // As many warps a token as let about all of them be on the card at once, up to one for each of its batches.  More tokens
+  // than that: two for bf16 pages, which ends the call more evenly, one for 4-bit pages, where each more looks up places
+  // and weights anew beside arithmetic that already counts.  us of 1, 2, 3, 5 (4 bits) and all warps a token, bf16: 512
+  // tokens of 32 + 8 + 8 heads of 128: 9.1, 6.4, 5.7, 5.8; 1024: 10.7, 8.1, 7.2, 9.6; 2048: 14.9, 12.6, 13.8, 15.6; 9000:
+  // 46.3, 43.7, 45.0, 54.7; 9000 of 16 + 8 + 8 heads of 256: 69.8, 63.8, 63.9, 72.3.  4 bits, of those: 16: 14.8, 9.6, 8.2, 6.9,
+  // 5.0; 512: 21.0, 15.4, 13.1, 11.4, 13.4; 1024: 24.5, 18.1, 16.1, 18.2, 20.9; 3000: 31.3, 33.9, 35.2, 43.1, 49.9.
   const int per = kSteps * (d == 128 ? 2 : 1);
   a.q_batches = (H_q + per - 1) / per;
-  a.kv_batches = (H + per - 1) / per;
-  const int all = a.q_batches + 2 * a.kv_batches;
+  a.v_batches = (H + per - 1) / per;
+  a.k_batches = e2m1 ? (H + per / kSteps - 1) / (per / kSteps) : a.v_batches;
+  const int all = a.q_batches + a.k_batches + a.v_batches;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return fail(TG_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
-  // (4 bits: one an SM more than are there at once, for 1024 tokens; a few warps behind the others cost less than longer shares)
-  const int fit = sms * (e2m1 ? kBlocksPerSm4 + 1 : kBlocksPerSm) / T;
+  // (4 bits: the number nearest to 18 of the 20 an SM: a few warps behind the others cost less than longer shares)
+  const int fit = e2m1 ? (sms * (kBlocksPerSm4 - 2) + T / 2) / T : sms * kBlocksPerSm / T;
   int parts = std::min({std::max(fit, e2m1 ? 1 : 2), all, kMaxParts});
-  if (!e2m1) {  // batches weigh alike: no more warps than the longest share needs (4 bits: keys weigh most)
+  if (!e2m1) {  // batches weigh alike: no more warps than the longest share needs
     const int share = (all + parts - 1) / parts;
     parts = (all + share - 1) / share;
   }
