@@ -99,6 +99,10 @@ class RaggedCache:
         nt = self.pages["ntok"] if layer is None else self.pages["ntok"][layer]
         return int(nt.sum(dtype=np.int64))
 
+    def held_tokens(self) -> np.ndarray:
+        """Tokens of each head, int32 [L][batch][H]."""
+        return self.pages["ntok"]
+
     def algorithmic_bytes(self, layer=None) -> int:
         """Bytes a decode step must move: retained K+V rows, page-table ids, q and out."""
         layers = range(self.L) if layer is None else [layer]
@@ -503,8 +507,9 @@ class SharedPrefix(_OnStreams):
 
     @classmethod
     def of_cache(cls, cache, req_off, n_cta=None):
-        """The prefixes held by a RaggedCache, its request r for group r."""
-        return cls(cache.H_q, cache.H_p, cache.P, cache.d, req_off, cache.pages["order"], cache.pages["ntok"],
+        """The prefixes held by a RaggedCache, its request r for group r (of a GrowingCache with the tokens that
+        advance() has counted)."""
+        return cls(cache.H_q, cache.H_p, cache.P, cache.d, req_off, cache.pages["order"], cache.held_tokens(),
                    n_cta=n_cta, device=cache.device)
 
     def attend(self, layer, q, pool, pool_pages, pt_off, pt_ids, out, lse=None, own_out=None, own_lse=None, scale=None,
@@ -637,6 +642,10 @@ class GrowingCache(RaggedCache):
         """As RaggedCache's, before any token is appended: 4-bit pages hold 9/16 of a byte a value."""
         total = super().algorithmic_bytes(layer)
         return total - self.retained_tokens(layer) * 2 * self.d * 23 // 16 if self.four else total
+
+    def held_tokens(self) -> np.ndarray:
+        """Retained tokens and those that advance() has counted (waits for the current stream)."""
+        return self.pages["ntok"] + self.lists.added.cpu().numpy().clip(0, self.reserve)[:, None]
 
     def _build_pages(self, pages):
         """The same heads' lists with the reserve."""

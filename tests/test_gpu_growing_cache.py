@@ -257,3 +257,39 @@ def test_a_step_without_a_token_for_each_request_is_refused(lib, cuda):
     qkv = torch.randn((1, 4, 128), device=cuda).to(torch.bfloat16)
     with pytest.raises(ValueError):
         lists.append(0, qkv, None, torch.empty((1, 2, 128), dtype=torch.bfloat16, device=cuda), pool, 2, off, ids)
+
+
+@pytest.mark.parametrize("pages", ["bf16", "e2m1"])
+def test_a_prefix_of_a_cache_that_has_grown_holds_what_was_appended(lib, cuda, pages):
+    """SharedPrefix over the cache after steps of uneven counts: every token that advance() counted, and none behind."""
+    from non_uniform_paged_gb300.ragged import SharedPrefix
+    w = synth.small(L=2, batch=3, N=300, H=4, H_q=8, H_p=2)
+    cache, N = _cache(w, cuda, pages, 40)
+    g, layer, steps = 2, 1, [18, 0, 5]
+    for l in range(2):
+        cache.compact_layer(l, synth.scores(w, l, cuda), *synth.keys_values(w, l, cuda))
+    gen = torch.Generator(device=cuda).manual_seed(3)
+    T = sum(steps) + 6
+    cu = torch.tensor(np.concatenate([[0], np.cumsum([n + 2 for n in steps])]), dtype=torch.int32, device=cuda)
+    qkv = torch.randn((T, 16, w.d), generator=gen, device=cuda).to(torch.bfloat16)
+    q = torch.empty((T, 8, w.d), dtype=torch.bfloat16, device=cuda)
+    cache.append_layer(layer, qkv, None, q, cu_q=cu)  # two tokens of each request are not counted
+    cache.advance(torch.tensor(steps, dtype=torch.int32, device=cuda))
+    want = cache.pages["ntok"] + np.asarray(steps)[None, :, None]
+    assert np.array_equal(cache.held_tokens(), want)
+    shared = SharedPrefix.of_cache(cache, [0, 1, 2, 3])
+    pool, n, off, ids = cache.dequantize_layer(layer)
+    q = torch.randn((3, 8, w.d), generator=gen, device=cuda).to(torch.bfloat16)
+    out, lse = torch.empty_like(q), torch.empty((3, 8), device=cuda)
+    shared.attend(layer, q, pool, n, off, ids, out, lse)
+    torch.cuda.synchronize()
+    assert lib.tg_check_status(shared.status) == 0 and lib.tg_check_status(cache.status) == 0
+    order = cache.pages["order"][layer]
+    for b in range(3):
+        for p in range(4):
+            h, l = int(order[p]), b * cache.G + p // 2
+            mine = ids[int(off[l]):int(off[l + 1])]
+            k, v = (rows_of(pool.view(-1, 2, 2, w.P, w.d), mine, 2, w.P, w.d, p % 2, int(want[layer, b, h]), i) for i in (False, True))
+            o, le, t, lt = attend64(q[b, h * g:(h + 1) * g], k, v, cache.scale, False)
+            assert bool(((out[b, h * g:(h + 1) * g].double() - o).abs() <= t).all())
+            assert bool(((lse[b, h * g:(h + 1) * g].double() - le).abs() <= lt).all())
