@@ -622,16 +622,19 @@ class GrowingCache(RaggedCache):
     format.  compact_layer and compact_layer_chunked retain into it; a decode step is append_layer and
     decode_layer of each layer, then advance().  With pages="e2m1" retention goes through bf16 pages of
     one layer, which the next one uses again; dequantize_layer gives a layer's tokens as bf16 pages, for
-    SharedPrefix and the like.  The base class' own decode plan (`plan`) covers the retained tokens alone."""
+    SharedPrefix and the like.  The base class' own decode plan (`plan`) covers the retained tokens alone.
+    Caches that share an allocator may share a pool (alloc_pool=False, then pool is set: n_pages of
+    tg_page_bytes).  One stream at a time; to be kept until its calls have run."""
 
     def __init__(self, L, batch, H, H_q, d, P, H_p, alpha, Bhat, N, reserve, pages="bf16", k_unit=1.0, v_unit=1.0,
-                 cluster=False, n_cta=None, device="cuda", allocator=None):
+                 cluster=False, n_cta=None, device="cuda", alloc_pool=True, allocator=None):
         self.reserve, self.four = int(reserve), _page_format(pages, reserve) == PAGES_E2M1  # refused before pages are taken
         super().__init__(L, batch, H, H_q, d, P, H_p, alpha, Bhat, N, cluster=cluster, n_cta=n_cta, device=device,
                          alloc_pool=False, allocator=allocator)
-        page = tg_page_bytes(PAGE_FORMATS[pages], H_p, P, d)
-        kind = torch.uint8 if self.four else torch.bfloat16
-        self.pool = torch.empty(max(self.n_pages, 1) * page // kind.itemsize, dtype=kind, device=self.device)
+        if alloc_pool:
+            page = tg_page_bytes(PAGE_FORMATS[pages], H_p, P, d)
+            kind = torch.uint8 if self.four else torch.bfloat16
+            self.pool = torch.empty(max(self.n_pages, 1) * page // kind.itemsize, dtype=kind, device=self.device)
         # after the pool: the uploads wait for what the current stream still has to do with its memory
         self.lists = GrowingLists(H_q, H_p, P, d, self.pages["order"], self.pages["ntok"], reserve, pages=pages,
                                   k_unit=k_unit, v_unit=v_unit, n_cta=n_cta, device=device)

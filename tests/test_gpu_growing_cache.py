@@ -293,3 +293,42 @@ def test_a_prefix_of_a_cache_that_has_grown_holds_what_was_appended(lib, cuda, p
             o, le, t, lt = attend64(q[b, h * g:(h + 1) * g], k, v, cache.scale, False)
             assert bool(((out[b, h * g:(h + 1) * g].double() - o).abs() <= t).all())
             assert bool(((lse[b, h * g:(h + 1) * g].double() - le).abs() <= lt).all())
+
+
+@pytest.mark.parametrize("pages", ["bf16", "e2m1"])
+def test_caches_of_one_allocator_share_a_pool(lib, cuda, pages):
+    """Two caches whose pages lie between each other's in one pool: each step's bits are those of caches apart."""
+    from non_uniform_paged_gb300.ragged import GrowingCache
+    w = synth.small(L=2, batch=2, N=200)
+    N, Bhat, g = synth.contexts(w), synth.budgets_hat(w), torch.Generator(device=cuda).manual_seed(9)
+
+    def make(allocator, pool=True):
+        return GrowingCache(w.L, w.batch, w.H, w.H_q, w.d, w.P, w.H_p, w.alpha, Bhat, N, 6, pages=pages, n_cta=16, device=cuda,
+                            alloc_pool=pool, allocator=allocator)
+    apart, alloc = [make(None), make(None)], lib.PageAllocator(3000)
+    shared = [make(alloc, False), make(alloc, False)]
+    page = lib.tg_page_bytes(shared[0].lists.format, w.H_p, w.P, w.d)
+    pool = torch.empty(3000 * page, dtype=torch.uint8, device=cuda)
+    for c in shared:
+        assert c.pool is None and c.n_pages == 3000
+        c.pool = pool if pages == "e2m1" else pool.view(torch.bfloat16)
+    data = [(synth.scores(w, l, cuda), *synth.keys_values(w, l, cuda)) for l in range(2)]
+    steps = torch.randn((2, 3, 2, w.batch, w.H_q + 2 * w.H, w.d), generator=g, device=cuda).to(torch.bfloat16)  # cache, step, layer
+    outs = []
+    for caches in (apart, shared):
+        out = torch.zeros((2, 3, 2, w.batch, w.H_q, w.d), dtype=torch.bfloat16, device=cuda)
+        q = torch.empty((w.batch, w.H_q, w.d), dtype=torch.bfloat16, device=cuda)
+        for i, c in enumerate(caches):
+            for l in range(2):
+                s, K, V = data[(l + i) % 2]
+                c.compact_layer(l, s, K, V)
+        for n in range(3):
+            for i, c in enumerate(caches):
+                for l in range(2):
+                    c.append_layer(l, steps[i, n, l], None, q)
+                    c.decode_layer(l, q, out[i, n, l])
+                c.advance()
+        torch.cuda.synchronize()
+        assert all(lib.tg_check_status(c.status) == 0 for c in caches)
+        outs.append(out)
+    assert torch.equal(*outs) and not torch.equal(outs[0][0], outs[0][1])
