@@ -537,7 +537,8 @@ class GrowingLists(_OnStreams):
     """Page lists that grow behind their retained tokens: the plan, counts and workspace of tg_append_rope
     and tg_decode_grown, over pages of either format ("bf16", or "e2m1": 4 bits).  order int32 [H] or [L][H] and
     ntok int32 [batch][H] or [L][batch][H] as tg_build_pages gives them; reserve: the tokens that a head may
-    get behind them.  k_unit, v_unit: of 4-bit pages (tg.h).
+    get behind them (the work is shared out as if they were there: no more than will be used).  k_unit, v_unit: of 4-bit
+    pages (tg.h).
 
     A decode step is append and attend of each layer, then advance(); added (int32 [batch], on the device)
     counts the tokens appended in earlier steps, so that a captured step may be replayed.  One stream at a time;
