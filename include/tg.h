@@ -799,7 +799,8 @@ int tg_dequant_pages(tg_stream_t stream, int batch, int H, int H_p, int P, int d
  *   added[b] + plus outside [0, reserve] sets TG_STATUS_BAD_INPUT and counts as the nearer end.  Rows behind the last token may hold anything.
  *   A list too short for its tokens, or a page id outside the pool, sets TG_STATUS_BAD_PAGE (out is then
  *   unspecified).  out = 0 and lse = -inf for a head without tokens.
- *   bf16 pages: arithmetic as tg_decode_attn, but that the sum of the weights is of the unrounded ones.
+ *   bf16 pages: arithmetic as tg_decode_attn, but that the weights are two bf16 terms (off by less than 2^-14 of themselves)
+ *   and their sum is of the whole ones.
  *   4-bit pages: products of f16 (codes times scales are exact in it, q is scaled by a power of two into its
  *   range, weights are rounded to it) with float32 sums.
  * Launch: programmatic dependent launch; waits for the kernel before it before it reads anything but the

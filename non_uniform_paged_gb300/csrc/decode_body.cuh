@@ -557,10 +557,24 @@ __device__ __forceinline__ void decode_body(const CUtensorMap *pool_map_p, const
           const float p0 = ex2(z0 - mn0), p1 = ex2(z1 - mn1), p2 = ex2(z2 - mn0), p3 = ex2(z3 - mn1);
           // the weights go to the P.V product rounded to bf16; the row sums add the same
           // rounded weights, so the output is a weighted mean of V under one set of weights
-          const uint32_t pk01 = pack_bf16x2(p0, p1), pk23 = pack_bf16x2(p2, p3);
-          // (a grown run adds the unrounded ones: of few tokens their roundings do not average out of the lse)
-          l0 = l0 * c0 + (GROWN ? p0 + p2 : __uint_as_float(pk01 << 16) + __uint_as_float(pk23 << 16));
-          l1 = l1 * c1 + (GROWN ? p1 + p3 : __uint_as_float(pk01 & 0xffff0000u) + __uint_as_float(pk23 & 0xffff0000u));
+          uint32_t pk01, pk23, rest0 = 0, rest1 = 0;
+          if (!GROWN) {
+            pk01 = pack_bf16x2(p0, p1), pk23 = pack_bf16x2(p2, p3);
+            l0 = l0 * c0 + __uint_as_float(pk01 << 16) + __uint_as_float(pk23 << 16);
+            l1 = l1 * c1 + __uint_as_float(pk01 & 0xffff0000u) + __uint_as_float(pk23 & 0xffff0000u);
+          } else {
+            // A grown run's weights are two bf16 terms, the first cut off, and its sums add the whole ones: of few tokens one
+            // rounding averages out neither of the output nor of the lse.  The rest is rounded, at most 2^-7 2^-8 of the
+            // weight, and 2^-20 of the weight larger than it is, so that it is above 0: 0 times an infinite value is none.
+            auto top = [](float p) { return __uint_as_float(__float_as_uint(p) & 0xffff0000u); };
+            auto rest = [&](float p) { return fmaf(p, 0x1p-20f, p - top(p)); };
+            pk01 = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+            pk23 = __byte_perm(__float_as_uint(p2), __float_as_uint(p3), 0x7632);
+            rest0 = movmatrix_t(pack_bf16x2(rest(p0), rest(p1)));
+            rest1 = movmatrix_t(pack_bf16x2(rest(p2), rest(p3)));
+            l0 = l0 * c0 + (p0 + p2);
+            l1 = l1 * c1 + (p1 + p3);
+          }
           m0 = mn0;
           m1 = mn1;
           const uint32_t b0 = movmatrix_t(pk01);
@@ -580,6 +594,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap *pool_map_p, const
             ldsm_x4_t(vbase + swz((lane & 7) + (lane >> 4) * 8, mb * 16 + ((lane >> 3) & 1) * 8), a0, a1, a2, a3);
             if (GROWN && part) a0 &= keep0, a1 &= keep0, a2 &= keep1, a3 &= keep1;
             mma_16816(o[mb], a0, a1, a2, a3, b0, b1);
+            if (GROWN) mma_16816(o[mb], a0, a1, a2, a3, rest0, rest1);
           }
           ++consumed;
           __syncwarp();
