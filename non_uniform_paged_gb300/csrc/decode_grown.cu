@@ -16,8 +16,8 @@
 //    which costs nothing that bf16 has but what is 2^-14 of the maximum and below.
 //  * O^T += V^T P^T: a lane takes one block of 16 values of four tokens.  A pair of tokens' codes are brought
 //    side by side in their bytes before the conversion, so that the pair of their scales multiplies them.
-//  * Weights are f16, 2^8 times the softmax's against a reference that moves only when a score passes it by 7
-//    (kWeightLog2 below): at most 2^15, and what f16 loses of a weight is below 2^-24 / 2^8 of the reference's.
+//  * Weights are f16, 2^8 times the softmax's against a maximum that moves only when a score passes it by 7
+//    (kWeightLog2 below): at most 2^15, and what f16 loses of a weight is below 2^-24 / 2^8 of the maximum's.
 // Measured: 2.7 M rows of 128 under 4 query heads a KV head (389 MB, 57.3 us at the copy rate) 74.5 us, 1.9 M rows of
 // 256 under 2 (545 MB, 80.3 us) 100.  A step's HMMAs and scale products share a port, 670 of the 830 clocks that a scheduler
 // gives it at d = 128; conversions and byte moves take 570 of another's.  Steps of 16 tokens with a maximum in each took
@@ -71,8 +71,11 @@ struct Layout4 {
   static int bytes(int g, int nb) { return SMALL + 128 + RING + nb * comb_floats(g) * 4 + kFacMax * 4; }
 };
 
-// A weight is 2^(x - m + 8), with m a reference that moves only when a score passes it by more than 7: at most
-// 2^15, in reach of f16, and a step that moves nothing neither reduces a maximum over lanes nor rescales O.
+// A weight is 2^(x - m), with m a reference 8 below the largest score when it was taken, which moves only when a weight
+// would pass 2^15: all are in reach of f16, and a step that moves nothing neither reduces a maximum over lanes nor
+// rescales O.  m is that difference rounded up, and scores are rounded before m is taken off them, as m's own was: then
+// the largest score's weight is between 1 and 2^8 whatever their magnitude (past 2^27 m is the score itself; one fma of
+// product and reference would leave the product's rounding, which passes 2^5 there, in the exponent).
 constexpr float kWeightLog2 = 8.f, kWeightMost = 15.f;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -265,8 +268,8 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
     at_nxt = tile_at(32 + lane);  // (looked up behind the first copies, which are fewer than sixteen steps)
 
     bool dead = false;  // a copy wait timed out: skip all further tiles, keep handing off
-    // the reference of each head's weights, 8 less it, and their sum
-    float m0 = -INFINITY, m1 = -INFINITY, d0 = INFINITY, d1 = INFINITY, l0 = 0.f, l1 = 0.f;
+    // the reference of each head's weights, and their sum
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     float o[C][8][4];
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -370,13 +373,13 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
             const uint32_t vt = stage + hf * LY::TILE + kVCodes4;
             vx[hf] = lds128(vt + 64 * gid + 16 * tig), vy[hf] = lds128(vt + 512 + 64 * gid + 16 * tig);
           }
-          // online softmax, base 2; y = x - m + 8
+          // online softmax, base 2; y = x - m
           auto logits = [&](float(&y)[2][4]) {
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
               for (int j = 0; j < 4; j += 2) {
-                const float2 v = fma2(make_float2(sc[hf][j], sc[hf][j + 1]), make_float2(z0, z1), make_float2(d0, d1));
+                const float2 v = add2(mul2(make_float2(sc[hf][j], sc[hf][j + 1]), make_float2(z0, z1)), make_float2(-m0, -m1));
                 y[hf][j] = v.x, y[hf][j + 1] = v.y;
               }
             if (part) {
@@ -393,7 +396,7 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
           logits(y);
           const float top = max3(max3(y[0][0], y[0][1], y[0][2]), max3(y[0][3], y[1][0], y[1][1]), fmaxf(y[1][2], y[1][3]));
           if (__any_sync(0xffffffffu, top > kWeightMost)) {
-            // the reference moves to the maximum so far
+            // the reference moves to 8 below the maximum so far
             float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf)
@@ -409,21 +412,15 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
               x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
               x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
             }
-            const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+            const float n0 = fmaxf(m0, __fadd_ru(x0, -kWeightLog2)), n1 = fmaxf(m1, __fadd_ru(x1, -kWeightLog2));
             const float c0 = n0 == m0 ? 1.f : ex2(m0 - n0), c1 = n1 == m1 ? 1.f : ex2(m1 - n1);
             m0 = n0, m1 = n1;
-            d0 = kWeightLog2 - m0, d1 = kWeightLog2 - m1;
             l0 *= c0, l1 *= c1;
 #pragma unroll
             for (int c = 0; c < C; ++c)
 #pragma unroll
               for (int j = 0; j < 8; ++j) o[c][j][0] *= c0, o[c][j][1] *= c1, o[c][j][2] *= c0, o[c][j][3] *= c1;
             logits(y);
-            // (where m is past 2^20 the sums round: no weight passes the largest for that)
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) y[hf][j] = y[hf][j] > kWeightMost ? kWeightMost : y[hf][j];
           }
           uint32_t wt[2][2];
 #pragma unroll
@@ -477,15 +474,13 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
         l0 += __shfl_xor_sync(0xffffffffu, l0, off);
         l1 += __shfl_xor_sync(0xffffffffu, l1, off);
       }
-      // the epilogue knows weights that are 1 at the reference, and V with its unit
-      constexpr float kBack = 1.f / 256.f;
-      const float back = kBack * pool.v_unit;
+      const float unit = pool.v_unit;
       float *cm = comb_m + (hb * NW + warp) * 8, *cl = comb_l + (hb * NW + warp) * 8;
       if (gid == 0) {
         cm[2 * tig] = m0;
         cm[2 * tig + 1] = m1;
-        cl[2 * tig] = l0 * kBack;
-        cl[2 * tig + 1] = l1 * kBack;
+        cl[2 * tig] = l0;
+        cl[2 * tig + 1] = l1;
       }
       float *co = comb_o + hb * cfl + warp * a.g * ostride;  // [g][ostride] of this warp
       const int h0 = 2 * tig, h1 = 2 * tig + 1;
@@ -495,12 +490,11 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
         for (int i = 0; i < 8; ++i) {
           float(&oo)[4] = o[c][i];
           const int at = 128 * c + 16 * gid + 2 * i;
-          if (h0 < a.g) *reinterpret_cast<float2 *>(co + h0 * ostride + at) = make_float2(oo[0] * back, oo[2] * back);
-          if (h1 < a.g) *reinterpret_cast<float2 *>(co + h1 * ostride + at) = make_float2(oo[1] * back, oo[3] * back);
+          if (h0 < a.g) *reinterpret_cast<float2 *>(co + h0 * ostride + at) = make_float2(oo[0] * unit, oo[2] * unit);
+          if (h1 < a.g) *reinterpret_cast<float2 *>(co + h1 * ostride + at) = make_float2(oo[1] * unit, oo[3] * unit);
           oo[0] = oo[1] = oo[2] = oo[3] = 0.f;
         }
       m0 = m1 = -INFINITY;
-      d0 = d1 = INFINITY;
       l0 = l1 = 0.f;
       mbar_arrive(&full[hb]);  // (release: this thread's hand-off writes come first)
     }
