@@ -510,35 +510,43 @@ __global__ void __launch_bounds__(Layout4<D>::THREADS, 1) decode4_kernel(const D
                             s_dead, full, empty, s_t0);
 }
 
-template <int D>
-int launch(cudaStream_t stream, int format, const void *map, const DecodeArgs &args, const Pool4 &pool, int N_CTA) {
-  const char *name = "tg_decode_grown";
-  Pool4 p = pool;
-  p.buffers = Layout4<D>::buffers(args.g);
+struct Kernel {
   void *fn;
-  int threads, smem;
+  int threads, smem, buffers;
+};
+
+// The kernel of a call with g query heads a KV head, ready to launch.  It comes ahead of the tensor map: a host thread's first
+// call into the runtime makes the context current that the driver's encoder needs.
+template <int D>
+int kernel_of(const char *name, int format, int g, Kernel &k) {
+  k.buffers = Layout4<D>::buffers(g);
   if (format == TG_PAGES_BF16) {
-    fn = reinterpret_cast<void *>(&grown_decode_kernel<D>);
-    threads = Layout<D>::THREADS, smem = Layout<D>::smem_bytes(args.g);
+    k.fn = reinterpret_cast<void *>(&grown_decode_kernel<D>);
+    k.threads = Layout<D>::THREADS, k.smem = Layout<D>::smem_bytes(g);
   } else {
-    fn = reinterpret_cast<void *>(&decode4_kernel<D>);
-    threads = Layout4<D>::THREADS, smem = Layout4<D>::bytes(args.g, p.buffers);
+    k.fn = reinterpret_cast<void *>(&decode4_kernel<D>);
+    k.threads = Layout4<D>::THREADS, k.smem = Layout4<D>::bytes(g, k.buffers);
   }
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
   if (e != cudaSuccess) return tgi::fail(TG_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", name, cudaGetErrorString(e));
+  return TG_OK;
+}
+
+int launch(const char *name, cudaStream_t stream, int format, const Kernel &k, const void *map, const DecodeArgs &args, const Pool4 &pool,
+           int N_CTA) {
   void *bf16[] = {const_cast<void *>(map), const_cast<DecodeArgs *>(&args)};
-  void *e2m1[] = {const_cast<DecodeArgs *>(&args), &p};
+  void *e2m1[] = {const_cast<DecodeArgs *>(&args), const_cast<Pool4 *>(&pool)};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(N_CTA);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.blockDim = dim3(k.threads);
+  cfg.dynamicSmemBytes = (size_t)k.smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelExC(&cfg, fn, format == TG_PAGES_BF16 ? bf16 : e2m1);
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, k.fn, format == TG_PAGES_BF16 ? bf16 : e2m1);
   if (e != cudaSuccess) return tgi::fail(TG_ERR_CUDA, "%s: launch failed: %s", name, cudaGetErrorString(e));
   return tgi::ok();
 }
@@ -572,8 +580,11 @@ extern "C" int tg_decode_grown(tg_stream_t stream, const void *plan_host, const 
                                 pool_pages, scale, dev_status, cta_time);
   args.ntok = ntok, args.added = added, args.plus = plus, args.reserve = reserve;
   args.wait_tables = 1;  // the kernel before it may have written pages, queries and added
+  Kernel k;
+  rc = hd->d == 128 ? kernel_of<128>(fn, format, args.g, k) : kernel_of<256>(fn, format, args.g, k);
+  if (rc) return rc;
   CUtensorMap map;
-  Pool4 p4 = {static_cast<const uint8_t *>(pool), hd->P / 16, v_unit, 2};
+  const Pool4 p4 = {static_cast<const uint8_t *>(pool), hd->P / 16, v_unit, k.buffers};
   if (format == TG_PAGES_BF16) {
     rc = make_pool_map(&map, static_cast<const uint16_t *>(pool), pool_pages, hd, fn);
     if (rc) return rc;
@@ -585,6 +596,5 @@ extern "C" int tg_decode_grown(tg_stream_t stream, const void *plan_host, const 
       return fail(TG_ERR_CAPACITY, "%s: pool_pages=%lld gives more than 2^31-1 tiles, or none", fn, (long long)pool_pages);
     args.scale_log2 *= k_unit;
   }
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return hd->d == 128 ? launch<128>(s, format, &map, args, p4, hd->N_CTA) : launch<256>(s, format, &map, args, p4, hd->N_CTA);
+  return launch(fn, reinterpret_cast<cudaStream_t>(stream), format, k, &map, args, p4, hd->N_CTA);
 }

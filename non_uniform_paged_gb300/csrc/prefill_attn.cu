@@ -24,7 +24,8 @@ extern "C" int tg_prefill_attn(tg_stream_t stream, const void *plan_host, const 
   if (misaligned(K, 16) || misaligned(V, 16)) return tgi::fail(TG_ERR_INVALID_ARG, "%s: K and V must be 16-byte aligned", fn);
   const TileArgs a = tile_args(hd, plan_dev, scale, workspace, out, lse, dev_status);
   CUtensorMap qm, km, vm;
-  rc = tile_map(&qm, fn, "q", q, hd->d, hd->H_q, hd->rows, a.g, a.tq);
+  rc = ready_tiles<false>(fn, hd->d);
+  if (!rc) rc = tile_map(&qm, fn, "q", q, hd->d, hd->H_q, hd->rows, a.g, a.tq);
   if (rc) return rc;
   if (hd->max_kv > 0) {
     rc = tile_map(&km, fn, "K", K, hd->d, Nmax, lists, tgi::kTileKeys, 1);

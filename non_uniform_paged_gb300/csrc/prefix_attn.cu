@@ -24,7 +24,8 @@ extern "C" int tg_prefix_attn(tg_stream_t stream, const void *plan_host, const v
   if (!hd->n_items) return tgi::ok();  // no request
   TileArgs a = tile_args(hd, plan_dev, scale, workspace, out, lse, dev_status);
   CUtensorMap qm, pm;
-  rc = tile_map(&qm, fn, "q", q, hd->d, hd->H_q, hd->rows, a.g, a.tq);
+  rc = ready_tiles<true>(fn, hd->d);
+  if (!rc) rc = tile_map(&qm, fn, "q", q, hd->d, hd->H_q, hd->rows, a.g, a.tq);
   if (rc) return rc;
   a.P = hd->P;
   a.H_p = hd->H_p;

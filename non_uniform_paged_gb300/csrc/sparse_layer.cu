@@ -42,15 +42,11 @@ __global__ void __launch_bounds__(Layout<kD>::THREADS, 1)
   decode_body<kD>(&pool_map, da, smem);
 }
 
-template <int GQ>
-int launch_fused(const char *fn_name, const CUtensorMap &map, const ScoreArgs &sa, const DecodeArgs &da, int grid,
+int launch_fused(const char *fn_name, const void *fn, int smem, const CUtensorMap &map, const ScoreArgs &sa, const DecodeArgs &da, int grid,
                  cudaStream_t s) {
-  auto fn = sparse_layer_kernel<GQ>;
-  const int smem = std::max(ScoreCfg<kD>::SMEM, Layout<kD>::smem_bytes(da.g));
   const int threads = Layout<kD>::THREADS;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   int dev = 0, sms = 0, per_sm = 0;
-  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, threads, smem);
   if (e != cudaSuccess) return tgi::fail(TG_ERR_CUDA, "%s: %s", fn_name, cudaGetErrorString(e));
@@ -69,7 +65,7 @@ int launch_fused(const char *fn_name, const CUtensorMap &map, const ScoreArgs &s
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelExC(&cfg, reinterpret_cast<void *>(fn), params);
+  e = cudaLaunchKernelExC(&cfg, fn, params);
   if (e != cudaSuccess) return tgi::fail(TG_ERR_CUDA, "%s: launch failed: %s", fn_name, cudaGetErrorString(e));
   return TG_OK;
 }
@@ -114,6 +110,14 @@ extern "C" int tg_sparse_layer(tg_stream_t stream, const void *plan_host, const 
   if (((reinterpret_cast<uintptr_t>(minmax) | reinterpret_cast<uintptr_t>(score_ws)) & 15) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255))
     return tgi::fail(TG_ERR_INVALID_ARG, "tg_sparse_layer: minmax and score workspace 16-byte, workspace 256-byte aligned");
+  const void *fn = g <= 1   ? reinterpret_cast<const void *>(&sparse_layer_kernel<1>)
+                   : g <= 2 ? reinterpret_cast<const void *>(&sparse_layer_kernel<2>)
+                   : g <= 4 ? reinterpret_cast<const void *>(&sparse_layer_kernel<4>)
+                            : reinterpret_cast<const void *>(&sparse_layer_kernel<8>);
+  const int smem = std::max(ScoreCfg<kD>::SMEM, Layout<kD>::smem_bytes(g));
+  // (ahead of the tensor map: a host thread's first call into the runtime makes the context current that the encoder needs)
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return tgi::fail(TG_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", fn_name, cudaGetErrorString(e));
   CUtensorMap map;
   rc = make_pool_map(&map, pool, pool_pages, hd, fn_name);
   if (rc) return rc;
@@ -145,9 +149,5 @@ extern "C" int tg_sparse_layer(tg_stream_t stream, const void *plan_host, const 
   if (wait_limit_ns > 0) da.wait_ns = (uint64_t)wait_limit_ns;
   da.epoch = epoch;
   da.wait_tables = 0;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (g <= 1) return launch_fused<1>(fn_name, map, sa, da, hd->N_CTA, s);
-  if (g <= 2) return launch_fused<2>(fn_name, map, sa, da, hd->N_CTA, s);
-  if (g <= 4) return launch_fused<4>(fn_name, map, sa, da, hd->N_CTA, s);
-  return launch_fused<8>(fn_name, map, sa, da, hd->N_CTA, s);
+  return launch_fused(fn_name, fn, smem, map, sa, da, hd->N_CTA, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -92,13 +92,20 @@ inline TileArgs tile_args(const tg_tile_header *hd, const void *plan_dev, float 
   return a;
 }
 
+// The tile kernel, ready to launch.  It comes ahead of the tensor maps: a host thread's first call into the runtime makes the
+// context current that the driver's encoder needs.
+template <bool PAGED>
+int ready_tiles(const char *fn, int d) {
+  void *kernel = d == 128 ? reinterpret_cast<void *>(&tile_attn_kernel<128, PAGED>) : reinterpret_cast<void *>(&tile_attn_kernel<256, PAGED>);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTileSmem);
+  if (e != cudaSuccess) return tgi::fail(TG_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", fn, cudaGetErrorString(e));
+  return TG_OK;
+}
+
 // the tile kernel and, where the plan cut runs, the merge as its programmatic dependent
 template <int D, bool PAGED>
 int launch_tiles(const char *fn, tg_stream_t stream, const tg_tile_header *hd, const void *plan_dev,
                  const CUtensorMap &qm, const CUtensorMap &km, const CUtensorMap &vm, const TileArgs &a) {
-  cudaError_t e = cudaFuncSetAttribute(tile_attn_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)kTileSmem);
-  if (e != cudaSuccess) return tgi::fail(TG_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", fn, cudaGetErrorString(e));
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -109,7 +116,7 @@ int launch_tiles(const char *fn, tg_stream_t stream, const tg_tile_header *hd, c
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, tile_attn_kernel<D, PAGED>, qm, km, vm, a);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, tile_attn_kernel<D, PAGED>, qm, km, vm, a);
   if (e != cudaSuccess) return tgi::fail(TG_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
   if (!hd->n_merge) return tgi::ok();
   MergeArgs m;
