@@ -53,19 +53,20 @@ void *kernel_ptr() {
 }
 
 int kernel_config(int d, int g, void **fn, int *threads, int *smem) {
+  int most;
   if (d == 128) {
     *fn = kernel_ptr<128>();
     *threads = Layout<128>::THREADS;
-    *smem = Layout<128>::smem_bytes(g);
+    *smem = Layout<128>::smem_bytes(g), most = Layout<128>::smem_most();
   } else if (d == 256) {
     *fn = kernel_ptr<256>();
     *threads = Layout<256>::THREADS;
-    *smem = Layout<256>::smem_bytes(g);
+    *smem = Layout<256>::smem_bytes(g), most = Layout<256>::smem_most();
   } else {
     return tgi::fail(TG_ERR_SHAPE, "tg_decode_attn: d=%d (128 or 256)", d);
   }
   if (g < 1 || g > 8) return tgi::fail(TG_ERR_SHAPE, "tg_decode_attn: g=%d (1..8)", g);
-  cudaError_t e = cudaFuncSetAttribute(*fn, cudaFuncAttributeMaxDynamicSharedMemorySize, *smem);
+  cudaError_t e = cudaFuncSetAttribute(*fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return tgi::fail(TG_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
   return TG_OK;
 }

@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 
@@ -111,6 +112,13 @@ struct Layout {
   __host__ __device__ static int ostride(int g) { return g <= 4 ? D + 4 : D; }
   __host__ __device__ static int comb_floats(int g) { return NW * g * ostride(g); }
   static int smem_bytes(int g) { return SMALL + 1008 + RING + 2 * comb_floats(g) * 4 + kFacMax * 4; }
+  // What a kernel is allowed, whatever the call takes: the limit belongs to the kernel, and another host thread's call
+  // with fewer heads may come between one's limit and its launch.
+  static int smem_most() {
+    int most = 0;
+    for (int g = 1; g <= 8; ++g) most = std::max(most, smem_bytes(g));
+    return most;
+  }
 };
 
 // byte offset of element (row, col) of a TMA tile loaded as D/64 boxes of

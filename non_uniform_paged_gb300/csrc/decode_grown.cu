@@ -69,6 +69,11 @@ struct Layout4 {
   // two hand-off buffers, or one where two do not fit (d = 256 with more than four query heads)
   static int buffers(int g) { return bytes(g, 2) <= MOST ? 2 : 1; }
   static int bytes(int g, int nb) { return SMALL + 128 + RING + nb * comb_floats(g) * 4 + kFacMax * 4; }
+  static int bytes_most() {  // as Layout::smem_most
+    int most = 0;
+    for (int g = 1; g <= 8; ++g) most = std::max(most, bytes(g, buffers(g)));
+    return most;
+  }
 };
 
 // A weight is 2^(x - m), with m a reference 8 below the largest score when it was taken, which moves only when a weight
@@ -520,14 +525,15 @@ struct Kernel {
 template <int D>
 int kernel_of(const char *name, int format, int g, Kernel &k) {
   k.buffers = Layout4<D>::buffers(g);
+  int most;
   if (format == TG_PAGES_BF16) {
     k.fn = reinterpret_cast<void *>(&grown_decode_kernel<D>);
-    k.threads = Layout<D>::THREADS, k.smem = Layout<D>::smem_bytes(g);
+    k.threads = Layout<D>::THREADS, k.smem = Layout<D>::smem_bytes(g), most = Layout<D>::smem_most();
   } else {
     k.fn = reinterpret_cast<void *>(&decode4_kernel<D>);
-    k.threads = Layout4<D>::THREADS, k.smem = Layout4<D>::bytes(g, k.buffers);
+    k.threads = Layout4<D>::THREADS, k.smem = Layout4<D>::bytes(g, k.buffers), most = Layout4<D>::bytes_most();
   }
-  cudaError_t e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+  cudaError_t e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return tgi::fail(TG_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", name, cudaGetErrorString(e));
   return TG_OK;
 }

@@ -116,7 +116,8 @@ extern "C" int tg_sparse_layer(tg_stream_t stream, const void *plan_host, const 
                             : reinterpret_cast<const void *>(&sparse_layer_kernel<8>);
   const int smem = std::max(ScoreCfg<kD>::SMEM, Layout<kD>::smem_bytes(g));
   // (ahead of the tensor map: a host thread's first call into the runtime makes the context current that the encoder needs)
-  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             std::max(ScoreCfg<kD>::SMEM, Layout<kD>::smem_most()));
   if (e != cudaSuccess) return tgi::fail(TG_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", fn_name, cudaGetErrorString(e));
   CUtensorMap map;
   rc = make_pool_map(&map, pool, pool_pages, hd, fn_name);
