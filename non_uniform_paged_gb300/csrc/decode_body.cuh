@@ -849,12 +849,17 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 // TMA map of the pool seen as rows of d bf16 values (boxes of 16 rows x 64 columns, 128-byte
 // swizzle); TG_OK or an error with the message set
-inline int make_pool_map(CUtensorMap *map, const uint16_t *pool, int64_t pool_pages, const tg_plan_header *hd,
-                         const char *fn) {
+inline int check_pool(int64_t pool_pages, const tg_plan_header *hd, const char *fn) {
   const int64_t rows = pool_pages * hd->H_p * 2 * hd->P;
   if (pool_pages <= 0 || rows > INT32_MAX)
     return tgi::fail(TG_ERR_CAPACITY, "%s: pool_pages=%lld gives %lld rows (1..2^31-1)", fn, (long long)pool_pages,
                      (long long)rows);
+  return TG_OK;
+}
+inline int make_pool_map(CUtensorMap *map, const uint16_t *pool, int64_t pool_pages, const tg_plan_header *hd,
+                         const char *fn) {
+  if (int rc = check_pool(pool_pages, hd, fn)) return rc;
+  const int64_t rows = pool_pages * hd->H_p * 2 * hd->P;
   PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
   if (!enc) return tgi::fail(TG_ERR_CUDA, "%s: cuTensorMapEncodeTiled is unavailable", fn);
   const cuuint64_t gdim[2] = {(cuuint64_t)hd->d, (cuuint64_t)rows};

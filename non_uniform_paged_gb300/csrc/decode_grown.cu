@@ -586,21 +586,22 @@ extern "C" int tg_decode_grown(tg_stream_t stream, const void *plan_host, const 
                                 pool_pages, scale, dev_status, cta_time);
   args.ntok = ntok, args.added = added, args.plus = plus, args.reserve = reserve;
   args.wait_tables = 1;  // the kernel before it may have written pages, queries and added
-  Kernel k;
-  rc = hd->d == 128 ? kernel_of<128>(fn, format, args.g, k) : kernel_of<256>(fn, format, args.g, k);
-  if (rc) return rc;
-  CUtensorMap map;
-  const Pool4 p4 = {static_cast<const uint8_t *>(pool), hd->P / 16, v_unit, k.buffers};
+  const int p16 = hd->P / 16;
   if (format == TG_PAGES_BF16) {
-    rc = make_pool_map(&map, static_cast<const uint16_t *>(pool), pool_pages, hd, fn);
-    if (rc) return rc;
+    if ((rc = check_pool(pool_pages, hd, fn))) return rc;
   } else {
     if (!unit_ok(k_unit) || !unit_ok(v_unit))
       return fail(TG_ERR_INVALID_ARG, "%s: k_unit=%g, v_unit=%g (powers of two in [2^-60, 2^60])", fn, (double)k_unit,
                   (double)v_unit);
-    if (pool_pages <= 0 || pool_pages > INT32_MAX / hd->H_p / p4.p16)
+    if (pool_pages <= 0 || pool_pages > INT32_MAX / hd->H_p / p16)
       return fail(TG_ERR_CAPACITY, "%s: pool_pages=%lld gives more than 2^31-1 tiles, or none", fn, (long long)pool_pages);
     args.scale_log2 *= k_unit;
   }
+  Kernel k;
+  rc = hd->d == 128 ? kernel_of<128>(fn, format, args.g, k) : kernel_of<256>(fn, format, args.g, k);
+  if (rc) return rc;
+  CUtensorMap map;
+  if (format == TG_PAGES_BF16 && (rc = make_pool_map(&map, static_cast<const uint16_t *>(pool), pool_pages, hd, fn))) return rc;
+  const Pool4 p4 = {static_cast<const uint8_t *>(pool), p16, v_unit, k.buffers};
   return launch(fn, reinterpret_cast<cudaStream_t>(stream), format, k, &map, args, p4, hd->N_CTA);
 }

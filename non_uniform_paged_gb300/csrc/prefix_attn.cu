@@ -22,6 +22,11 @@ extern "C" int tg_prefix_attn(tg_stream_t stream, const void *plan_host, const v
   if (misaligned(own_out, 16) || misaligned(pool, 16))
     return tgi::fail(TG_ERR_INVALID_ARG, "%s: pool and own_out must be 16-byte aligned", fn);
   if (!hd->n_items) return tgi::ok();  // no request
+  if (hd->max_kv > 0) {
+    if (!pool || !pt_off || !pt_ids) return tgi::fail(TG_ERR_INVALID_ARG, "%s: NULL pool or page table", fn);
+    if (pool_pages <= 0 || pool_pages > INT32_MAX / (2 * hd->H_p) - 1)
+      return tgi::fail(TG_ERR_CAPACITY, "%s: pool_pages=%lld", fn, (long long)pool_pages);
+  }
   TileArgs a = tile_args(hd, plan_dev, scale, workspace, out, lse, dev_status);
   CUtensorMap qm, pm;
   rc = ready_tiles<true>(fn, hd->d);
@@ -30,9 +35,6 @@ extern "C" int tg_prefix_attn(tg_stream_t stream, const void *plan_host, const v
   a.P = hd->P;
   a.H_p = hd->H_p;
   if (hd->max_kv > 0) {
-    if (!pool || !pt_off || !pt_ids) return tgi::fail(TG_ERR_INVALID_ARG, "%s: NULL pool or page table", fn);
-    if (pool_pages <= 0 || pool_pages > INT32_MAX / (2 * hd->H_p) - 1)
-      return tgi::fail(TG_ERR_CAPACITY, "%s: pool_pages=%lld", fn, (long long)pool_pages);
     rc = tile_map(&pm, fn, "pool", pool, hd->d, hd->P, pool_pages * hd->H_p * 2, 16, 1);
     if (rc) return rc;
   } else {

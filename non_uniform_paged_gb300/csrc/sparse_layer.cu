@@ -110,6 +110,7 @@ extern "C" int tg_sparse_layer(tg_stream_t stream, const void *plan_host, const 
   if (((reinterpret_cast<uintptr_t>(minmax) | reinterpret_cast<uintptr_t>(score_ws)) & 15) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255))
     return tgi::fail(TG_ERR_INVALID_ARG, "tg_sparse_layer: minmax and score workspace 16-byte, workspace 256-byte aligned");
+  if ((rc = check_pool(pool_pages, hd, fn_name))) return rc;
   const void *fn = g <= 1   ? reinterpret_cast<const void *>(&sparse_layer_kernel<1>)
                    : g <= 2 ? reinterpret_cast<const void *>(&sparse_layer_kernel<2>)
                    : g <= 4 ? reinterpret_cast<const void *>(&sparse_layer_kernel<4>)
