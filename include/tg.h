@@ -796,7 +796,9 @@ int tg_dequant_pages(tg_stream_t stream, int batch, int H, int H_p, int P, int d
  * Arguments: plan, q, pt_off, pt_ids, scale, workspace, out, lse, dev_status, cta_time as tg_decode_attn, q and
  *   out 16-byte aligned; format and pool (16-byte aligned; tokens of all its heads fit int32); ntok int32
  *   [batch][H] of this layer; added int32 [batch] (NULL: zeros); plus >= 0; k_unit, v_unit as tg_append_rope.
- *   added[b] + plus outside [0, reserve] sets TG_STATUS_BAD_INPUT and counts as the nearer end.  Rows behind the last token may hold anything.
+ *   added[b] + plus outside [0, reserve] sets TG_STATUS_BAD_INPUT and counts as the nearer end.  Rows behind the last token may hold anything;
+ *   a row that is counted but was not written is read as it is.  Where requests bring unlike numbers of tokens in a step, added
+ *   may be an array of the caller's that counts those too, with plus = 0 (tg_append_rope takes the counts ahead of the step).
  *   A list too short for its tokens, or a page id outside the pool, sets TG_STATUS_BAD_PAGE (out is then
  *   unspecified).  out = 0 and lse = -inf for a head without tokens.
  *   bf16 pages: arithmetic as tg_decode_attn, but that the weights are two bf16 terms (off by less than 2^-14 of themselves)

@@ -574,6 +574,7 @@ class GrowingLists(_OnStreams):
         placed, counts, self.one_each = tables.split([order.size, ntok.size, self.batch + 1])
         self.order, self.ntok = placed.view(L, H).unbind(), counts.view(L, self.batch, H).unbind()
         self.scale = 1.0 / math.sqrt(d)
+        self._step = ["none"] * L  # of each layer: appended to never ("none"), in this step ("now"), in an earlier one ("before")
         self._own(self.plan.plan_dev, self.workspace, self.status, self.added, tables)
 
     def append(self, layer, qkv, cos_sin, q, pool, pool_pages, pt_off, pt_ids, cu_q=None, origin=None, positions=None,
@@ -586,14 +587,16 @@ class GrowingLists(_OnStreams):
                        k_unit=self.k_unit, v_unit=self.v_unit, q_weight=q_weight, k_weight=k_weight, eps=eps, pairs=pairs,
                        positions=positions, axis_of=axis_of, origin=origin, K=K, V=V, start=start, dev_status=self.status,
                        stream=stream)
+        self._step[layer] = "now"
         self._used_on(stream)
 
     def attend(self, layer, q, pool, pool_pages, pt_off, pt_ids, out, lse=None, plus=1, scale=None, cta_time=None,
-               stream=None):
+               stream=None, added=None):
         """One layer's decode attention over retained and appended tokens (tg_decode_grown); plus: the tokens
-        appended in this step, which added does not count yet."""
-        tg_decode_grown(self.plan, layer, self.format, q, pool, pool_pages, pt_off, pt_ids, self.ntok[layer], self.added,
-                        plus, self.reserve, self.scale if scale is None else scale, out, lse=lse, k_unit=self.k_unit,
+        appended in this step, which added does not count yet.  added (int32 [batch], on the device): counts to go by in
+        place of the owner's, where requests brought unlike numbers of tokens in this step."""
+        tg_decode_grown(self.plan, layer, self.format, q, pool, pool_pages, pt_off, pt_ids, self.ntok[layer],
+                        self.added if added is None else added, plus, self.reserve, self.scale if scale is None else scale, out, lse=lse, k_unit=self.k_unit,
                         v_unit=self.v_unit, workspace=self.workspace, dev_status=self.status, cta_time=cta_time,
                         stream=stream)
         self._used_on(stream)
@@ -601,6 +604,7 @@ class GrowingLists(_OnStreams):
     def advance(self, n=1):
         """Count a step's tokens, after its last layer, on the current stream: n for each request, or int32 [batch]."""
         self.added.add_(n)
+        self._step = ["none" if s == "none" else "before" for s in self._step]
         self._used_on(None)
 
     def quantize(self, layer, src, src_pages, src_off, src_ids, dst, dst_pages, dst_off, dst_ids, stream=None):
@@ -686,10 +690,18 @@ class GrowingCache(RaggedCache):
         self.lists.append(layer, qkv, cos_sin, q, self.pool, self.n_pages, self.list_offsets(layer), self.pt_ids_dev,
                           stream=stream, **how)
 
-    def decode_layer(self, layer, q, out, lse=None, cta_time=None, stream=None, pool=None, plus=1):
-        """GrowingLists.attend over this cache's pages."""
+    def decode_layer(self, layer, q, out, lse=None, cta_time=None, stream=None, pool=None, plus=None, added=None):
+        """GrowingLists.attend over this cache's pages.  plus by default: 1 if the layer was appended to since advance(),
+        0 if it never was (a cache that only retained), or with added, which then counts this step's tokens too.  Between
+        steps it has to be given: a graph that appends may have been replayed meanwhile, or not."""
+        if plus is None:
+            step = self.lists._step[layer]
+            if step == "before" and added is None:
+                raise ValueError(f"layer {layer} was not appended to since advance(): plus=0 attends to what advance() has "
+                                 "counted, plus=1 to a token of this step too")
+            plus = 1 if step == "now" and added is None else 0
         self.lists.attend(layer, q, self.pool if pool is None else pool, self.n_pages, self.list_offsets(layer),
-                          self.pt_ids_dev, out, lse=lse, plus=plus, cta_time=cta_time, stream=stream)
+                          self.pt_ids_dev, out, lse=lse, plus=plus, cta_time=cta_time, stream=stream, added=added)
 
     def advance(self, n=1):
         self.lists.advance(n)
