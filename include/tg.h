@@ -558,6 +558,7 @@ int tg_alloc_query(const void *state, int64_t *n_free, int64_t *n_live);
  *   [batch][H][Nmax][d] (outputs; q may not overlap qkv).  Every pointer 16-byte aligned
  *   (cu_q, start, positions: 4).
  *   Host sizes: d in {128, 256}, rot % 16 == 0, 0 <= rot <= d, eps >= 0.
+ *   (The mean is float32's: with an eps below 2^-100, rows whose mean square is below that too lose their squares.)
  *   Rows from cu_q[batch] on are left as they are.  A token whose position is outside
  *   [0, max_pos) (with rot > 0) or whose context row is outside [0, Nmax) sets
  *   TG_STATUS_BAD_INPUT and writes nothing.  T = 0 launches nothing.
@@ -748,7 +749,7 @@ int tg_reserve_pages(int L, int batch, int H, int H_p, int P, const int32_t *hea
  *   Host sizes: d in {128, 256}, rot % 16 == 0, P % 16 == 0, H % H_p == 0.
  *   4-bit pages: a K value is rounded to 4 bits from what float32 arithmetic gives, or, where that is too
  *   close to the border of two codes or scales to tell, from float64 arithmetic: the codes are those of the formulas
- *   (of projections below 2^59 in magnitude, whose squares' sum float32 holds).
+ *   (of projections below 2^59 in magnitude, whose squares' sum float32 holds; small ones, and any eps >= 0, are no limit).
  *   A token ahead of its request's cu_q[b] (cu_q[0] > 0, or one that descends), with added[b] < 0, added[b] + i >= reserve,
  *   a position outside [0, max_pos) (rot > 0) or a dense row outside [0, Nmax) sets TG_STATUS_BAD_INPUT and writes nothing.  A head whose list is too short
  *   or names a page outside [0, pool_pages) sets TG_STATUS_BAD_PAGE and none of its rows is written.

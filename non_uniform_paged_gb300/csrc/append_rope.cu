@@ -39,6 +39,10 @@ using namespace tgk;
 constexpr int kSteps = 4;  // loads of a batch: heads at d = 256, pairs of heads at d = 128
 constexpr int kBlocksPerSm = 28, kBlocksPerSm4 = 20;  // of 72 and, for 4-bit pages, 96 registers
 constexpr int kMaxParts = 512;                        // warps of a token
+// A row whose mean square and eps together are below this is normalised as 2^100 times itself, with 2^200 eps: float32 loses squares
+// of values below 2^-63.  The factor takes such a row to 2^54 at most.  Only an eps below it lets a row be one, and such calls run
+// kernels of their own (SMALL): in the others the test alone costs 1% (68.0 and 68.7 us, 30.3 and 30.9).
+constexpr float kSmallMean = 0x1p-100f, kSmallUp = 0x1p100f;
 
 struct AppendArgs {
   const int32_t *cu_q, *positions, *origin, *head_order, *ntok, *added, *pt_ids, *start;
@@ -72,7 +76,7 @@ __device__ __forceinline__ float sticky(double v) {
   return f;
 }
 
-template <int D, bool PAIRS, bool E2M1>
+template <int D, bool PAIRS, bool E2M1, bool SMALL>
 __global__ void __launch_bounds__(32, E2M1 ? kBlocksPerSm4 : kBlocksPerSm) append_rope_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int LANES = D / 8, PER = 32 / LANES;  // lanes of a head, heads side by side
   constexpr int BATCH = kSteps * PER;             // heads of a batch: divides 32
@@ -196,19 +200,32 @@ __global__ void __launch_bounds__(32, E2M1 ? kBlocksPerSm4 : kBlocksPerSm) appen
       xv[j] = PAIRS ? make_float2(x[2 * j].y, x[2 * j + 1].y) : x[j + 2];
     }
   };
-  auto root = [&](const float2(&xu)[2], const float2(&xv)[2]) {
-    float2 sq = mul2(xu[0], xu[0]);
-    sq = fma2(xu[1], xu[1], sq), sq = fma2(xv[0], xv[0], sq), sq = fma2(xv[1], xv[1], sq);
-    float ss = sq.x + sq.y;
+  // what the norm multiplies the head's values by; those of a small row are scaled up here, by `lift`
+  auto root = [&](float2(&xu)[2], float2(&xv)[2], float &lift) {
+    auto mean = [&](float eps) {
+      float2 sq = mul2(xu[0], xu[0]);
+      sq = fma2(xu[1], xu[1], sq), sq = fma2(xv[0], xv[0], sq), sq = fma2(xv[1], xv[1], sq);
+      float ss = sq.x + sq.y;
 #pragma unroll
-    for (int d = LANES / 2; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-    return rsqrtf(fmaf(ss, 1.f / D, a.eps));
+      for (int d = LANES / 2; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+      return fmaf(ss, 1.f / D, eps);
+    };
+    float m = mean(a.eps);
+    if (SMALL) {
+      lift = m < kSmallMean ? kSmallUp : 1.f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) xu[j] = mul2(xu[j], make_float2(lift, lift)), xv[j] = mul2(xv[j], make_float2(lift, lift));
+      m = mean(a.eps * lift * lift);
+    }
+    return rsqrtf(m);
   };
 
   // a lane's rotated values of a head, as bf16
   auto turn = [&](const Head8 &in, bool norm, uint2 &oa, uint2 &ob) {
     float2 xu[2], xv[2], zu[2], zv[2];
     split(in, xu, xv);
+    float f, lift;
+    if (SMALL && norm) f = root(xu, xv, lift);
 #pragma unroll
     for (int j = 0; j < 2; ++j) zu[j] = mul2(uc[j], xu[j]), zv[j] = mul2(vc[j], xv[j]);
     if (turned) {  // behind rot a value meets no other: 0 times an infinite one would be NaN
@@ -216,7 +233,7 @@ __global__ void __launch_bounds__(32, E2M1 ? kBlocksPerSm4 : kBlocksPerSm) appen
       for (int j = 0; j < 2; ++j) zu[j] = fma2(vs[j], xv[j], zu[j]), zv[j] = fma2(us[j], xu[j], zv[j]);
     }
     if (norm) {
-      const float f = root(xu, xv);
+      if (!SMALL) f = root(xu, xv, lift);
 #pragma unroll
       for (int j = 0; j < 2; ++j) zu[j] = mul2(zu[j], make_float2(f, f)), zv[j] = mul2(zv[j], make_float2(f, f));
     }
@@ -313,6 +330,8 @@ __global__ void __launch_bounds__(32, E2M1 ? kBlocksPerSm4 : kBlocksPerSm) appen
       const bool w = a.kw != nullptr;
       float2 xu[2], xv[2], zu[2], zv[2];
       split(in, xu, xv);
+      float f = 1.f, lift = 1.f;
+      if (SMALL && w) f = root(xu, xv, lift);
       float ta, tb;  // the largest |first product| + |second one| of the first and of the second group
 #pragma unroll
       for (int j = 0; j < 2; ++j) zu[j] = mul2(uc[j], xu[j]), zv[j] = mul2(vc[j], xv[j]);
@@ -333,7 +352,7 @@ __global__ void __launch_bounds__(32, E2M1 ? kBlocksPerSm4 : kBlocksPerSm) appen
                         fmaxf(fmaxf(fabsf(zv[0].x), fabsf(zv[0].y)), fmaxf(fabsf(zv[1].x), fabsf(zv[1].y))));
       }
       if (w) {
-        const float f = root(xu, xv);
+        if (!SMALL) f = root(xu, xv, lift);
         const float2 ff = {f, f};
 #pragma unroll
         for (int j = 0; j < 2; ++j) zu[j] = mul2(zu[j], ff), zv[j] = mul2(zv[j], ff);
@@ -389,7 +408,7 @@ __global__ void __launch_bounds__(32, E2M1 ? kBlocksPerSm4 : kBlocksPerSm) appen
       codes();
       if (__any_sync(0xffffffffu, o.scale != scale_up || o.codes != up)) {
         // the row again in float64; the root's reciprocal by a Newton step from float32's (2^-43 off at most)
-        double f = 1.0;
+        double f64 = 1.0;
         if (w) {
           double ss = 0.0;
 #pragma unroll
@@ -399,16 +418,16 @@ __global__ void __launch_bounds__(32, E2M1 ? kBlocksPerSm4 : kBlocksPerSm) appen
           }
 #pragma unroll
           for (int e = LANES / 2; e; e >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, e);
-          const double mean = fma(ss, 1.0 / D, (double)a.eps);
-          f = (double)rsqrtf((float)mean);
-          f = f * fma(-0.5 * mean, f * f, 1.5);
+          const double mean = fma(ss, 1.0 / D, (double)a.eps * lift * lift);
+          f64 = (double)rsqrtf((float)mean);
+          f64 = f64 * fma(-0.5 * mean, f64 * f64, 1.5);
         }
         double *zp = zd + side * D;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int iu = PAIRS ? ga + 2 * j : ga + j, iv = PAIRS ? ga + 2 * j + 1 : gb + j;
-          const double yu = (double)(j & 1 ? xu[j / 2].y : xu[j / 2].x) * f * (w ? a.kw[iu] : 1.f);
-          const double yv = (double)(j & 1 ? xv[j / 2].y : xv[j / 2].x) * f * (w ? a.kw[iv] : 1.f);
+          const double yu = (double)(j & 1 ? xu[j / 2].y : xu[j / 2].x) * f64 * (w ? a.kw[iu] : 1.f);
+          const double yv = (double)(j & 1 ? xv[j / 2].y : xv[j / 2].x) * f64 * (w ? a.kw[iv] : 1.f);
           zp[iu] = turned ? yu * c[j] - yv * sn[j] : yu;
           zp[iv] = turned ? yv * c[j] + yu * sn[j] : yv;
         }
@@ -478,13 +497,13 @@ __global__ void __launch_bounds__(32, E2M1 ? kBlocksPerSm4 : kBlocksPerSm) appen
 
 bool misaligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
-template <int D>
+template <int D, bool SMALL>
 cudaError_t launch(const cudaLaunchConfig_t &cfg, bool pairs, bool e2m1, const AppendArgs &a) {
   if (e2m1)
-    return pairs ? cudaLaunchKernelEx(&cfg, append_rope_kernel<D, true, true>, a)
-                 : cudaLaunchKernelEx(&cfg, append_rope_kernel<D, false, true>, a);
-  return pairs ? cudaLaunchKernelEx(&cfg, append_rope_kernel<D, true, false>, a)
-               : cudaLaunchKernelEx(&cfg, append_rope_kernel<D, false, false>, a);
+    return pairs ? cudaLaunchKernelEx(&cfg, append_rope_kernel<D, true, true, SMALL>, a)
+                 : cudaLaunchKernelEx(&cfg, append_rope_kernel<D, false, true, SMALL>, a);
+  return pairs ? cudaLaunchKernelEx(&cfg, append_rope_kernel<D, true, false, SMALL>, a)
+               : cudaLaunchKernelEx(&cfg, append_rope_kernel<D, false, false, SMALL>, a);
 }
 
 }  // namespace
@@ -580,7 +599,10 @@ extern "C" int tg_append_rope(tg_stream_t stream, int batch, int T, int H_q, int
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const bool pairs = flags & TG_ROPE_PAIRS;
-  e = d == 128 ? launch<128>(cfg, pairs, e2m1, a) : launch<256>(cfg, pairs, e2m1, a);
+  if (eps < kSmallMean && (q_weight || k_weight))
+    e = d == 128 ? launch<128, true>(cfg, pairs, e2m1, a) : launch<256, true>(cfg, pairs, e2m1, a);
+  else
+    e = d == 128 ? launch<128, false>(cfg, pairs, e2m1, a) : launch<256, false>(cfg, pairs, e2m1, a);
   if (e != cudaSuccess) return fail(TG_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
   return tgi::ok();
 }
