@@ -533,6 +533,21 @@ def _page_format(pages, reserve):
     return PAGE_FORMATS[pages]
 
 
+def _grown_blocks(most, H_p, full):
+    """Blocks of threads of a grown decode: most [L][batch][H] the tokens of each list at the end of its reserve, full as many as
+    fit on the GPU.
+
+    Fewer than that where each would have less than 256 tokens, for what the merge of more pieces takes is then longer than what
+    they save (us, 4 bits and bf16, 32 + 8 heads; 20000 tokens of one request: 76 blocks 10.9 and 13.0, 152 blocks 14.0 and 15.6; 74000:
+    100 blocks 13.0 and 17.5, 152 blocks 13.9 and 19.1; 290000: 22.9 and 34.2, 20.2 and 33.2).  But one for two lists at
+    least, for a block takes its lists one after the other (256 lists of 1 to 8 tokens, bf16: 8 blocks 115, 32 26.5, 128 15.2; 512 of 6 to
+    20: 42 blocks 36.1, 152 17.6; 64 of 8 to 64: 13 blocks 20.0, 32 14.6; a block for each list costs more where they are few: 16
+    lists of 30 to 60, 8 blocks 6.6, 16 9.3)."""
+    L, batch, H = most.shape
+    tokens = int(most.sum((1, 2)).max(initial=0))
+    return max(H // H_p, min(full, max(-(-tokens // 256), -(-batch * H // 2))))
+
+
 class GrowingLists(_OnStreams):
     """Page lists that grow behind their retained tokens: the plan, counts and workspace of tg_append_rope
     and tg_decode_grown, over pages of either format ("bf16", or "e2m1": 4 bits).  order int32 [H] or [L][H] and
@@ -556,12 +571,7 @@ class GrowingLists(_OnStreams):
         most = ntok.astype(np.int64) + self.reserve  # the plan's tokens; the split goes by them too
         if most.size and most.max() > 2 ** 31 - 1 - P:
             raise ValueError(f"{most.max()} tokens of a head")
-        # One block of threads an SM, fewer where each would have less than 256 tokens: what the merge of more pieces
-        # takes is then longer than what they save (20000 tokens of 32 + 8 heads, 4 bits and bf16: 76 blocks 10.9 and 13.0
-        # us, 152 blocks 14.0 and 15.6; 74000 tokens: 100 blocks 13.0 and 17.5, 152 blocks 13.9 and 19.1; 290000: 22.9 and
-        # 34.2, 20.2 and 33.2).
-        largest = int(most.sum((1, 2)).max(initial=0))
-        self.n_cta = int(n_cta) if n_cta else max(H // H_p, min(tg_query_ncta(d, H_q // H), -(-largest // 256)))
+        self.n_cta = int(n_cta) if n_cta else _grown_blocks(most, H_p, tg_query_ncta(d, H_q // H))
         Phi = np.stack([most[l][:, order[l]].sum(0).reshape(-1, H_p).sum(1) for l in range(L)])
         plan, workspace = tg_plan_decode(tg_split_map(Phi, self.n_cta), order, most.astype(np.int32), H_q, H_p, P, d)
         self.workspace = torch.zeros(workspace, dtype=torch.uint8, device=self.device)
