@@ -46,18 +46,14 @@ class RaggedCache:
         if allocator is not None:
             self._take_pages(allocator)
         self.n_cta = int(n_cta) if n_cta else tg_query_ncta(d, self.g)
-        Phi = np.ones_like(self.pages["Phi"]) if uniform_split else self.pages["Phi"]
-        self.S = tg_split_map(Phi, self.n_cta)
-        self.plan, self.workspace_bytes = tg_plan_decode(self.S, self.pages["order"], self.pages["ntok"],
-                                                         H_q, H_p, P, d)
+        self.uniform_split = uniform_split
+        self._plan_decode()
         dev = self.device
         self.N_dev = torch.from_numpy(self.N).to(dev)
         self.order_dev = torch.from_numpy(self.pages["order"]).to(dev)
         self.ntok_dev = torch.from_numpy(self.pages["ntok"]).to(dev)
         self.pt_off_dev = torch.from_numpy(self.pages["pt_off"]).to(dev)
         self.pt_ids_dev = torch.from_numpy(self.pages["pt_ids"]).to(dev)
-        self.plan_dev = torch.from_numpy(self.plan).to(dev)
-        self.workspace = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         self._compact_ws = {}  # tg_compact_topk's workspace, by Nmax
         self.pool = None
@@ -68,6 +64,15 @@ class RaggedCache:
     def _build_pages(self, pages):
         """The page tables to use of tg_build_pages' (a cache with a reserve has longer lists)."""
         return pages
+
+    def _plan_decode(self):
+        """The split map, plan and workspace of tg_decode_attn over the retained tokens."""
+        Phi = np.ones_like(self.pages["Phi"]) if self.uniform_split else self.pages["Phi"]
+        self.S = tg_split_map(Phi, self.n_cta)
+        self.plan, self.workspace_bytes = tg_plan_decode(self.S, self.pages["order"], self.pages["ntok"],
+                                                         self.H_q, self.H_p, self.P, self.d)
+        self.plan_dev = torch.from_numpy(self.plan).to(self.device)
+        self.workspace = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.device)
 
     def _take_pages(self, allocator):
         """Budget reservation: each request's page lists, over all layers and groups, come from
@@ -637,7 +642,8 @@ class GrowingCache(RaggedCache):
     format.  compact_layer and compact_layer_chunked retain into it; a decode step is append_layer and
     decode_layer of each layer, then advance().  With pages="e2m1" retention goes through bf16 pages of
     one layer, which the next one uses again; dequantize_layer gives a layer's tokens as bf16 pages, for
-    SharedPrefix and the like.  The base class' own decode plan (`plan`) covers the retained tokens alone.
+    SharedPrefix and the like.  The base class' own decode plan (`plan`) covers the retained tokens alone; it is made when it is
+    asked for, with its workspace.
     Caches that share an allocator may share a pool (alloc_pool=False, then pool is set: n_pages of
     tg_page_bytes).  One stream at a time; to be kept until its calls have run."""
 
@@ -655,6 +661,15 @@ class GrowingCache(RaggedCache):
                                   k_unit=k_unit, v_unit=v_unit, n_cta=n_cta, device=device)
         self.status = self.lists.status  # one word for all calls
         self._layer_pages = None
+
+    def _plan_decode(self):
+        pass
+
+    def __getattr__(self, name):
+        if name not in ("S", "plan", "workspace_bytes", "plan_dev", "workspace"):
+            raise AttributeError(f"{type(self).__name__!r} object has no attribute {name!r}")
+        super()._plan_decode()
+        return self.__dict__[name]
 
     def algorithmic_bytes(self, layer=None) -> int:
         """As RaggedCache's, before any token is appended: 4-bit pages hold 9/16 of a byte a value."""
