@@ -589,7 +589,9 @@ class GrowingLists(_OnStreams):
         placed, counts, self.one_each = tables.split([order.size, ntok.size, self.batch + 1])
         self.order, self.ntok = placed.view(L, H).unbind(), counts.view(L, self.batch, H).unbind()
         self.scale = 1.0 / math.sqrt(d)
-        self._step = ["none"] * L  # of each layer: appended to never ("none"), in this step ("now"), in an earlier one ("before")
+        # of each layer: appended to never ("none"), since advance() ("now"), ahead of it ("before"), or into a graph, whose replays
+        # are not seen here ("graph")
+        self._step = ["none"] * L
         self._own(self.plan.plan_dev, self.workspace, self.status, self.added, tables)
 
     def append(self, layer, qkv, cos_sin, q, pool, pool_pages, pt_off, pt_ids, cu_q=None, origin=None, positions=None,
@@ -602,7 +604,8 @@ class GrowingLists(_OnStreams):
                        k_unit=self.k_unit, v_unit=self.v_unit, q_weight=q_weight, k_weight=k_weight, eps=eps, pairs=pairs,
                        positions=positions, axis_of=axis_of, origin=origin, K=K, V=V, start=start, dev_status=self.status,
                        stream=stream)
-        self._step[layer] = "now"
+        if self._step[layer] != "graph":
+            self._step[layer] = "graph" if torch.cuda.is_current_stream_capturing() else "now"
         self._used_on(stream)
 
     def attend(self, layer, q, pool, pool_pages, pt_off, pt_ids, out, lse=None, plus=1, scale=None, cta_time=None,
@@ -619,7 +622,7 @@ class GrowingLists(_OnStreams):
     def advance(self, n=1):
         """Count a step's tokens, after its last layer, on the current stream: n for each request, or int32 [batch]."""
         self.added.add_(n)
-        self._step = ["none" if s == "none" else "before" for s in self._step]
+        self._step = ["before" if s == "now" else s for s in self._step]
         self._used_on(None)
 
     def quantize(self, layer, src, src_pages, src_off, src_ids, dst, dst_pages, dst_off, dst_ids, stream=None):
@@ -716,15 +719,15 @@ class GrowingCache(RaggedCache):
                           stream=stream, **how)
 
     def decode_layer(self, layer, q, out, lse=None, cta_time=None, stream=None, pool=None, plus=None, added=None):
-        """GrowingLists.attend over this cache's pages.  plus by default: 1 if the layer was appended to since advance(),
-        0 if it never was (a cache that only retained), or with added, which then counts this step's tokens too.  Between
-        steps it has to be given: a graph that appends may have been replayed meanwhile, or not."""
+        """GrowingLists.attend over this cache's pages.  plus by default: 1 if the layer was appended to since advance(), or
+        ever by a captured call (whose replays count as this step's); 0 if it never was (a cache that only retained), or with
+        added, which then counts this step's tokens too.  Else, between steps, it has to be given."""
         if plus is None:
             step = self.lists._step[layer]
             if step == "before" and added is None:
                 raise ValueError(f"layer {layer} was not appended to since advance(): plus=0 attends to what advance() has "
                                  "counted, plus=1 to a token of this step too")
-            plus = 1 if step == "now" and added is None else 0
+            plus = 1 if step in ("now", "graph") and added is None else 0
         self.lists.attend(layer, q, self.pool if pool is None else pool, self.n_pages, self.list_offsets(layer),
                           self.pt_ids_dev, out, lse=lse, plus=plus, cta_time=cta_time, stream=stream, added=added)
 

@@ -49,7 +49,7 @@ def test_the_default_follows_the_step(lib, cuda, pages):
     assert torch.equal(new, _decode(cache, q, plus=1)) and not torch.equal(new, old)
     assert torch.equal(_decode(cache, q, 1), _decode(cache, q, 1, plus=0))  # this layer brought nothing yet
     cache.advance()
-    # between steps there is no telling whether a replayed graph has appended: the call says
+    # between steps nothing tells which tokens are meant: the call says
     with pytest.raises(ValueError):
         _decode(cache, q)
     assert torch.equal(_decode(cache, q, plus=0), new)
@@ -84,6 +84,24 @@ def test_a_replayed_step_decodes_as_it_was_captured(lib, cuda, pages):
         step(eager)
         torch.cuda.synchronize()
         assert torch.equal(got[0], out) and torch.equal(got[1], lse)
+
+
+@pytest.mark.parametrize("pages", ["bf16", "e2m1"])
+def test_a_replayed_append_counts_for_the_calls_behind_it(lib, cuda, pages):
+    """Only the append is in the graph; decode_layer and advance() are called between its replays."""
+    w, cache, q, qkv = _cache(cuda, pages, L=1)
+    w2, eager, _, _ = _cache(cuda, pages, L=1)
+    own, side = torch.empty_like(q), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        cache.append_layer(0, qkv[:3], None, own)
+    for _ in range(3):
+        graph.replay()
+        eager.append_layer(0, qkv[:3], None, own)
+        assert torch.equal(_decode(cache, q), _decode(eager, q))
+        cache.advance(), eager.advance()
+    assert lib.tg_check_status(cache.status) == 0
 
 
 @pytest.mark.parametrize("pages", ["bf16", "e2m1"])
