@@ -10,8 +10,10 @@
 // exchanges nothing, or 8 consecutive ones (pairs (2i, 2i + 1), values behind rot, V).  Where the heads' rows lie is
 // looked up once, for 32 places of the groups at a time, each by a lane; K and V lie side by side.  Queries, keys and
 // values have a loop each; a batch of queries (a unit of 4-bit keys) is on its way while the one before it is worked
-// on.  15000 tokens of 16 + 8 + 8 heads of 128 into bf16 pages, 372 MB: 68 us, 5.5 TB/s (71.5 with one loop for all
+// on.  15000 tokens of 32 + 8 + 8 heads of 128 into bf16 pages, 372 MB: 68 us, 5.5 TB/s (71.5 with one loop for all
 // three; 70.1 with 24 blocks to an SM and 72.9 with 20, for 28; 72.6 with batches of 2 loads for 4; one warp a token).
+// The 72 registers of 28 blocks do not hold two batches of queries: 144 to 188 bytes a thread are spilled (64 to 136 read
+// back), 4% of that call's instructions.
 //
 // 4-bit pages.  A head's rotated values go through shared memory, so that a lane has 8 consecutive ones and a pair
 // of lanes a block of 16.  float32 leaves a value z = f (u c x_u - v s x_v) off by at most 15 2^-24 t,
@@ -19,8 +21,8 @@
 // rest; z / s adds three, and two are to spare.  That decides a code or a scale wrongly where z / s comes so close
 // to the border of two.  So both are taken of the value moved down and up by as much, with the block's
 // largest t; where they differ (a row in some hundred) the row is computed again in float64, from the projections in
-// registers, and what was open is taken from that.  V is exact and needs none of this.  (2600 tokens of 16 + 16 heads
-// of 256: 30.8 us.  A bound by the row's largest value with float64 divisions costs 23 more; the keys'
+// registers, and what was open is taken from that.  V is exact and needs none of this.  (2500 tokens of 16 + 8 + 8 heads
+// of 256: 30.5 us.  A bound by the row's largest value with float64 divisions costs 23 more; the keys'
 // loop unrolled 16 more, waiting for instructions.)
 #include "packed.cuh"
 #include "page4.cuh"

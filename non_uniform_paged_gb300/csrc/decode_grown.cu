@@ -1,6 +1,7 @@
 // Decode attention over runs that grow, of bf16 pages and of 4-bit pages (tg_decode_grown).
 //
-// bf16 pages: the body of tg_decode_attn (decode_body.cuh) over the pieces that grown_item gives.
+// bf16 pages: the body of tg_decode_attn (decode_body.cuh) over the pieces that grown_item gives.  1.35 M rows of 128 (691 MB, 101.7
+// us at the copy rate) 109 us; 1.32 M rows of 256 under 2 query heads (1355 MB, 199.6 us) 204, tg_decode_attn over the same rows 187.
 //
 // 4-bit pages.  Mathematics: out = sum_t softmax_t(scale q . k_t) v_t with k, v = code * block scale * unit.
 // A token is 9/16 of a byte a value, so that the same bytes hold 3.6 times the tokens of bf16 pages and
@@ -18,9 +19,10 @@
 //    side by side in their bytes before the conversion, so that the pair of their scales multiplies them.
 //  * Weights are f16, 2^8 times the softmax's against a maximum that moves only when a score passes it by 7
 //    (kWeightLog2 below): at most 2^15, and what f16 loses of a weight is below 2^-24 / 2^8 of the maximum's.
-// Measured: 2.7 M rows of 128 under 4 query heads a KV head (389 MB, 57.3 us at the copy rate) 74.5 us, 1.9 M rows of
-// 256 under 2 (545 MB, 80.3 us) 100.  A step's HMMAs and scale products share a port, 670 of the 830 clocks that a scheduler
-// gives it at d = 128; conversions and byte moves take 570 of another's.  Steps of 16 tokens with a maximum in each took
+// Measured: 2.7 M rows of 128 under 4 query heads a KV head (389 MB, 57.3 us at the copy rate) 72.7 us, 1.9 M rows of
+// 256 under 2 (545 MB, 80.2 us) 98.  No unit is at its limit: of the active clocks ALU (conversions, byte moves) 52%, FMA (with the
+// f16 products) 34, HMMA 26, issue 58; DRAM 64% of all (48, 32, 27, 51 and 68 at d = 256).  Three (two) streaming warps a
+// scheduler do not cover the chains of dependent instructions of a step.  Steps of 16 tokens with a maximum in each took
 // 106.9 and 165; warps that only load, 87 us and more where this took 81; 16 streaming warps spill; three stages, no gain.
 #include "decode_body.cuh"
 #include "page4.cuh"
