@@ -16,6 +16,7 @@ in libtg's kernels.
 """
 from __future__ import annotations
 
+import contextlib
 import math
 
 import numpy as np
@@ -45,21 +46,22 @@ class RaggedCache:
         self.request_pages = None
         if allocator is not None:
             self._take_pages(allocator)
-        self.n_cta = int(n_cta) if n_cta else tg_query_ncta(d, self.g)
-        self.uniform_split = uniform_split
-        self._plan_decode()
-        dev = self.device
-        self.N_dev = torch.from_numpy(self.N).to(dev)
-        self.order_dev = torch.from_numpy(self.pages["order"]).to(dev)
-        self.ntok_dev = torch.from_numpy(self.pages["ntok"]).to(dev)
-        self.pt_off_dev = torch.from_numpy(self.pages["pt_off"]).to(dev)
-        self.pt_ids_dev = torch.from_numpy(self.pages["pt_ids"]).to(dev)
-        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
-        self._compact_ws = {}  # tg_compact_topk's workspace, by Nmax
-        self.pool = None
-        if alloc_pool:
-            self.pool = torch.empty(max(self.n_pages, 1) * H_p * 2 * P * d, dtype=torch.bfloat16, device=dev)
-        self.scale = 1.0 / math.sqrt(d)
+        with self._pages_go_back(allocator):
+            self.n_cta = int(n_cta) if n_cta else tg_query_ncta(d, self.g)
+            self.uniform_split = uniform_split
+            self._plan_decode()
+            dev = self.device
+            self.N_dev = torch.from_numpy(self.N).to(dev)
+            self.order_dev = torch.from_numpy(self.pages["order"]).to(dev)
+            self.ntok_dev = torch.from_numpy(self.pages["ntok"]).to(dev)
+            self.pt_off_dev = torch.from_numpy(self.pages["pt_off"]).to(dev)
+            self.pt_ids_dev = torch.from_numpy(self.pages["pt_ids"]).to(dev)
+            self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+            self._compact_ws = {}  # tg_compact_topk's workspace, by Nmax
+            self.pool = None
+            if alloc_pool:
+                self.pool = torch.empty(max(self.n_pages, 1) * H_p * 2 * P * d, dtype=torch.bfloat16, device=dev)
+            self.scale = 1.0 / math.sqrt(d)
 
     def _build_pages(self, pages):
         """The page tables to use of tg_build_pages' (a cache with a reserve has longer lists)."""
@@ -73,6 +75,16 @@ class RaggedCache:
                                                          self.H_q, self.H_p, self.P, self.d)
         self.plan_dev = torch.from_numpy(self.plan).to(self.device)
         self.workspace = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.device)
+
+    @contextlib.contextmanager
+    def _pages_go_back(self, allocator):
+        """What follows the pages' reservation: if it is refused, they are the allocator's again."""
+        try:
+            yield
+        except BaseException:
+            for taken in self.request_pages or ():
+                allocator.release(taken)
+            raise
 
     def _take_pages(self, allocator):
         """Budget reservation: each request's page lists, over all layers and groups, come from
@@ -655,13 +667,14 @@ class GrowingCache(RaggedCache):
         self.reserve, self.four = int(reserve), _page_format(pages, reserve) == PAGES_E2M1  # refused before pages are taken
         super().__init__(L, batch, H, H_q, d, P, H_p, alpha, Bhat, N, cluster=cluster, n_cta=n_cta, device=device,
                          alloc_pool=False, allocator=allocator)
-        if alloc_pool:
-            page = tg_page_bytes(PAGE_FORMATS[pages], H_p, P, d)
-            kind = torch.uint8 if self.four else torch.bfloat16
-            self.pool = torch.empty(max(self.n_pages, 1) * page // kind.itemsize, dtype=kind, device=self.device)
-        # after the pool: the uploads wait for what the current stream still has to do with its memory
-        self.lists = GrowingLists(H_q, H_p, P, d, self.pages["order"], self.pages["ntok"], reserve, pages=pages,
-                                  k_unit=k_unit, v_unit=v_unit, n_cta=n_cta, device=device)
+        with self._pages_go_back(allocator):
+            if alloc_pool:
+                page = tg_page_bytes(PAGE_FORMATS[pages], H_p, P, d)
+                kind = torch.uint8 if self.four else torch.bfloat16
+                self.pool = torch.empty(max(self.n_pages, 1) * page // kind.itemsize, dtype=kind, device=self.device)
+            # after the pool: the uploads wait for what the current stream still has to do with its memory
+            self.lists = GrowingLists(H_q, H_p, P, d, self.pages["order"], self.pages["ntok"], reserve, pages=pages,
+                                      k_unit=k_unit, v_unit=v_unit, n_cta=n_cta, device=device)
         self.status = self.lists.status  # one word for all calls
         self._layer_pages = None
 
